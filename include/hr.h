@@ -543,7 +543,12 @@ typedef enum {
     HR_DECLINE_TOO_LARGE = 5     /* payload above the cap */
 } hr_route;
 
-typedef enum { HR_DTYPE_F16 = 0, HR_DTYPE_BF16 = 1, HR_DTYPE_OTHER = 2 } hr_dtype;
+typedef enum {
+    HR_DTYPE_F16 = 0,
+    HR_DTYPE_BF16 = 1,
+    HR_DTYPE_OTHER = 2,
+    HR_DTYPE_F32 = 3   /* router logits only; hr_admit declines it */
+} hr_dtype;
 
 typedef struct {
     int enabled;       /* 0 declines everything (HR_DECLINE_DISABLED)          */
@@ -565,6 +570,116 @@ HR_API const char *hr_route_str(hr_route r);
 /* Decode-sized bound in values: max_batch x tokens_per_request (0 counts as
  * 1) x hidden -- e.g. 64 x 1 x 6144 = 393216, the SGLang page's default. */
 HR_API size_t hr_decode_numel(size_t max_batch, size_t tokens_per_request, size_t hidden);
+
+/*
+ * Around the combine.
+ *
+ * A layer never uses an all-reduce's sum bare: it is added to the residual
+ * stream, normed, and (for 8-bit products) quantised.  And where a layer's
+ * experts are spread over the ranks, what a rank contributes to the sum is
+ * itself a combination: its experts' outputs, weighted and added per token.
+ * The functions below compute both sides on one GPU, in the same manner as
+ * the fold: one call enqueues its kernels on `stream` and never synchronises,
+ * allocates or copies, so it may be captured into a graph.
+ *
+ * Rows.  Buffers of rows take a stride between rows; 0 stands for contiguous
+ * rows, any other value is at least the row's length.  Pointers need only
+ * their element type's alignment.  Outputs may not overlap inputs or one
+ * another, except where a function allows an output to be exactly an input
+ * (same address, same stride).  Interleaved columns of one buffer (equal
+ * strides) do not overlap.
+ */
+
+/* Largest row of hr_reduce_rmsnorm and its gradient, in values. */
+#define HR_RMSNORM_MAX_HIDDEN 32768u
+
+typedef struct {
+    const void *inputs[HR_MAX_G]; /* G contributions, rows x hidden values each   */
+    const void *residual;     /* the fold's last operand; NULL = none             */
+    const void *weight;       /* hidden values; NULL = ones                       */
+    void *residual_out;       /* h, the new residual stream; NULL = not wanted    */
+    void *out;                /* y in 16 bits; NULL = not wanted                  */
+    void *codes;              /* y in e4m3 (OCP, largest 448); NULL = not wanted  */
+    float *scales;            /* one per row or per group; with codes             */
+    float *rstd;              /* one per row, kept for the gradient; NULL = none  */
+    size_t rows, hidden;      /* hidden 1..HR_RMSNORM_MAX_HIDDEN                  */
+    size_t input_stride;      /* values between rows; 0 = hidden                  */
+    size_t residual_stride, residual_out_stride, out_stride;
+    size_t codes_stride;      /* bytes between rows; 0 = hidden                   */
+    size_t scales_stride;     /* scales between rows; 0 = their number            */
+    int G;                    /* 1..HR_MAX_G                                      */
+    int weight_f32;           /* 0: weight has the values' type; else binary32    */
+    int group;                /* values that share a scale: 0 = the row, or 32,
+                                 64 or 128 (the last group may be shorter)        */
+    float eps;                /* at least 0                                       */
+} hr_rmsnorm_args;
+
+/*
+ * hr_reduce_rmsnorm_f16 / _bf16 -- fold, residual, norm and quantisation in
+ * one kernel:
+ *
+ *     h    = left fold of inputs[0] .. inputs[G-1], residual
+ *     rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ *     y    = h * rstd * weight
+ *
+ * h is hr_reduce's fold of G + 1 contributions, bit for bit (one rounding per
+ * add); with G = 1 the input is an activation that is already summed, such as
+ * an exchange's output.  The norm is taken of the rounded h in binary32 and y
+ * is rounded once, to `out`.  The 8-bit output comes from the unrounded y:
+ *
+ *     scale = max(max |y| over the group / 448, 2^-126)
+ *     code  = e4m3(y / scale), to nearest even
+ *
+ * so a group of zeros has codes 0 and the smallest scale.  A row that holds a
+ * NaN or an infinity gives what the formulas give: NaN where h is one, and a
+ * NaN scale for the groups with a NaN.  (Squares are summed in binary32: a row
+ * whose mean square lies above its range gives rstd 0.)
+ *
+ * residual_out and out may each be exactly one of the inputs or the residual.
+ * Errors: HR_ERR_INVALID_ARG (G, hidden 0, group, eps, a null input, codes
+ * without scales or scales without codes, nothing to write, a stride below the
+ * row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (hidden above
+ * HR_RMSNORM_MAX_HIDDEN, 2^31 rows or more), HR_ERR_HIP.
+ */
+HR_API hr_status hr_reduce_rmsnorm_f16(const hr_rmsnorm_args *args, hr_stream_t stream);
+HR_API hr_status hr_reduce_rmsnorm_bf16(const hr_rmsnorm_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *dy;           /* gradient of y                                    */
+    const void *h;            /* the forward call's residual_out                  */
+    const float *rstd;        /* the forward call's                               */
+    const void *weight;       /* NULL = ones                                      */
+    const void *dresidual;    /* gradient that h has from elsewhere; NULL = none  */
+    void *dx;                 /* gradient of h                                    */
+    float *dweight;           /* hidden sums; NULL = not wanted                   */
+    void *workspace;          /* hr_rmsnorm_grad_workspace bytes, 4-byte aligned,
+                                 needed with dweight                              */
+    size_t workspace_bytes;
+    size_t rows, hidden;
+    size_t dy_stride, h_stride, dresidual_stride, dx_stride;   /* values; 0 = hidden */
+    int weight_f32;
+} hr_rmsnorm_grad_args;
+
+/*
+ * hr_rmsnorm_grad_f16 / _bf16 -- the gradient of hr_reduce_rmsnorm's y:
+ *
+ *     u  = h * rstd,  g = dy * weight
+ *     dx = rstd * (g - u * mean over the row of (g u)) + dresidual
+ *     dweight = sum over the rows of dy * u
+ *
+ * dx is the gradient of h, and so of every contribution and of the residual
+ * (a sum hands its gradient to each operand; the roundings of the fold are
+ * taken as exact).  Sums are binary32 in a fixed order: the same inputs give
+ * the same bits.  dx may be exactly dy, h or dresidual.  rows 0 writes zeros
+ * to dweight.  The workspace holds per-workgroup sums of dweight; its contents
+ * mean nothing between calls, and calls that may run at once need their own.
+ * Errors: as hr_reduce_rmsnorm; HR_ERR_INVALID_ARG for a workspace that is
+ * missing or too small.
+ */
+HR_API hr_status hr_rmsnorm_grad_f16(const hr_rmsnorm_grad_args *args, hr_stream_t stream);
+HR_API hr_status hr_rmsnorm_grad_bf16(const hr_rmsnorm_grad_args *args, hr_stream_t stream);
+/* Bytes of workspace that a gradient call with dweight needs (0: none). */
+HR_API size_t hr_rmsnorm_grad_workspace(size_t rows, size_t hidden);
 
 /* Static, human-readable name of a status code. */
 HR_API const char *hr_status_str(hr_status s);

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhr.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fold.hip", "exchange.hip", "admit.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fold.hip", "exchange.hip", "admit.hip", "norm.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -31,6 +31,7 @@ FLAGS = [
     # kernels receive their first five arguments in SGPRs (the per-rank
     # exchange kernels put what their first loads need there)
     "-mllvm", "-amdgpu-kernarg-preload-count=5",
+    "-parallel-jobs=8",
     "-I", INCLUDE,
     "-Wl,-rpath,/opt/rocm/lib",
 ]

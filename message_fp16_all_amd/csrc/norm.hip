@@ -1,0 +1,647 @@
+// norm.hip -- hr_reduce_rmsnorm_f16 / _bf16: the fold of G contributions with
+// the residual as its last operand, the root-mean-square norm of the sum and
+// its output in 16 bits, in e4m3 with scales, or both; and the norm's gradient
+// hr_rmsnorm_grad_f16 / _bf16.
+//
+//   h = fold(x_0, .., x_{G-1}, residual)        16 bits, one rounding per add
+//   rstd = 1 / sqrt(mean(h^2) + eps)            binary32
+//   y = h * rstd * weight                       binary32, rounded once to out
+//   scale = max(max|y| / 448, 2^-126)           over the row or a group of it
+//   code = e4m3(y / scale)                      from the unrounded y
+//
+// h is what hr_reduce_f16 gives for G + 1 contributions, bit for bit, and the
+// norm is taken of these 16-bit values, not of an unrounded sum: a residual
+// stream kept by this call, by hr_reduce and by an exchange is the same.
+#include "rows.h"
+
+namespace hr {
+
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxWaves = kNormMaxThreads / kWave;
+constexpr int kOperands = HR_MAX_G + 1;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinScale = 0x1p-126f;
+
+struct NormArgs {
+    const uint16_t *in[kOperands];   // contributions, then the residual if there is one
+    const void *weight;
+    uint16_t *h;
+    uint16_t *out;
+    uint8_t *codes;
+    float *scales;
+    float *rstd;
+    size_t rows;
+    size_t in_stride, last_stride;   // of in[0 .. n-2] and of in[n-1]
+    size_t h_stride, out_stride, codes_stride, scales_stride;
+    int n;                           // operands of the fold
+    int hidden;
+    int weight_f32;
+    int group_lanes;                 // lanes (8 values each) that share a scale; 0 = the row
+    float eps;
+};
+
+// The 8 weights of unit i; values past the end are 0, and 1 without a weight.
+template <class E, bool TAIL>
+__device__ __forceinline__ void load_weight(const void *w, int f32, int i, int n, float (&f)[8]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 1.0f;
+    } else if (f32) {
+        const float *p = reinterpret_cast<const float *>(static_cast<const char *>(w) + 32u * i);
+        if (!TAIL || 8 * i + 8 <= n) {
+            const f32x4 a = *reinterpret_cast<const f32x4_row *>(p), b = *reinterpret_cast<const f32x4_row *>(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = a[e];
+                f[e + 4] = b[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = 8 * i + e < n ? p[e] : 0.0f;
+        }
+    } else {
+        Wide<E>::widen(load_unit<TAIL>(static_cast<const uint16_t *>(w), i, n), f);
+    }
+}
+
+// A sum over the L lanes of a row, or (L = 0) over the workgroup's waves.
+// `part` holds one value per wave; a call's barrier separates its writes from
+// its reads, and callers alternate between two of them.
+template <int L>
+__device__ __forceinline__ float sum_row(float v, float *part) {
+    if constexpr (L > 0) {
+        return sum_lanes<L>(v);
+    } else {
+        v = sum_lanes<kWave>(v);
+        const int waves = (blockDim.x + kWave - 1) / kWave;
+        if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+        __syncthreads();
+        const int lane = threadIdx.x % kNormMaxWaves;
+        return sum_lanes<kNormMaxWaves>(lane < waves ? part[lane] : 0.0f);
+    }
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t max_row(uint32_t v, uint32_t *part) {
+    if constexpr (L > 0) {
+        return max_lanes<L>(v);
+    } else {
+        v = max_lanes<kWave>(v);
+        const int waves = (blockDim.x + kWave - 1) / kWave;
+        if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+        __syncthreads();
+        const int lane = threadIdx.x % kNormMaxWaves;
+        return max_lanes<kNormMaxWaves>(lane < waves ? part[lane] : 0u);
+    }
+}
+
+__device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
+    if (lanes == 16) return max_lanes<16>(v);
+    if (lanes == 8) return max_lanes<8>(v);
+    return max_lanes<4>(v);
+}
+
+// One row per workgroup (L = 0), or one row per L lanes of a workgroup.
+// Thread t of a row holds units t, t + threads, .. (U of them) from the fold's
+// loads to the stores, so every input byte is read once.
+template <class E, int U, int L, bool TAIL>
+__global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
+    __shared__ float sums[kNormMaxWaves];
+    __shared__ uint32_t maxs[kNormMaxWaves];
+    const int threads = L > 0 ? L : static_cast<int>(blockDim.x);
+    const int t = L > 0 ? static_cast<int>(threadIdx.x) % L : static_cast<int>(threadIdx.x);
+    const size_t row = L > 0 ? static_cast<size_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / (L > 0 ? L : 1)
+                             : static_cast<size_t>(blockIdx.x);
+    const int hidden = a.hidden;
+    const int units = (hidden + 7) / 8;
+    const bool there = L == 0 || row < a.rows;
+    // operands in flight at once: all of them for one unit per lane, and the
+    // eight contributions and residual of a full group for two
+    constexpr int B = U == 1 ? kOperands : U == 2 ? 9 : 4;
+
+    u32x4 h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) h[u] = u32x4{0, 0, 0, 0};
+    for (int g0 = 0; g0 < a.n; g0 += B) {
+        u32x4 x[B][U];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int g = g0 + b;
+            if (g < a.n) {
+                const uint16_t *p = a.in[g] + row * (g == a.n - 1 ? a.last_stride : a.in_stride);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = t + u * threads;
+                    x[b][u] = u32x4{0, 0, 0, 0};
+                    if (there && i < units) x[b][u] = load_unit<TAIL>(p, i, hidden);
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (g0 + b < a.n) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) h[u] = (g0 + b == 0) ? x[b][u] : E::add8(h[u], x[b][u]);
+            }
+        }
+    }
+
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[8];
+        Wide<E>::widen(h[u], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+    }
+    float w[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = t + u * threads;
+        if (i < units) load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w[u]);
+    }
+    sum = sum_row<L>(sum, sums);
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(hidden) + a.eps);
+    if (there && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+
+    float y[U][8];
+    uint32_t top[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = t + u * threads;
+        top[u] = 0;
+        if (i >= units) continue;
+        Wide<E>::widen(h[u], y[u]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            y[u][e] = y[u][e] * rstd * w[u][e];
+            // magnitudes compared as integers, so that a NaN is the largest
+            if (!TAIL || 8 * i + e < hidden) {
+                const uint32_t m = __builtin_bit_cast(uint32_t, y[u][e]) & 0x7FFFFFFFu;
+                top[u] = top[u] > m ? top[u] : m;
+            }
+        }
+        if (!there) continue;
+        if (a.h != nullptr) store_unit<TAIL>(a.h + row * a.h_stride, i, hidden, h[u]);
+        if (a.out != nullptr) store_unit<TAIL>(a.out + row * a.out_stride, i, hidden, Wide<E>::narrow(y[u]));
+    }
+    if (a.codes == nullptr) return;
+
+    if (a.group_lanes == 0) {
+        uint32_t m = top[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) m = m > top[u] ? m : top[u];
+        m = max_row<L>(m, maxs);
+#pragma unroll
+        for (int u = 0; u < U; ++u) top[u] = m;
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) top[u] = max_of_group(top[u], a.group_lanes);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = t + u * threads;
+        if (!there || i >= units) continue;
+        const float m = __builtin_bit_cast(float, top[u]);
+        const float scale = m < kE4m3Max * kMinScale ? kMinScale : m / kE4m3Max;   // NaN stays NaN
+        // one reciprocal for the group's values: at most 1.5 units in the last
+        // of 24 bits from the quotient, against 4 bits that the code keeps
+        const float inv = 1.0f / scale;
+        if (a.group_lanes == 0 ? i == 0 : i % a.group_lanes == 0)
+            a.scales[row * a.scales_stride + (a.group_lanes == 0 ? 0 : i / a.group_lanes)] = scale;
+        u32x2 c;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[u][4 * q] * inv, y[u][4 * q + 1] * inv, 0, false);
+            v = __builtin_amdgcn_cvt_pk_fp8_f32(y[u][4 * q + 2] * inv, y[u][4 * q + 3] * inv, v, true);
+            c[q] = static_cast<uint32_t>(v);
+        }
+        uint8_t *p = a.codes + row * a.codes_stride + 8 * static_cast<size_t>(i);
+        if (!TAIL || 8 * i + 8 <= hidden) {
+            *reinterpret_cast<u32x2_row *>(p) = c;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (8 * i + e < hidden) p[e] = static_cast<uint8_t>(c[e / 4] >> (8 * (e & 3)));
+        }
+    }
+}
+
+struct NormGradArgs {
+    const uint16_t *dy, *h, *dres;
+    const float *rstd;
+    const void *weight;
+    uint16_t *dx;
+    float *part;                     // one row of `hidden` sums per workgroup; null: not wanted
+    size_t rows;
+    size_t dy_stride, h_stride, dres_stride, dx_stride;
+    int hidden;
+    int weight_f32;
+};
+
+// dx = rstd * (g - u * mean(g u)) + dres with g = dy * weight, u = h * rstd,
+// and this workgroup's sum over its rows of dy * u.  Rows are dealt out to the
+// workgroups (L = 0) or to groups of L lanes in turn; a thread keeps its
+// columns' sums in registers from its first row to its last.
+template <class E, int U, int L, bool TAIL>
+__global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a) {
+    __shared__ float sums[2][kNormMaxWaves];
+    const int threads = L > 0 ? L : static_cast<int>(blockDim.x);
+    const int t = L > 0 ? static_cast<int>(threadIdx.x) % L : static_cast<int>(threadIdx.x);
+    const int per = L > 0 ? static_cast<int>(blockDim.x) / (L > 0 ? L : 1) : 1;
+    const size_t step = static_cast<size_t>(gridDim.x) * per;
+    const int hidden = a.hidden;
+    const int units = (hidden + 7) / 8;
+
+    float acc[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[u][e] = 0.0f;
+
+    // Up to two units per thread the row stays in registers between its two
+    // uses, and the weights from row to row; four would spill.
+    constexpr bool kKeep = U <= 2;
+    float kept[kKeep ? U : 1][8];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kept[u][e] = 0.0f;
+            if (t + u * threads < units)
+                load_weight<E, TAIL>(a.weight, a.weight_f32, t + u * threads, hidden, kept[u]);
+        }
+    }
+
+    int turn = 0;
+    for (size_t row0 = static_cast<size_t>(blockIdx.x) * per; row0 < a.rows; row0 += step, turn ^= 1) {
+        const size_t row = row0 + (L > 0 ? threadIdx.x / (L > 0 ? L : 1) : 0);
+        const bool there = L == 0 || row < a.rows;
+        const float rstd = there ? a.rstd[row] : 0.0f;
+        u32x4 d[U], h[U], r[U];
+        auto load = [&](int u) {
+            const int i = t + u * threads;
+            d[u] = h[u] = r[u] = u32x4{0, 0, 0, 0};
+            if (there && i < units) {
+                d[u] = load_unit<TAIL>(a.dy + row * a.dy_stride, i, hidden);
+                h[u] = load_unit<TAIL>(a.h + row * a.h_stride, i, hidden);
+                if (a.dres != nullptr) r[u] = load_unit<TAIL>(a.dres + row * a.dres_stride, i, hidden);
+            }
+        };
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(u);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = t + u * threads;
+            float dy[8], unit[8], w[8];
+            if constexpr (!kKeep) load(u);
+            Wide<E>::widen(d[u], dy);
+            Wide<E>::widen(h[u], unit);
+            if constexpr (kKeep) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = kept[u][e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+                if (i < units) load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                unit[e] *= rstd;
+                acc[u][e] = fmaf(dy[e], unit[e], acc[u][e]);
+                sum = fmaf(dy[e] * w[e], unit[e], sum);
+            }
+            if constexpr (!kKeep) {
+                // one unit at a time: the empty statement stops the compiler
+                // from loading all of them first, which spills
+#pragma unroll
+                for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(acc[u][e]));
+                asm volatile("" : "+v"(sum)::"memory");
+            }
+        }
+        const float mean = sum_row<L>(sum, sums[turn]) / static_cast<float>(hidden);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = t + u * threads;
+            if (!there || i >= units) continue;
+            float dy[8], unit[8], w[8], f[8];
+            if constexpr (!kKeep) {
+                load(u);   // again, from the caches
+            }
+            Wide<E>::widen(d[u], dy);
+            Wide<E>::widen(h[u], unit);
+            Wide<E>::widen(r[u], f);
+            if constexpr (kKeep) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = kept[u][e];
+            } else {
+                load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += rstd * (dy[e] * w[e] - unit[e] * rstd * mean);
+            store_unit<TAIL>(a.dx + row * a.dx_stride, i, hidden, Wide<E>::narrow(f));
+            if constexpr (!kKeep) asm volatile("" ::: "memory");
+        }
+    }
+    if (a.part == nullptr) return;
+    float *part = a.part + static_cast<size_t>(blockIdx.x) * hidden;
+    if constexpr (L > 0) {
+        // the row groups of the workgroup, added in order
+        __shared__ float cols[4 * kWave * 8];       // 256 threads at most (launch)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cols[threadIdx.x * 8 + e] = acc[0][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < hidden; c += blockDim.x) {
+            float s = 0.0f;
+            for (int k = 0; k < per; ++k) s += cols[k * (L * 8) + c];
+            part[c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = t + u * threads;
+            if (i >= units) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!TAIL || 8 * i + e < hidden) part[8 * i + e] = acc[u][e];
+        }
+    }
+}
+
+// out[c] = sum over p of part[p][c], in a fixed order: 16 waves of a workgroup
+// take 64 columns, each wave every 16th row, and the waves' sums are added in
+// order.
+constexpr int kColumnWaves = 16;
+
+__global__ __launch_bounds__(kColumnWaves *kWave) void sum_columns(const float *part, size_t parts, int hidden,
+                                                                   float *out) {
+    __shared__ float sums[kColumnWaves][kWave];
+    const int c = static_cast<int>(blockIdx.x) * kWave + threadIdx.x % kWave;
+    const int wave = threadIdx.x / kWave;
+    float s = 0.0f;
+    if (c < hidden) {
+#pragma unroll 8
+        for (size_t p = wave; p < parts; p += kColumnWaves) s += part[p * hidden + c];
+    }
+    sums[wave][threadIdx.x % kWave] = s;
+    __syncthreads();
+    if (wave == 0 && c < hidden) {
+        s = sums[0][threadIdx.x];
+        for (int k = 1; k < kColumnWaves; ++k) s += sums[k][threadIdx.x];
+        out[c] = s;
+    }
+}
+
+namespace {
+
+constexpr int kRowGroupThreads = 256;
+
+// How a row of `hidden` values is laid over threads.
+struct RowShape {
+    int lanes;     // lanes per row; 0 = a workgroup per row
+    int units;     // units of 8 values per thread
+    int threads;   // of a workgroup
+};
+
+RowShape row_shape(int hidden) {
+    const int units = (hidden + 7) / 8;
+    if (units <= 16) return {16, 1, kRowGroupThreads};
+    if (units <= 32) return {32, 1, kRowGroupThreads};
+    if (units <= 64) return {64, 1, kRowGroupThreads};
+    const int per = units <= 512 ? 1 : units <= 2048 ? 2 : 4;
+    const int threads = ((units + per - 1) / per + kWave - 1) / kWave * kWave;
+    return {0, per, threads};
+}
+
+template <template <class, int, int, bool> class K, class E, class... A>
+hipError_t launch_rows(const RowShape &s, bool tail, unsigned grid, hipStream_t stream, const A &...args) {
+#define HR_ROWS(U, L)                                                                                      \
+    if (tail)                                                                                              \
+        hipLaunchKernelGGL((K<E, U, L, true>::kernel), dim3(grid), dim3(s.threads), 0, stream, args...);   \
+    else                                                                                                   \
+        hipLaunchKernelGGL((K<E, U, L, false>::kernel), dim3(grid), dim3(s.threads), 0, stream, args...);
+    if (s.lanes == 16) {
+        HR_ROWS(1, 16)
+    } else if (s.lanes == 32) {
+        HR_ROWS(1, 32)
+    } else if (s.lanes == 64) {
+        HR_ROWS(1, 64)
+    } else if (s.units == 1) {
+        HR_ROWS(1, 0)
+    } else if (s.units == 2) {
+        HR_ROWS(2, 0)
+    } else {
+        HR_ROWS(4, 0)
+    }
+#undef HR_ROWS
+    return hipGetLastError();
+}
+
+template <class E, int U, int L, bool TAIL>
+struct NormKernel {
+    static constexpr auto kernel = norm_rows<E, U, L, TAIL>;
+};
+
+template <class E, int U, int L, bool TAIL>
+struct NormGradKernel {
+    static constexpr auto kernel = norm_grad_rows<E, U, L, TAIL>;
+};
+
+constexpr size_t kMaxRows = 0x7FFFFFFF;
+
+// Workgroups of the gradient, hence partial sums: two per compute unit at most.
+constexpr int kGradGroupsPerCu = 2;
+
+size_t grad_groups(size_t rows, int hidden, int cus) {
+    const RowShape s = row_shape(hidden);
+    const size_t per = s.lanes > 0 ? s.threads / s.lanes : 1;
+    const size_t groups = (rows + per - 1) / per;
+    const size_t cap = static_cast<size_t>(cus) * kGradGroupsPerCu;
+    return groups < cap ? groups : cap;
+}
+
+// The largest number of compute units a device of this kind has; the workspace
+// is sized without asking a device.
+constexpr int kMaxCus = 256;
+
+bool any_overlap(const Region *outs, int no, const Region *ins, int ni, unsigned in_place) {
+    for (int o = 0; o < no; ++o) {
+        for (int i = 0; i < ni; ++i)
+            if (regions_overlap(outs[o], ins[i]) && !((in_place >> o & 1) && regions_same(outs[o], ins[i]))) return true;
+        for (int p = 0; p < o; ++p)
+            if (regions_overlap(outs[o], outs[p])) return true;
+    }
+    return false;
+}
+
+template <class E>
+hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
+    if (q == nullptr || q->G < 1 || q->G > HR_MAX_G || q->hidden == 0 || !(q->eps >= 0.0f)) return HR_ERR_INVALID_ARG;
+    if (q->group != 0 && q->group != 32 && q->group != 64 && q->group != 128) return HR_ERR_INVALID_ARG;
+    if (q->hidden > HR_RMSNORM_MAX_HIDDEN || q->rows > kMaxRows) return HR_ERR_TOO_LARGE;
+    if (q->rows == 0) return HR_OK;
+    if (q->out == nullptr && q->residual_out == nullptr && q->codes == nullptr && q->rstd == nullptr)
+        return HR_ERR_INVALID_ARG;
+    if ((q->codes == nullptr) != (q->scales == nullptr)) return HR_ERR_INVALID_ARG;
+
+    const size_t rows = q->rows, hidden = q->hidden;
+    const size_t groups = q->group == 0 ? 1 : (hidden + q->group - 1) / q->group;
+    NormArgs a{};
+    a.in_stride = q->input_stride;
+    a.last_stride = q->residual_stride;
+    a.h_stride = q->residual_out_stride;
+    a.out_stride = q->out_stride;
+    a.codes_stride = q->codes_stride;
+    a.scales_stride = q->scales_stride;
+    if (!row_stride(rows, hidden, &a.in_stride, 2) || !row_stride(rows, hidden, &a.last_stride, 2) ||
+        !row_stride(rows, hidden, &a.h_stride, 2) || !row_stride(rows, hidden, &a.out_stride, 2) ||
+        !row_stride(rows, hidden, &a.codes_stride, 1) || !row_stride(rows, groups, &a.scales_stride, 4))
+        return HR_ERR_INVALID_ARG;
+
+    Region ins[kOperands + 1];
+    int ni = 0;
+    for (int g = 0; g < q->G; ++g) {
+        if (q->inputs[g] == nullptr) return HR_ERR_INVALID_ARG;
+        if (!aligned(q->inputs[g], 2)) return HR_ERR_ALIGNMENT;
+        a.in[g] = static_cast<const uint16_t *>(q->inputs[g]);
+        ins[ni++] = Region{q->inputs[g], rows, hidden * 2, a.in_stride * 2};
+    }
+    a.n = q->G;
+    if (q->residual != nullptr) {
+        if (!aligned(q->residual, 2)) return HR_ERR_ALIGNMENT;
+        a.in[a.n++] = static_cast<const uint16_t *>(q->residual);
+        ins[ni++] = Region{q->residual, rows, hidden * 2, a.last_stride * 2};
+    } else {
+        a.last_stride = a.in_stride;
+    }
+    if (q->weight != nullptr) {
+        if (!aligned(q->weight, q->weight_f32 ? 4 : 2)) return HR_ERR_ALIGNMENT;
+        ins[ni++] = Region{q->weight, 1, hidden * (q->weight_f32 ? 4 : 2), 0};
+    }
+    if (!aligned(q->residual_out, 2) || !aligned(q->out, 2) || !aligned(q->scales, 4) || !aligned(q->rstd, 4))
+        return HR_ERR_ALIGNMENT;
+    const Region outs[] = {{q->residual_out, rows, hidden * 2, a.h_stride * 2},
+                           {q->out, rows, hidden * 2, a.out_stride * 2},
+                           {q->codes, rows, hidden, a.codes_stride},
+                           {q->scales, rows, groups * 4, a.scales_stride * 4},
+                           {q->rstd, rows, 4, 4}};
+    // a row is read whole before any of it is written, so the 16-bit outputs
+    // may take an input's place
+    if (any_overlap(outs, 5, ins, ni, 0x3)) return HR_ERR_INVALID_ARG;
+
+    a.weight = q->weight;
+    a.weight_f32 = q->weight_f32 != 0;
+    a.h = static_cast<uint16_t *>(q->residual_out);
+    a.out = static_cast<uint16_t *>(q->out);
+    a.codes = static_cast<uint8_t *>(q->codes);
+    a.scales = q->scales;
+    a.rstd = q->rstd;
+    a.rows = rows;
+    a.hidden = static_cast<int>(hidden);
+    a.group_lanes = q->group / 8;
+    a.eps = q->eps;
+
+    const RowShape s = row_shape(a.hidden);
+    const size_t per = s.lanes > 0 ? s.threads / s.lanes : 1;
+    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, static_cast<unsigned>((rows + per - 1) / per),
+                                                    reinterpret_cast<hipStream_t>(stream), a);
+    return e == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+template <class E>
+hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
+    if (q == nullptr || q->hidden == 0) return HR_ERR_INVALID_ARG;
+    if (q->hidden > HR_RMSNORM_MAX_HIDDEN || q->rows > kMaxRows) return HR_ERR_TOO_LARGE;
+    const size_t rows = q->rows, hidden = q->hidden;
+    if (rows == 0 && q->dweight == nullptr) return HR_OK;
+    if (rows > 0 && (q->dy == nullptr || q->h == nullptr || q->rstd == nullptr || q->dx == nullptr))
+        return HR_ERR_INVALID_ARG;
+    NormGradArgs a{};
+    a.dy_stride = q->dy_stride;
+    a.h_stride = q->h_stride;
+    a.dres_stride = q->dresidual_stride;
+    a.dx_stride = q->dx_stride;
+    if (!row_stride(rows, hidden, &a.dy_stride, 2) || !row_stride(rows, hidden, &a.h_stride, 2) ||
+        !row_stride(rows, hidden, &a.dres_stride, 2) || !row_stride(rows, hidden, &a.dx_stride, 2))
+        return HR_ERR_INVALID_ARG;
+    if (!aligned(q->dy, 2) || !aligned(q->h, 2) || !aligned(q->dresidual, 2) || !aligned(q->dx, 2) ||
+        !aligned(q->weight, q->weight_f32 ? 4 : 2) || !aligned(q->rstd, 4) || !aligned(q->dweight, 4) ||
+        !aligned(q->workspace, 4))
+        return HR_ERR_ALIGNMENT;
+
+    int dev = 0, cus = 0;
+    const size_t need = hr_rmsnorm_grad_workspace(rows, hidden);
+    if (q->dweight != nullptr && need > 0 && (q->workspace == nullptr || q->workspace_bytes < need))
+        return HR_ERR_INVALID_ARG;
+    const size_t used = q->dweight != nullptr ? need : 0;
+    const Region ins[] = {{q->dy, rows, hidden * 2, a.dy_stride * 2},
+                          {q->h, rows, hidden * 2, a.h_stride * 2},
+                          {q->dresidual, rows, hidden * 2, a.dres_stride * 2},
+                          {q->weight, 1, hidden * (q->weight_f32 ? 4 : 2), 0},
+                          {q->rstd, rows, 4, 4}};
+    const Region outs[] = {{q->dx, rows, hidden * 2, a.dx_stride * 2},
+                           {q->dweight, 1, hidden * 4, 0},
+                           {q->workspace, 1, used, 0}};
+    if (any_overlap(outs, 3, ins, 5, 0x1)) return HR_ERR_INVALID_ARG;
+    if (stream_device(stream, &dev) != hipSuccess) return HR_ERR_HIP;
+    if (device_cu_count(dev, &cus) != hipSuccess) return HR_ERR_HIP;
+    if (cus > kMaxCus) cus = kMaxCus;
+    const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+
+    a.dy = static_cast<const uint16_t *>(q->dy);
+    a.h = static_cast<const uint16_t *>(q->h);
+    a.dres = static_cast<const uint16_t *>(q->dresidual);
+    a.rstd = q->rstd;
+    a.weight = q->weight;
+    a.weight_f32 = q->weight_f32 != 0;
+    a.dx = static_cast<uint16_t *>(q->dx);
+    a.rows = rows;
+    a.hidden = static_cast<int>(hidden);
+    const size_t parts = grad_groups(rows, a.hidden, cus);
+    // a single workgroup's sums are the result
+    float *part = parts == 1 ? q->dweight : static_cast<float *>(q->workspace);
+    a.part = q->dweight != nullptr ? part : nullptr;
+    if (rows > 0) {
+        const hipError_t e = launch_rows<NormGradKernel, E>(row_shape(a.hidden), hidden % 8 != 0,
+                                                            static_cast<unsigned>(parts), st, a);
+        if (e != hipSuccess) return HR_ERR_HIP;
+    }
+    if (q->dweight != nullptr && parts != 1) {
+        hipLaunchKernelGGL(sum_columns, dim3(static_cast<unsigned>((hidden + kWave - 1) / kWave)),
+                           dim3(kColumnWaves * kWave), 0, st, static_cast<const float *>(q->workspace), parts, a.hidden,
+                           q->dweight);
+        if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
+    }
+    return HR_OK;
+}
+
+}  // namespace
+
+}  // namespace hr
+
+using namespace hr;
+
+extern "C" HR_API hr_status hr_reduce_rmsnorm_f16(const hr_rmsnorm_args *args, hr_stream_t stream) {
+    return norm_impl<F16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_reduce_rmsnorm_bf16(const hr_rmsnorm_args *args, hr_stream_t stream) {
+    return norm_impl<BF16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_rmsnorm_grad_f16(const hr_rmsnorm_grad_args *args, hr_stream_t stream) {
+    return norm_grad_impl<F16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_rmsnorm_grad_bf16(const hr_rmsnorm_grad_args *args, hr_stream_t stream) {
+    return norm_grad_impl<BF16>(args, stream);
+}
+
+extern "C" HR_API size_t hr_rmsnorm_grad_workspace(size_t rows, size_t hidden) {
+    if (rows > kMaxRows || hidden == 0 || hidden > HR_RMSNORM_MAX_HIDDEN) return 0;
+    const size_t parts = grad_groups(rows, static_cast<int>(hidden), kMaxCus);
+    return parts > 1 ? parts * hidden * sizeof(float) : 0;
+}

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhr.so")
@@ -48,7 +49,9 @@ EXPORTS = ("hr_create_channel", "hr_allreduce_f16", "hr_reduce_f16", "hr_channel
            "hr_loopback_stream_create", "hr_loopback_stream_destroy",
            "hr_reduce_bf16", "hr_allreduce_bf16", "hr_admit", "hr_route_str", "hr_decode_numel",
            "hr_workspace_stride", "hr_exchange_algorithm", "hr_allreduce_group_f16",
-           "hr_allreduce_group_bf16", "hr_allreduce_group_noalloc_f16", "hr_channel_timeout_info")
+           "hr_allreduce_group_bf16", "hr_allreduce_group_noalloc_f16", "hr_channel_timeout_info",
+           "hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
+           "hr_rmsnorm_grad_workspace")
 
 HR_ROUTE_HOST = 0
 HR_DECLINE_DISABLED = 1
@@ -59,6 +62,9 @@ HR_DECLINE_TOO_LARGE = 5
 HR_DTYPE_F16 = 0
 HR_DTYPE_BF16 = 1
 HR_DTYPE_OTHER = 2
+HR_DTYPE_F32 = 3
+
+HR_RMSNORM_MAX_HIDDEN = 32768
 
 
 class hr_channel_config(ctypes.Structure):
@@ -98,6 +104,27 @@ class hr_channel_info(ctypes.Structure):
                 ("ll_stride", ctypes.c_size_t),
                 ("link_mbps", ctypes.c_uint32),
                 ("dev_epochs", ctypes.c_void_p)]
+
+
+class hr_rmsnorm_args(ctypes.Structure):
+    _fields_ = [("inputs", ctypes.c_void_p * HR_MAX_G),
+                *((n, ctypes.c_void_p) for n in ("residual", "weight", "residual_out", "out", "codes", "scales",
+                                                 "rstd")),
+                *((n, ctypes.c_size_t) for n in ("rows", "hidden", "input_stride", "residual_stride",
+                                                 "residual_out_stride", "out_stride", "codes_stride",
+                                                 "scales_stride")),
+                ("G", ctypes.c_int),
+                ("weight_f32", ctypes.c_int),
+                ("group", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class hr_rmsnorm_grad_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("dy", "h", "rstd", "weight", "dresidual", "dx", "dweight",
+                                                 "workspace")),
+                *((n, ctypes.c_size_t) for n in ("workspace_bytes", "rows", "hidden", "dy_stride", "h_stride",
+                                                 "dresidual_stride", "dx_stride")),
+                ("weight_f32", ctypes.c_int)]
 
 
 class HrError(RuntimeError):
@@ -150,11 +177,16 @@ def load() -> ctypes.CDLL:
     lib.hr_route_str.argtypes = [ctypes.c_int]
     lib.hr_route_str.restype = ctypes.c_char_p
     lib.hr_decode_numel.argtypes = [ctypes.c_size_t, ctypes.c_size_t, ctypes.c_size_t]
-    lib.hr_decode_numel.restype = ctypes.c_size_t
     lib.hr_workspace_stride.argtypes = [ctypes.c_size_t]
-    lib.hr_workspace_stride.restype = ctypes.c_size_t
+    # argument structs: byref of the ctypes struct, or its bytes
+    for name in ("hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16"):
+        getattr(lib, name).argtypes = [vp, vp]
+    lib.hr_rmsnorm_grad_workspace.argtypes = [ctypes.c_size_t, ctypes.c_size_t]
+    sizes = ("hr_decode_numel", "hr_workspace_stride", "hr_rmsnorm_grad_workspace")
+    for name in sizes:
+        getattr(lib, name).restype = ctypes.c_size_t
     for name in EXPORTS:
-        if name not in ("hr_status_str", "hr_route_str", "hr_decode_numel", "hr_workspace_stride"):
+        if name not in ("hr_status_str", "hr_route_str", *sizes):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -297,6 +329,31 @@ def hr_workspace_stride(numel: int) -> int:
     return load().hr_workspace_stride(numel)
 
 
+def hr_reduce_rmsnorm_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_rmsnorm_args.  Returns the hr_status code."""
+    return load().hr_reduce_rmsnorm_f16(ctypes.byref(args), stream)
+
+
+def hr_reduce_rmsnorm_bf16(args, stream: int) -> int:
+    """As hr_reduce_rmsnorm_f16 for bfloat16 buffers."""
+    return load().hr_reduce_rmsnorm_bf16(ctypes.byref(args), stream)
+
+
+def hr_rmsnorm_grad_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_rmsnorm_grad_args.  Returns the hr_status code."""
+    return load().hr_rmsnorm_grad_f16(ctypes.byref(args), stream)
+
+
+def hr_rmsnorm_grad_bf16(args, stream: int) -> int:
+    """As hr_rmsnorm_grad_f16 for bfloat16 buffers."""
+    return load().hr_rmsnorm_grad_bf16(ctypes.byref(args), stream)
+
+
+def hr_rmsnorm_grad_workspace(rows: int, hidden: int) -> int:
+    """Bytes of workspace that a gradient call with dweight needs."""
+    return load().hr_rmsnorm_grad_workspace(rows, hidden)
+
+
 def workspace(G: int, numel: int, dtype=None, device=0):
     """A device buffer holding G contributions in the hr_workspace_stride
     layout; returns (buffer, [view of contribution g])."""
@@ -404,6 +461,168 @@ def allreduce_group_noalloc(ins, outs, status=None, stream=None):
     _check(hr_allreduce_group_noalloc_f16(ip, op, W, n, sp, _stream_handle(stream, outs[0])),
            "hr_allreduce_group_noalloc_f16")
     return outs
+
+
+# ------------------------------------------------------- around the combine
+#
+# The argument structs go over as packed bytes: one struct.pack costs a tenth
+# of a ctypes.Structure with as many fields (0.6 against 6 us), which is as
+# long as a small call's kernel runs.
+
+_NORM = struct.Struct("@23P8N3if")
+_NORM_GRAD = struct.Struct("@8P7Ni4x")
+_entries = {}
+
+
+def _entry(name: str, dtype):
+    """(function, its name) of an entry point's variant for torch.float16 or
+    torch.bfloat16, bound once."""
+    got = _entries.get((name, dtype))
+    if got is None:
+        _tm()
+        if dtype is not _F16 and dtype is not _BF16:
+            raise TypeError(f"{name}: expected torch.float16 or torch.bfloat16, got {dtype}")
+        full = f"{name}_{'bf16' if dtype is _BF16 else 'f16'}"
+        got = _entries[(name, dtype)] = (getattr(load(), full), full)
+    return got
+
+
+def _row_view(t, name: str, dtype, rows=None, width=None):
+    """(address, rows, row length, row stride) of a device tensor whose last
+    dimension is a row: two dimensions with any row stride, or contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a device tensor")
+    shape = t.shape
+    if len(shape) == 2:
+        r, w = shape
+        sr, sc = t.stride()
+        if (sc != 1 and w > 1) or (r > 1 and sr < w):
+            raise ValueError(f"{name}: expected rows of adjacent values that do not overlap")
+        if r <= 1:
+            sr = 0
+    else:
+        if not shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected two dimensions or a contiguous tensor")
+        w, sr = shape[-1], 0
+        r = t.numel() // w if w else 0
+    if rows is not None and (r != rows or w != width):
+        raise ValueError(f"{name}: {r} rows of {w} values, expected {rows} of {width}")
+    return t.data_ptr(), r, w, sr
+
+
+def _flat_ptr(t, name: str, dtype, numel: int) -> int:
+    """Address of a contiguous device tensor of ``numel`` values."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a device tensor")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {numel} values")
+    return t.data_ptr()
+
+
+def _weight_ptr(t, dtype, hidden: int):
+    """(address, is binary32) of a norm's weight, or of none."""
+    if t is None:
+        return 0, 0
+    f32 = t.dtype is _torch.float32
+    return _flat_ptr(t, "weight", _torch.float32 if f32 else dtype, hidden), int(f32)
+
+
+def _scratch(nbytes: int, like, stream):
+    """A workspace for one call on ``stream``.  It comes from that stream's
+    pool, so what reuses its memory afterwards is ordered behind the call."""
+    if stream is None:
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+
+
+def reduce_rmsnorm(tensors, out=None, *, residual=None, residual_out=None, weight=None, eps: float = 1e-6,
+                   out8=None, scales=None, group: int = 0, rstd=None, stream=None):
+    """The fold of ``tensors`` with ``residual`` as its last operand (into
+    ``residual_out``), its root-mean-square norm times ``weight`` (into
+    ``out``), and the norm in e4m3 with scales (into ``out8`` and ``scales``),
+    in one kernel (hr_reduce_rmsnorm).
+
+    ``tensors`` are torch.float16 or torch.bfloat16, all of one shape and row
+    stride; the last dimension is the row.  ``weight`` has their type or
+    torch.float32.  ``out8`` is torch.float8_e4m3fn and ``scales``
+    torch.float32, one per row (``group`` 0) or per 32, 64 or 128 values of
+    it.  ``rstd`` (torch.float32, one per row) is what rmsnorm_grad takes.
+    Whatever is None is not computed or not written; ``residual_out`` and
+    ``out`` may be an input."""
+    first = tensors[0]
+    dt = first.dtype
+    fn, name = _entry("hr_reduce_rmsnorm", dt)
+    if len(tensors) > HR_MAX_G:
+        raise ValueError(f"{len(tensors)} contributions, at most {HR_MAX_G}")
+    p0, rows, hidden, stride = _row_view(first, "tensors[0]", dt)
+    ptrs = [p0]
+    for i in range(1, len(tensors)):
+        p, _, _, s = _row_view(tensors[i], f"tensors[{i}]", dt, rows, hidden)
+        if s != stride and (s or hidden) != (stride or hidden):
+            raise ValueError(f"tensors[{i}]: row stride {s}, tensors[0] has {stride}")
+        ptrs.append(p)
+    ptrs += [0] * (HR_MAX_G - len(ptrs))
+    rp = hp = op = cp = sp = tp = 0
+    rs = hs = os_ = cs = ss = 0
+    if residual is not None:
+        rp, _, _, rs = _row_view(residual, "residual", dt, rows, hidden)
+    if residual_out is not None:
+        hp, _, _, hs = _row_view(residual_out, "residual_out", dt, rows, hidden)
+    if out is not None:
+        op, _, _, os_ = _row_view(out, "out", dt, rows, hidden)
+    if out8 is not None:
+        cp, _, _, cs = _row_view(out8, "out8", _torch.float8_e4m3fn, rows, hidden)
+    if scales is not None:
+        groups = -(-hidden // group) if group else 1
+        if scales.dim() == 1 and groups == 1:
+            scales = scales.unsqueeze(1)
+        sp, _, _, ss = _row_view(scales, "scales", _torch.float32, rows, groups)
+    if rstd is not None:
+        tp = _flat_ptr(rstd, "rstd", _torch.float32, rows)
+    wp, wf = _weight_ptr(weight, dt, hidden)
+    args = _NORM.pack(*ptrs, rp, wp, hp, op, cp, sp, tp, rows, hidden, stride, rs, hs, os_, cs, ss,
+                      len(tensors), wf, group, eps)
+    st = fn(args, _stream_handle(stream, first))
+    if st != HR_OK:
+        raise HrError(st, name)
+    return out
+
+
+def rmsnorm_grad(dy, h, rstd, dx, *, weight=None, dresidual=None, dweight=None, workspace=None, stream=None):
+    """The gradient of reduce_rmsnorm's ``out``: ``dx`` of its sum ``h`` (the
+    forward call's residual_out), ``dresidual`` added, and ``dweight``
+    (torch.float32) if given (hr_rmsnorm_grad).  ``workspace``: a device
+    tensor of hr_rmsnorm_grad_workspace(rows, hidden) bytes or more; None
+    takes one from torch's allocator when the call needs one."""
+    dt = h.dtype
+    fn, name = _entry("hr_rmsnorm_grad", dt)
+    hp, rows, hidden, hs = _row_view(h, "h", dt)
+    yp, _, _, ys = _row_view(dy, "dy", dt, rows, hidden)
+    xp, _, _, xs = _row_view(dx, "dx", dt, rows, hidden)
+    tp = _flat_ptr(rstd, "rstd", _torch.float32, rows)
+    rp = rs = gp = kp = kb = 0
+    if dresidual is not None:
+        rp, _, _, rs = _row_view(dresidual, "dresidual", dt, rows, hidden)
+    wp, wf = _weight_ptr(weight, dt, hidden)
+    if dweight is not None:
+        gp = _flat_ptr(dweight, "dweight", _torch.float32, hidden)
+        if workspace is None:
+            need = load().hr_rmsnorm_grad_workspace(rows, hidden)
+            if need:
+                workspace = _scratch(need, h, stream)
+        if workspace is not None:
+            kb = workspace.numel() * workspace.element_size()
+            kp = _flat_ptr(workspace, "workspace", workspace.dtype, workspace.numel())
+    args = _NORM_GRAD.pack(yp, hp, tp, wp, rp, xp, gp, kp, kb, rows, hidden, ys, hs, rs, xs, wf)
+    st = fn(args, _stream_handle(stream, h))
+    if st != HR_OK:
+        raise HrError(st, name)
+    return dx
 
 
 class Channel:

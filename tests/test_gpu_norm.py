@@ -1,0 +1,422 @@
+"""hr_reduce_rmsnorm and hr_rmsnorm_grad on the GPU: the sum bit for bit
+against the oracle's fold, the rest against the formulas in 64 bits, at row
+lengths on both sides of every layout's limit, odd lengths, strides and
+addresses, special values, and in place."""
+import numpy as np
+import pytest
+import torch
+
+from message_fp16_all_amd import hr
+from _gpu import needs_gpu, specials_mix, specials_mix_bf16
+from _rows import F32, TYPES, Maker, fold_ref, half_step, same, within
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+EPS = 1e-5
+F8 = torch.float8_e4m3fn
+
+
+def norm_ref(h, weight, eps=EPS):
+    """(y, rstd) in 64 bits of 16-bit sums (CPU)."""
+    x = h.double()
+    rstd = 1.0 / torch.sqrt((x * x).mean(1) + eps)
+    y = x * rstd[:, None]
+    return (y if weight is None else y * weight.double().cpu()), rstd
+
+
+def check_codes(codes, scales, y, group, what):
+    """Scales against the largest magnitudes, codes against y / scale."""
+    width = y.shape[1] if group == 0 else group
+    c = codes.float().double().cpu()
+    s = scales.double().cpu().reshape(y.shape[0], -1)
+    parts = list(y.split(width, 1))
+    assert s.shape[1] == len(parts), what
+    for i, part in enumerate(parts):
+        top = part.abs().amax(1)
+        want = (top / 448).clamp_min(2.0 ** -126)
+        within(s[:, i], want, want * F32, f"{what}: scale {i}")
+        got = c[:, i * width:i * width + part.shape[1]] * s[:, i:i + 1]
+        # half a step of e4m3: 2^-4 of the value, or half of its smallest, 2^-10
+        tol = part.abs() * (2.0 ** -4 + F32) + s[:, i:i + 1] * 2.0 ** -10 * (1 + F32)
+        within(got, torch.where(torch.isnan(s[:, i:i + 1]), torch.nan, part), tol, f"{what}: codes {i}")
+
+
+def run_case(seed, dt, rows, hidden, G, residual=True, weight="same", group=None, out=True, stride=None, offset=0):
+    m = Maker(seed)
+    dtype = TYPES[dt]
+    xs = [m.normal(rows, hidden, sigma=0.5, dtype=dtype) for _ in range(G)]
+    r = m.normal(rows, hidden, dtype=dtype) if residual else None
+    w = {"same": lambda: (m.normal(hidden, sigma=0.2) + 1).to(dtype), "f32": lambda: m.normal(hidden, sigma=0.2) + 1,
+         "none": lambda: None}[weight]()
+    dx = [m.place(rows, hidden, dtype, stride, offset, x) for x in xs]
+    dr = m.place(rows, hidden, dtype, stride, offset + 1, r) if residual else None
+    dw = m.place(1, hidden, w.dtype, None, offset, w[None])[0] if w is not None else None
+    h = m.place(rows, hidden, dtype, stride, offset)
+    y = m.place(rows, hidden, dtype, stride, offset + 3) if out else None
+    rstd = torch.full((rows,), 9.0, device="cuda:0")
+    codes = scales = None
+    if group is not None:
+        codes = m.place(rows, hidden, F8, stride, offset)
+        n = -(-hidden // group) if group else 1
+        scales = m.place(rows, n, torch.float32, n + 3 if stride else None, 1)
+    print(f"norm {dt} {rows}x{hidden} G={G} residual={residual} weight={weight} group={group} stride={stride} "
+          f"offset={offset}", flush=True)
+    hr.reduce_rmsnorm(dx, y, residual=dr, residual_out=h, weight=dw, eps=EPS, out8=codes, scales=scales,
+                      group=group or 0, rstd=rstd)
+    torch.cuda.synchronize()
+    href = fold_ref(xs + ([r] if residual else []))
+    same(h, href, "h")
+    yref, rref = norm_ref(href, w)
+    within(rstd, rref, rref * F32, "rstd")
+    if out:
+        within(y, yref, half_step(dtype, yref) * (1 + F32) + yref.abs() * F32, "y")
+    if group is not None:
+        check_codes(codes, scales, yref, group, "e4m3")
+    m.check_frames()
+
+
+# both sides of every layout's limit: 16, 32 and 64 lanes per row, then a
+# workgroup with one, two and four units per thread
+WIDTHS = [1, 7, 8, 9, 64, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 2048, 4096, 4097, 5120, 6144, 8192, 16384,
+          16385, 20001, 32767, 32768]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_widths(dt, hidden):
+    run_case(hidden, dt, 5, hidden, 3, group=128)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("G", list(range(1, 17)))
+def test_group_sizes(dt, G):
+    for hidden in (128, 1024, 6144, 17000):
+        run_case(100 + G, dt, 3, hidden, G, residual=G % 2 == 0, weight="f32", group=0)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 1000, 5003])
+def test_rows(rows):
+    run_case(rows, "bf16", rows, 128, 2, weight="none", group=32)
+    run_case(rows, "f16", rows, 320, 1, residual=False, group=64)
+    if rows <= 1000:
+        run_case(rows, "bf16", rows, 5120, 2, group=0)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden,stride,offset", [(128, 130, 1), (500, 777, 3), (4096, 4099, 1), (5121, 5121, 5),
+                                                  (9000, 9008, 7), (32768, 40001, 1)])
+def test_strides_and_odd_addresses(dt, hidden, stride, offset):
+    for group in (0, 128):
+        run_case(hidden, dt, 7, hidden, 2, weight="f32", group=group, stride=stride, offset=offset)
+
+
+def test_codes_alone():
+    run_case(1, "bf16", 33, 6144, 8, group=128, out=False)
+    run_case(2, "f16", 33, 200, 1, group=0, out=False)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_special_values(dt):
+    """Infinities, NaN, subnormals and zeros: rows of each, and all together."""
+    dtype = TYPES[dt]
+    n = 2048
+    make = specials_mix_bf16 if dt == "bf16" else specials_mix
+    rows = [torch.from_numpy(make(n, s).view(np.int16).copy()).view(dtype) for s in (1, 2)]
+    tiny = torch.finfo(dtype).tiny
+    z = torch.zeros(n, dtype=dtype)
+    one = {"inf": float("inf"), "-inf": float("-inf"), "nan": float("nan")}
+    x = [rows[0], z, z + tiny / 4, -z]
+    for v in one.values():
+        r = torch.linspace(-3, 3, n).to(dtype)
+        r[777] = v
+        x.append(r)
+    x = torch.stack(x)
+    res = torch.zeros_like(x)
+    res[0] = rows[1]
+    dev = "cuda:0"
+    h, y, codes = (torch.empty(x.shape, dtype=t, device=dev) for t in (dtype, dtype, F8))
+    scales, rstd = torch.empty(len(x), 16, device=dev), torch.empty(len(x), device=dev)
+    hr.reduce_rmsnorm([x.to(dev)], y, residual=res.to(dev), residual_out=h, eps=EPS, out8=codes, scales=scales,
+                      group=128, rstd=rstd)
+    torch.cuda.synchronize()
+    href = fold_ref([x, res])
+    same(h, href, "h")
+    # squares are summed in 32 bits: the reference says so where they pass its range
+    f = href.float()
+    rref = (1.0 / torch.sqrt((f * f).mean(1) + EPS)).double()
+    yref = href.double() * rref[:, None]
+    ok = torch.isfinite(href).all(1)
+    within(rstd, rref, rref.abs() * 2 * F32, "rstd")
+    within(y[ok.to(dev)], yref[ok], half_step(dtype, yref[ok]) + yref[ok].abs() * 3 * F32, "y")
+    assert torch.equal(torch.isnan(y).cpu(), torch.isnan(yref)), "NaN where the formula gives NaN"
+    # the zero rows: codes 0 and the smallest scale
+    assert (codes[1].float() == 0).all() and (scales[1] == 2.0 ** -126).all()
+    # the groups with a NaN have a NaN scale and NaN codes; a row with an infinity is zero elsewhere
+    for i, v in enumerate(one.values()):
+        g = 777 // 128
+        assert torch.isnan(scales[4 + i, g]) and torch.isnan(codes[4 + i, 777].float())
+        if v == v:
+            assert (codes[4 + i, :128].float() == 0).all()
+        else:
+            assert torch.isnan(codes[4 + i].float()).all()
+
+
+@pytest.mark.parametrize("hidden", [128, 4096, 9001, 20000])
+def test_in_place(hidden):
+    """residual_out over the residual, out over a contribution; and out over
+    the residual beside residual_out over a contribution."""
+    m = Maker(hidden)
+    rows, dtype = 9, torch.bfloat16
+    xs = [m.normal(rows, hidden, dtype=dtype) for _ in range(3)]
+    r = m.normal(rows, hidden, dtype=dtype)
+    href = fold_ref(xs + [r])
+    yref, _ = norm_ref(href, None)
+    for swap in (False, True):
+        dx, dr = [x.cuda() for x in xs], r.cuda()
+        h, y = (dx[1], dr) if swap else (dr, dx[1])
+        hr.reduce_rmsnorm(dx, y, residual=dr, residual_out=h, eps=EPS)
+        torch.cuda.synchronize()
+        same(h, href, "h")
+        within(y, yref, half_step(dtype, yref) + yref.abs() * F32, "y")
+
+
+def test_same_bits_as_reduce():
+    m = Maker(5)
+    xs = [m.normal(64, 6144, dtype=torch.float16).cuda() for _ in range(9)]
+    out, h = torch.empty_like(xs[0]), torch.empty_like(xs[0])
+    hr.reduce(xs, out)
+    hr.reduce_rmsnorm(xs[:8], residual=xs[8], residual_out=h)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), h.view(torch.int16))
+
+
+def test_no_rows_and_other_shapes():
+    x = torch.zeros(0, 64, dtype=torch.float16, device="cuda:0")
+    hr.reduce_rmsnorm([x], torch.empty_like(x))
+    x = torch.randn(2, 3, 40, 128, device="cuda:0").half()      # heads, contiguous
+    y = torch.empty_like(x)
+    hr.reduce_rmsnorm([x], y, eps=EPS)
+    ref, _ = norm_ref(x.cpu().reshape(-1, 128), None)
+    within(y.reshape(-1, 128), ref, half_step(torch.float16, ref) + ref.abs() * F32, "heads")
+    v = torch.randn(4096, device="cuda:0").half()               # one row
+    y = torch.empty_like(v)
+    hr.reduce_rmsnorm([v], y, eps=EPS)
+    ref, _ = norm_ref(v.cpu()[None], None)
+    within(y[None], ref, half_step(torch.float16, ref) + ref.abs() * F32, "one row")
+
+
+def test_far_rows():
+    """Offsets past 2^32 bytes (and past 2^31 values) of a strided buffer."""
+    hidden, stride, rows = 256, (1 << 31) + 24, 2
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    buf = torch.empty(stride + hidden, dtype=torch.float16, device="cuda:0")
+    view = buf.as_strided((rows, hidden), (stride, 1))
+    x = torch.randn(rows, hidden).half()
+    view.copy_(x)
+    y = torch.empty(rows, hidden, dtype=torch.float16, device="cuda:0")
+    hr.reduce_rmsnorm([view], y, residual_out=view, eps=EPS)
+    ref, _ = norm_ref(x, None)
+    within(y, ref, half_step(torch.float16, ref) + ref.abs() * F32, "y")
+    same(view, x, "h")
+
+
+# ------------------------------------------------------------------ gradient
+
+def grad_ref(dy, h, rstd, w, dres):
+    """dx, dweight in 64 bits, and the magnitudes that went into them."""
+    dy, h, r = dy.double(), h.double(), rstd.double().cpu()[:, None]
+    g = dy * (w.double() if w is not None else 1.0)
+    u = h * r
+    mean = (g * u).mean(1, keepdim=True)
+    dx = r * (g - u * mean)
+    size = r * (g.abs() + u.abs() * (g * u).abs().mean(1, keepdim=True))
+    if dres is not None:
+        dx, size = dx + dres.double(), size + dres.double().abs()
+    return dx, size, (dy * u).sum(0), (dy * u).abs().sum(0)
+
+
+def run_grad(seed, dt, rows, hidden, weight="same", dres=True, stride=None, offset=0, in_place=None, workspace=True):
+    m = Maker(seed)
+    dtype = TYPES[dt]
+    dy, h = m.normal(rows, hidden, sigma=0.3, dtype=dtype), m.normal(rows, hidden, sigma=2.0, dtype=dtype)
+    r = m.normal(rows, hidden, sigma=0.3, dtype=dtype) if dres else None
+    w = {"same": lambda: (m.normal(hidden, sigma=0.2) + 1).to(dtype), "f32": lambda: m.normal(hidden, sigma=0.2) + 1,
+         "none": lambda: None}[weight]()
+    rstd = (1.0 / torch.sqrt(h.float().square().mean(1) + EPS)).cuda()
+    d = {"dy": m.place(rows, hidden, dtype, stride, offset, dy), "h": m.place(rows, hidden, dtype, stride, offset + 1, h),
+         "dres": m.place(rows, hidden, dtype, stride, offset, r) if dres else None}
+    dx = d[in_place] if in_place else m.place(rows, hidden, dtype, stride, offset + 3)
+    dw = m.place(1, hidden, torch.float32, None, 1)[0]
+    ws = None
+    if workspace:
+        # dirty, so that nothing is taken for granted
+        ws = torch.full((hr.hr_rmsnorm_grad_workspace(rows, hidden) + 64,), 255, dtype=torch.uint8, device="cuda:0")
+    print(f"norm grad {dt} {rows}x{hidden} weight={weight} dres={dres} stride={stride} in_place={in_place}", flush=True)
+    hr.rmsnorm_grad(d["dy"], d["h"], rstd, dx, weight=w.cuda() if w is not None else None, dresidual=d["dres"],
+                    dweight=dw, workspace=ws)
+    torch.cuda.synchronize()
+    ref, size, wref, wsize = grad_ref(dy, h, rstd, w, r)
+    within(dx, ref, half_step(dtype, ref) * (1 + F32) + size * 2 * F32, "dx")
+    # a column's sum: at most rows additions in sequence and 16 more
+    within(dw, wref, wsize * (rows + 32) * 2.0 ** -24, "dweight")
+    m.check_frames()
+    return dx.clone(), dw.clone()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_grad_widths(dt, hidden):
+    run_grad(hidden, dt, 5, hidden)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 511, 512, 513, 8193, 20000])
+def test_grad_rows(rows):
+    run_grad(rows, "bf16", rows, 128, weight="f32", dres=False)
+    run_grad(rows, "f16", rows, 257, weight="none")
+    if rows < 8000:
+        run_grad(rows, "f16", rows, 4096)
+        run_grad(rows, "bf16", rows, 8200, weight="f32", workspace=False)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden,stride,offset", [(128, 130, 1), (500, 777, 3), (5121, 5121, 5), (32767, 40001, 1)])
+def test_grad_strides(dt, hidden, stride, offset):
+    run_grad(hidden, dt, 19, hidden, weight="f32", stride=stride, offset=offset)
+
+
+@pytest.mark.parametrize("what", ["dy", "h", "dres"])
+def test_grad_in_place(what):
+    for hidden in (128, 4096, 20000):
+        run_grad(3, "f16", 700, hidden, in_place=what)
+
+
+def test_grad_is_the_same_every_time():
+    a = run_grad(9, "bf16", 5003, 1024)
+    b = run_grad(9, "bf16", 5003, 1024)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_grad_without_rows_or_weight_gradient():
+    dw = torch.full((96,), 5.0, device="cuda:0")
+    e = torch.zeros(0, 96, dtype=torch.float16, device="cuda:0")
+    hr.rmsnorm_grad(e, e, torch.zeros(0, device="cuda:0"), torch.empty_like(e), dweight=dw)
+    assert (dw == 0).all()
+    m = Maker(4)
+    h, dy = m.normal(40, 96, dtype=torch.float16), m.normal(40, 96, dtype=torch.float16)
+    rstd = (1.0 / torch.sqrt(h.float().square().mean(1) + EPS)).cuda()
+    dx = torch.empty(40, 96, dtype=torch.float16, device="cuda:0")
+    hr.rmsnorm_grad(dy.cuda(), h.cuda(), rstd, dx)
+    ref, size, _, _ = grad_ref(dy, h, rstd, None, None)
+    within(dx, ref, half_step(torch.float16, ref) + size * 2 * F32, "dx")
+
+
+def test_grad_against_differences():
+    """dx and dweight against central differences of the forward formula in 64
+    bits.  A difference's own error is step^2 / 6 times the third derivative,
+    far below the 16-bit rounding at step 1e-4 for values of order one."""
+    m = Maker(12)
+    rows, hidden, step = 2, 24, 1e-4
+    h, dy = m.normal(rows, hidden, dtype=torch.float16), m.normal(rows, hidden, dtype=torch.float16)
+    w = m.normal(hidden) + 1
+    x = h.double()
+
+    def loss(x, w):
+        return (x / torch.sqrt((x * x).mean(1, keepdim=True) + EPS) * w * dy.double()).sum()
+
+    ref = torch.zeros(rows, hidden, dtype=torch.float64)
+    wref = torch.zeros(hidden, dtype=torch.float64)
+    for i in range(rows):
+        for j in range(hidden):
+            e = torch.zeros_like(x)
+            e[i, j] = step
+            ref[i, j] = (loss(x + e, w.double()) - loss(x - e, w.double())) / (2 * step)
+    for j in range(hidden):
+        e = torch.zeros(hidden, dtype=torch.float64)
+        e[j] = step
+        wref[j] = (loss(x, w.double() + e) - loss(x, w.double() - e)) / (2 * step)
+    out, hh, rstd = (torch.empty(rows, hidden, dtype=torch.float16, device="cuda:0") for _ in range(2)), None, None
+    y, hh = out
+    rstd = torch.empty(rows, device="cuda:0")
+    hr.reduce_rmsnorm([h.cuda()], y, residual_out=hh, weight=w.cuda(), eps=EPS, rstd=rstd)
+    dx, dw = torch.empty_like(hh), torch.empty(hidden, device="cuda:0")
+    hr.rmsnorm_grad(dy.cuda(), hh, rstd, dx, weight=w.cuda(), dweight=dw)
+    _, size, _, wsize = grad_ref(dy, h, rstd, w, None)
+    within(dx, ref, half_step(torch.float16, ref) + size * 2 * F32 + 1e-6, "dx")
+    within(dw, wref, wsize * 64 * 2.0 ** -24 + 1e-6, "dweight")
+
+
+# ------------------------------------------------------------ streams, graphs
+
+def test_another_stream_and_a_graph():
+    m = Maker(21)
+    rows, hidden = 300, 4096
+    xs = [m.normal(rows, hidden, dtype=torch.float16).cuda() for _ in range(2)]
+    w = (m.normal(hidden, sigma=0.1) + 1).cuda()
+    h, y, dx = (torch.empty_like(xs[0]) for _ in range(3))
+    rstd, dw = torch.empty(rows, device="cuda:0"), torch.empty(hidden, device="cuda:0")
+    ws = torch.empty(hr.hr_rmsnorm_grad_workspace(rows, hidden), dtype=torch.uint8, device="cuda:0")
+
+    def step(stream=None, workspace=None):
+        hr.reduce_rmsnorm(xs, y, residual_out=h, weight=w, rstd=rstd, stream=stream)
+        hr.rmsnorm_grad(y, h, rstd, dx, weight=w, dweight=dw, workspace=workspace, stream=stream)
+
+    def eager():
+        step()
+        torch.cuda.synchronize()
+        return [t.clone() for t in (h, y, dx, rstd, dw)]
+
+    first = eager()
+    s = torch.cuda.Stream()
+    for t in (h, y, dx, rstd, dw):
+        t.zero_()
+    torch.cuda.synchronize()
+    step(stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (h, y, dx, rstd, dw)))
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(workspace=ws)
+    for k in range(4):
+        for x in xs:
+            x.copy_(m.normal(rows, hidden, dtype=torch.float16))
+        want = eager()
+        for t in (h, y, dx, rstd, dw):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (h, y, dx, rstd, dw))), f"replay {k}"
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_binding_refusals():
+    x = torch.zeros(4, 64, dtype=torch.float16, device="cuda:0")
+    y = torch.empty_like(x)
+    for bad, err in [(lambda: hr.reduce_rmsnorm([x.float()], y), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x, x.bfloat16()], y), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x], y.bfloat16()), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x], y.cpu()), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x], y[:3]), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x], y.t()), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x[:1].expand(4, 64)], y), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x, x[:, :64].clone().repeat(1, 2)[:, :64]], y), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x] * 17, y), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x], y, weight=torch.ones(63, device="cuda:0")), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x], y, weight=torch.ones(64, device="cuda:0").double()), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x], y, rstd=torch.ones(3, device="cuda:0")), ValueError),
+                     (lambda: hr.reduce_rmsnorm([x], y, out8=torch.empty(4, 64, dtype=F8, device="cuda:0")),
+                      hr.HrError),
+                     (lambda: hr.reduce_rmsnorm([x], y, out8=y, scales=torch.ones(4, device="cuda:0")), TypeError),
+                     (lambda: hr.reduce_rmsnorm([x], y, eps=-1.0), hr.HrError),
+                     (lambda: hr.reduce_rmsnorm([x]), hr.HrError),
+                     (lambda: hr.rmsnorm_grad(y, x, torch.ones(4, device="cuda:0"), y.bfloat16()), TypeError),
+                     (lambda: hr.rmsnorm_grad(y, x, torch.ones(5, device="cuda:0"), y), ValueError),
+                     (lambda: hr.rmsnorm_grad(y, x, torch.ones(4, device="cuda:0"), y,
+                                              dweight=torch.ones(64, device="cuda:0").half()), TypeError)]:
+        with pytest.raises(err):
+            bad()
+    hr.reduce_rmsnorm([x + 1], y, eps=0.0)
+    torch.cuda.synchronize()
+    assert (y == 1).all()
