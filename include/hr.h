@@ -681,6 +681,56 @@ HR_API hr_status hr_rmsnorm_grad_bf16(const hr_rmsnorm_grad_args *args, hr_strea
 /* Bytes of workspace that a gradient call with dweight needs (0: none). */
 HR_API size_t hr_rmsnorm_grad_workspace(size_t rows, size_t hidden);
 
+/* Largest number of logits per token and of picks. */
+#define HR_ROUTER_MAX_EXPERTS 1024
+#define HR_ROUTER_MAX_K 32
+
+/*
+ * hr_router_topk -- which experts a token goes to, and with which weights: the
+ * k largest of its logits and their softmax.
+ *
+ *     p       = softmax over the token's logits
+ *     ids     = the k largest logits, by value downward, equal ones (+0 and
+ *               -0 are equal) by index upward
+ *     weights = p of the picks; with renormalize, divided by their sum
+ *
+ * A logit that is NaN or -infinity is never picked and has p 0 (a masked
+ * expert); where fewer than k are left, the remaining picks have id -1 and
+ * weight 0 (a token that is all masked picks nothing).  +infinities share the
+ * softmax equally.  Exponents and sums are binary32.
+ *
+ * logits:  tokens rows of `experts` values of `dtype` (HR_DTYPE_F16, _BF16 or
+ *          _F32), logits_stride values apart (0 = experts).
+ * weights, ids: tokens x k, contiguous.
+ * Errors: HR_ERR_INVALID_ARG (k outside 1..experts, dtype, null pointers, a
+ * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (experts
+ * above HR_ROUTER_MAX_EXPERTS, k above HR_ROUTER_MAX_K, 2^31 tokens or more),
+ * HR_ERR_HIP.
+ */
+HR_API hr_status hr_router_topk(const void *logits, hr_dtype dtype, size_t tokens, int experts,
+                                size_t logits_stride, int k, int renormalize, float *weights, int32_t *ids,
+                                hr_stream_t stream);
+
+/*
+ * hr_router_topk_grad -- the gradient of hr_router_topk's weights with respect
+ * to the logits (the choice itself is taken as fixed).  With c the token's sum
+ * of dweights x weights:
+ *
+ *     dlogits_e = p_e * (dweights of e's pick, or 0, - c)
+ *     with renormalize: weights * (dweights - c) at the picks, 0 elsewhere
+ *
+ * weights, ids: the forward call's.  An id outside 0..experts-1 is no pick,
+ * and its dweights are not used.
+ * logits:  the forward call's; with renormalize not read, and may be NULL.
+ * dlogits: tokens rows of dtype, dlogits_stride apart (0 = experts); it may be
+ *          exactly logits.
+ * Errors: as hr_router_topk.
+ */
+HR_API hr_status hr_router_topk_grad(const float *dweights, const float *weights, const int32_t *ids,
+                                     const void *logits, hr_dtype dtype, size_t tokens, int experts,
+                                     size_t logits_stride, int k, int renormalize, void *dlogits,
+                                     size_t dlogits_stride, hr_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 HR_API const char *hr_status_str(hr_status s);
 

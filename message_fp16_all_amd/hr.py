@@ -51,7 +51,7 @@ EXPORTS = ("hr_create_channel", "hr_allreduce_f16", "hr_reduce_f16", "hr_channel
            "hr_workspace_stride", "hr_exchange_algorithm", "hr_allreduce_group_f16",
            "hr_allreduce_group_bf16", "hr_allreduce_group_noalloc_f16", "hr_channel_timeout_info",
            "hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
-           "hr_rmsnorm_grad_workspace")
+           "hr_rmsnorm_grad_workspace", "hr_router_topk", "hr_router_topk_grad")
 
 HR_ROUTE_HOST = 0
 HR_DECLINE_DISABLED = 1
@@ -65,6 +65,8 @@ HR_DTYPE_OTHER = 2
 HR_DTYPE_F32 = 3
 
 HR_RMSNORM_MAX_HIDDEN = 32768
+HR_ROUTER_MAX_EXPERTS = 1024
+HR_ROUTER_MAX_K = 32
 
 
 class hr_channel_config(ctypes.Structure):
@@ -182,6 +184,10 @@ def load() -> ctypes.CDLL:
     for name in ("hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16"):
         getattr(lib, name).argtypes = [vp, vp]
     lib.hr_rmsnorm_grad_workspace.argtypes = [ctypes.c_size_t, ctypes.c_size_t]
+    lib.hr_router_topk.argtypes = [vp, ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
+                                   ctypes.c_int, vp, vp, vp]
+    lib.hr_router_topk_grad.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t,
+                                        ctypes.c_int, ctypes.c_int, vp, ctypes.c_size_t, vp]
     sizes = ("hr_decode_numel", "hr_workspace_stride", "hr_rmsnorm_grad_workspace")
     for name in sizes:
         getattr(lib, name).restype = ctypes.c_size_t
@@ -352,6 +358,21 @@ def hr_rmsnorm_grad_bf16(args, stream: int) -> int:
 def hr_rmsnorm_grad_workspace(rows: int, hidden: int) -> int:
     """Bytes of workspace that a gradient call with dweight needs."""
     return load().hr_rmsnorm_grad_workspace(rows, hidden)
+
+
+def hr_router_topk(logits_ptr, dtype: int, tokens: int, experts: int, logits_stride: int, k: int, renormalize: int,
+                   weights_ptr, ids_ptr, stream: int) -> int:
+    """Raw call; returns the hr_status code."""
+    return load().hr_router_topk(logits_ptr, dtype, tokens, experts, logits_stride, k, renormalize, weights_ptr,
+                                 ids_ptr, stream)
+
+
+def hr_router_topk_grad(dweights_ptr, weights_ptr, ids_ptr, logits_ptr, dtype: int, tokens: int, experts: int,
+                        logits_stride: int, k: int, renormalize: int, dlogits_ptr, dlogits_stride: int,
+                        stream: int) -> int:
+    """Raw call; returns the hr_status code."""
+    return load().hr_router_topk_grad(dweights_ptr, weights_ptr, ids_ptr, logits_ptr, dtype, tokens, experts,
+                                      logits_stride, k, renormalize, dlogits_ptr, dlogits_stride, stream)
 
 
 def workspace(G: int, numel: int, dtype=None, device=0):
@@ -623,6 +644,60 @@ def rmsnorm_grad(dy, h, rstd, dx, *, weight=None, dresidual=None, dweight=None, 
     if st != HR_OK:
         raise HrError(st, name)
     return dx
+
+
+def _dtype_code(dtype, name: str) -> int:
+    """The hr_dtype of router logits."""
+    _tm()
+    if dtype is _torch.float32:
+        return HR_DTYPE_F32
+    if dtype is _F16:
+        return HR_DTYPE_F16
+    if dtype is _BF16:
+        return HR_DTYPE_BF16
+    raise TypeError(f"{name}: expected torch.float32, torch.float16 or torch.bfloat16, got {dtype}")
+
+
+def _picks(weights, ids, tokens: int):
+    """(addresses of weights and ids, k) of a token's picks."""
+    k = ids.shape[-1]
+    return (_flat_ptr(weights, "weights", _torch.float32, tokens * k),
+            _flat_ptr(ids, "ids", _torch.int32, tokens * k), k)
+
+
+def router_topk(logits, weights, ids, *, renormalize: bool = False, stream=None):
+    """The k largest logits of every token, by value downward and equal ones
+    by index upward, into ``ids`` (torch.int32, tokens x k), and their softmax
+    weights into ``weights`` (torch.float32); ``renormalize`` divides them by
+    their sum (hr_router_topk).  NaN and -inf logits are never picked: id -1,
+    weight 0 where nothing is left."""
+    code = _dtype_code(logits.dtype, "logits")
+    lp, tokens, experts, ls = _row_view(logits, "logits", logits.dtype)
+    wp, ip, k = _picks(weights, ids, tokens)
+    st = load().hr_router_topk(lp, code, tokens, experts, ls, k, 1 if renormalize else 0, wp, ip,
+                               _stream_handle(stream, logits))
+    if st != HR_OK:
+        raise HrError(st, "hr_router_topk")
+    return weights, ids
+
+
+def router_topk_grad(dweights, weights, ids, dlogits, *, logits=None, renormalize: bool = False, stream=None):
+    """The gradient of router_topk's weights with respect to the logits, into
+    ``dlogits`` (hr_router_topk_grad).  ``logits`` are needed unless
+    ``renormalize``; ``dlogits`` may be ``logits``."""
+    dt = dlogits.dtype
+    code = _dtype_code(dt, "dlogits")
+    dp, tokens, experts, ds = _row_view(dlogits, "dlogits", dt)
+    wp, ip, k = _picks(weights, ids, tokens)
+    gp = _flat_ptr(dweights, "dweights", _torch.float32, tokens * k)
+    lp = ls = 0
+    if logits is not None and not renormalize:
+        lp, _, _, ls = _row_view(logits, "logits", dt, tokens, experts)
+    st = load().hr_router_topk_grad(gp, wp, ip, lp, code, tokens, experts, ls, k, 1 if renormalize else 0, dp, ds,
+                                    _stream_handle(stream, dlogits))
+    if st != HR_OK:
+        raise HrError(st, "hr_router_topk_grad")
+    return dlogits
 
 
 class Channel:
