@@ -639,7 +639,9 @@ typedef struct {
  * Errors: HR_ERR_INVALID_ARG (G, hidden 0, group, eps, a null input, codes
  * without scales or scales without codes, nothing to write, a stride below the
  * row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (hidden above
- * HR_RMSNORM_MAX_HIDDEN, 2^31 rows or more), HR_ERR_HIP.
+ * HR_RMSNORM_MAX_HIDDEN, 2^31 rows or more, or more rows than a launch of
+ * 2^32 work-items takes: 2^22 of the longest, 2^28 of up to 128 values),
+ * HR_ERR_HIP.
  */
 HR_API hr_status hr_reduce_rmsnorm_f16(const hr_rmsnorm_args *args, hr_stream_t stream);
 HR_API hr_status hr_reduce_rmsnorm_bf16(const hr_rmsnorm_args *args, hr_stream_t stream);
@@ -681,7 +683,9 @@ HR_API hr_status hr_rmsnorm_grad_bf16(const hr_rmsnorm_grad_args *args, hr_strea
 /* Bytes of workspace that a gradient call with dweight needs (0: none). */
 HR_API size_t hr_rmsnorm_grad_workspace(size_t rows, size_t hidden);
 
-/* Largest number of logits per token and of picks. */
+/* Largest number of logits per token, of picks, and of tokens (64 lanes each
+ * in a launch of fewer than 2^32 work-items). */
+#define HR_ROUTER_MAX_TOKENS ((1u << 26) - 4)
 #define HR_ROUTER_MAX_EXPERTS 1024
 #define HR_ROUTER_MAX_K 32
 
@@ -704,8 +708,8 @@ HR_API size_t hr_rmsnorm_grad_workspace(size_t rows, size_t hidden);
  * weights, ids: tokens x k, contiguous.
  * Errors: HR_ERR_INVALID_ARG (k outside 1..experts, dtype, null pointers, a
  * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (experts
- * above HR_ROUTER_MAX_EXPERTS, k above HR_ROUTER_MAX_K, 2^31 tokens or more),
- * HR_ERR_HIP.
+ * above HR_ROUTER_MAX_EXPERTS, k above HR_ROUTER_MAX_K, tokens above
+ * HR_ROUTER_MAX_TOKENS), HR_ERR_HIP.
  */
 HR_API hr_status hr_router_topk(const void *logits, hr_dtype dtype, size_t tokens, int experts,
                                 size_t logits_stride, int k, int renormalize, float *weights, int32_t *ids,
@@ -730,6 +734,132 @@ HR_API hr_status hr_router_topk_grad(const float *dweights, const float *weights
                                      const void *logits, hr_dtype dtype, size_t tokens, int experts,
                                      size_t logits_stride, int k, int renormalize, void *dlogits,
                                      size_t dlogits_stride, hr_stream_t stream);
+
+/*
+ * Tokens by expert.  The picks of `tokens` tokens, k each, are slots
+ * s = token * k + j.  A sort lays the slots out by expert; rows are gathered
+ * into that order, the experts' products run over whole segments, and the
+ * combine adds every token's rows back with their weights.  A rank that holds
+ * experts first .. first + experts - 1 sorts only these, and its combined rows
+ * are its contribution to the all-reduce: hr_reduce_rmsnorm folds them.
+ */
+#define HR_EXPERTS_MAX 1024     /* experts of one sort */
+#define HR_EXPERTS_MAX_K 32     /* picks per token */
+
+/* Rows that sorted tokens take at most: tokens * k, and pad - 1 more for every
+ * segment that can hold a slot.  0 when an argument is out of range. */
+HR_API size_t hr_experts_rows(size_t tokens, int k, int experts, int pad);
+/* Bytes of workspace that a sort needs (0: none). */
+HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int experts);
+
+/*
+ * hr_experts_sort -- where every slot goes.
+ *
+ * Expert e's slots (ids == first + e) take rows offsets[e], offsets[e] + 1, ..
+ * in slot order; offsets[e + 1] is offsets[e] plus their number rounded up to
+ * a multiple of pad.  A slot whose id is none of this rank's experts (below
+ * first, above the last, -1 for no pick) goes nowhere.
+ *
+ * ids:     tokens x k.
+ * offsets: experts + 1 row numbers, the first 0.
+ * order:   rows entries: the slot of every sorted row, -1 in the padding and
+ *          past the last segment.
+ * rows:    at least hr_experts_rows(tokens, k, experts, pad).
+ * pos:     tokens x k: the row of every slot, or -1.
+ * workspace: hr_experts_sort_workspace bytes, 4-byte aligned; its contents
+ *          mean nothing between calls.
+ * The result is the same in every run.  tokens 0 writes offsets and order.
+ * Errors: HR_ERR_INVALID_ARG (k, experts or pad below 1, first below 0, rows
+ * or workspace too small, null pointers, overlap), HR_ERR_ALIGNMENT,
+ * HR_ERR_TOO_LARGE (experts above HR_EXPERTS_MAX, k above HR_EXPERTS_MAX_K,
+ * 2^31 slots or rows or more), HR_ERR_HIP.
+ */
+HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, int k, int first, int experts, int pad,
+                                 int32_t *offsets, int32_t *order, size_t rows, int32_t *pos, void *workspace,
+                                 size_t workspace_bytes, hr_stream_t stream);
+
+typedef struct {
+    const void *in;           /* tokens rows of row_bytes bytes, of any type      */
+    const float *scales;      /* tokens rows of scales_width scales; NULL = none  */
+    void *out;                /* rows rows                                        */
+    float *scales_out;        /* rows rows; with scales                           */
+    const int32_t *pos;       /* the sort's                                       */
+    const int32_t *order;     /* the sort's; NULL: padding rows are left alone    */
+    const int32_t *offsets;   /* the sort's; with order                           */
+    size_t tokens, rows;      /* rows: of out, and entries of order               */
+    size_t row_bytes, in_stride, out_stride;                /* bytes; 0 = row_bytes */
+    size_t scales_width, scales_stride, scales_out_stride;  /* scales; 0 = width  */
+    int k, experts;
+} hr_experts_gather_args;
+
+/*
+ * hr_experts_gather -- every token's row (and its scales) to its slots' rows:
+ * out[pos[t][j]] = in[t].  Padding rows inside the segments become zeros; rows
+ * past offsets[experts] are not written.  A pos outside 0..rows-1 goes nowhere.
+ * Its gradient is hr_experts_combine without weights.
+ * Errors: HR_ERR_INVALID_ARG (row_bytes 0, k outside 1..HR_EXPERTS_MAX_K,
+ * scales without scales_out or the reverse, order without offsets, null
+ * pointers, a stride below the row, overlap), HR_ERR_ALIGNMENT,
+ * HR_ERR_TOO_LARGE (2^31 slots, rows or row bytes or more; a launch of 2^32
+ * work-items or more, one per 16 bytes of the tokens' rows), HR_ERR_HIP.
+ */
+HR_API hr_status hr_experts_gather(const hr_experts_gather_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *z;            /* rows rows of hidden values                       */
+    const void *addend;       /* tokens rows; NULL = none                         */
+    void *out;                /* tokens rows                                      */
+    const int32_t *pos;       /* the sort's                                       */
+    const float *weights;     /* tokens x k; NULL = ones                          */
+    size_t tokens, rows, hidden;
+    size_t z_stride, addend_stride, out_stride;             /* values; 0 = hidden */
+    int k;
+} hr_experts_combine_args;
+
+/*
+ * hr_experts_combine_f16 / _bf16 -- every token's rows back, weighted:
+ *
+ *     out[t] = addend[t] + sum over j of weights[t][j] * z[pos[t][j]]
+ *
+ * summed in binary32 in that order and rounded once.  A pos outside 0..rows-1
+ * adds nothing (its row and weight are not used); a token without any row gets
+ * its addend, or zeros.  out may be exactly addend.
+ * Errors: HR_ERR_INVALID_ARG (hidden 0, k outside 1..HR_EXPERTS_MAX_K, null
+ * pointers, a stride below the row, overlap), HR_ERR_ALIGNMENT,
+ * HR_ERR_TOO_LARGE (2^31 slots or rows or more, rows of 2^27 values or more, a
+ * launch of 2^32 work-items or more, one per 8 values of out), HR_ERR_HIP.
+ */
+HR_API hr_status hr_experts_combine_f16(const hr_experts_combine_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_combine_bf16(const hr_experts_combine_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *dy;           /* gradient of the combine's out: tokens rows       */
+    const void *z;            /* the combine's; needed for dweights               */
+    void *dz;                 /* gradient of z: rows rows; NULL = not wanted      */
+    const int32_t *pos;
+    const float *weights;     /* NULL = ones                                      */
+    float *dweights;          /* tokens x k; NULL = not wanted                    */
+    const int32_t *order;     /* the sort's; NULL: padding rows are left alone    */
+    const int32_t *offsets;   /* the sort's; with order                           */
+    size_t tokens, rows, hidden;
+    size_t dy_stride, z_stride, dz_stride;                  /* values; 0 = hidden */
+    int k, experts;
+} hr_experts_combine_grad_args;
+
+/*
+ * hr_experts_combine_grad_f16 / _bf16 -- the combine's gradient:
+ *
+ *     dz[pos[t][j]]  = weights[t][j] * dy[t], rounded once
+ *     dweights[t][j] = sum over the row of dy[t] * z[pos[t][j]], in binary32
+ *
+ * dweights is 0 for a slot without a row.  Padding rows of dz become zeros;
+ * rows past offsets[experts] are not written.  (The addend's gradient is dy.)
+ * dz may be exactly z.
+ * Errors: as hr_experts_combine; HR_ERR_INVALID_ARG when neither dz nor
+ * dweights is wanted.
+ */
+HR_API hr_status hr_experts_combine_grad_f16(const hr_experts_combine_grad_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_combine_grad_bf16(const hr_experts_combine_grad_args *args, hr_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 HR_API const char *hr_status_str(hr_status s);

@@ -1,0 +1,800 @@
+// experts.hip -- tokens sorted by expert and back.
+//
+//   hr_experts_sort          where each (token, pick) goes: a stable counting
+//                            sort of the picks by expert
+//   hr_experts_gather        rows copied to their sorted places
+//   hr_experts_combine       y[t] = sum_j weights[t][j] * z[pos[t][j]] (+ addend)
+//   hr_experts_combine_grad  dz[pos[t][j]] = weights[t][j] * dy[t],
+//                            dweights[t][j] = <dy[t], z[pos[t][j]]>
+//
+// (The gradient of the gather is the combine without weights.)  Apart from
+// the sort, every kernel moves rows once and is bound by HBM: a workgroup (or
+// a part of it, for short rows) takes a token, so the token's own row is read
+// or written once and its k expert rows are all in flight together.
+#include "rows.h"
+
+namespace hr {
+
+constexpr int kExpertThreads = 256;
+constexpr int kMaxSortThreads = 1024;
+
+// ------------------------------------------------------------------ the sort
+
+struct SortArgs {
+    const int32_t *ids;
+    int32_t *offsets, *order, *pos;
+    int32_t *counts;         // [blocks][experts], then [experts]: totals
+    uint32_t slots, rows;
+    uint32_t chunk;          // slots per workgroup
+    int first, experts, pad;
+    int bits;                // of an expert's number, `experts` (none) included
+    int blocks;
+};
+
+// The expert of a slot, counted from `first`; `experts` for a slot that goes
+// nowhere.
+__device__ __forceinline__ int slot_expert(const SortArgs &a, uint32_t s) {
+    const uint32_t e = static_cast<uint32_t>(a.ids[s]) - static_cast<uint32_t>(a.first);
+    return a.ids[s] >= a.first && e < static_cast<uint32_t>(a.experts) ? static_cast<int>(e) : a.experts;
+}
+
+// Lanes of the wave that hold the same number.
+__device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
+    uint64_t mask = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (e >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        mask &= one ? ones : ~ones;
+    }
+    return mask;
+}
+
+// counts[w][e] = slots of expert e among wave w's share of [begin, end).
+__device__ __forceinline__ void count_share(const SortArgs &a, uint32_t begin, uint32_t end, int *counts) {
+    for (uint32_t s = begin + threadIdx.x % kWave; s < end; s += kWave) {
+        const int e = slot_expert(a, s);
+        if (e < a.experts) atomicAdd(&counts[e], 1);     // whole numbers: the order does not matter
+    }
+}
+
+// The share of a workgroup's slots [begin, end) that a wave takes, in order.
+__device__ __forceinline__ void wave_share(uint32_t begin, uint32_t end, int wave, int waves, uint32_t *b, uint32_t *e) {
+    const uint32_t per = ((end - begin + waves - 1) / waves + kWave - 1) / kWave * kWave;
+    *b = begin + wave * per < end ? begin + wave * per : end;
+    *e = *b + per < end ? *b + per : end;
+}
+
+// The wave's slots to their places: next[e] is the place of the next slot of
+// expert e in this wave's share.
+__device__ __forceinline__ void place_share(const SortArgs &a, uint32_t begin, uint32_t end, int *next) {
+    const uint32_t lane = threadIdx.x % kWave;
+    for (uint32_t s0 = begin; s0 < end; s0 += kWave) {
+        const uint32_t s = s0 + lane;
+        const int e = s < end ? slot_expert(a, s) : a.experts;
+        const uint64_t mask = same_lanes(e, a.bits);
+        const int rank = __builtin_popcountll(mask & ((1ull << lane) - 1));
+        int place = -1;
+        if (e < a.experts) place = next[e] + rank;
+        // every lane has read its expert's place before one of them moves it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (e < a.experts && rank == 0) next[e] = place + __builtin_popcountll(mask);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (s < end) {
+            a.pos[s] = place;
+            if (place >= 0) a.order[place] = static_cast<int32_t>(s);
+        }
+    }
+}
+
+// Inclusive sums of v over the workgroup's threads, through `tmp` (a value per
+// thread); every thread of the workgroup calls it.
+__device__ __forceinline__ int scan_threads(int v, int *tmp) {
+    const int t = threadIdx.x, n = blockDim.x;
+    tmp[t] = v;
+    __syncthreads();
+    for (int d = 1; d < n; d *= 2) {
+        const int before = t >= d ? tmp[t - d] : 0;
+        __syncthreads();
+        tmp[t] += before;
+        __syncthreads();
+    }
+    return tmp[t];
+}
+
+__device__ __forceinline__ int padded(int count, int pad) { return (count + pad - 1) / pad * pad; }
+
+// order = -1 in the segments' padding, from their counts, and past the last
+// segment; the experts and the tail are dealt out to the workgroups.
+__device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offsets, const int *counts) {
+    if (a.pad > 1) {
+        const int waves = blockDim.x / kWave;
+        for (int e = blockIdx.x * waves + threadIdx.x / kWave; e < a.experts; e += gridDim.x * waves)
+            for (int p = offsets[e] + counts[e] + threadIdx.x % kWave; p < offsets[e + 1]; p += kWave) a.order[p] = -1;
+    }
+    for (size_t p = static_cast<size_t>(offsets[a.experts]) + blockIdx.x * blockDim.x + threadIdx.x; p < a.rows;
+         p += static_cast<size_t>(gridDim.x) * blockDim.x)
+        a.order[p] = -1;
+}
+
+// Everything in one workgroup.  Dynamic LDS: [waves][experts] counts, then
+// [experts + 1] offsets, [experts] totals and [threads] for the scan.
+__global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
+    extern __shared__ int lds[];
+    const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave;
+    int *counts = lds, *offsets = counts + waves * a.experts, *totals = offsets + a.experts + 1,
+        *tmp = totals + a.experts;
+    for (int i = threadIdx.x; i < waves * a.experts; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    uint32_t b, e;
+    wave_share(0, a.slots, wave, waves, &b, &e);
+    count_share(a, b, e, counts + wave * a.experts);
+    __syncthreads();
+    for (int e0 = 0, base = 0; e0 < a.experts; e0 += blockDim.x) {
+        const int x = e0 + threadIdx.x;
+        int sum = 0;
+        if (x < a.experts)
+            for (int w = 0; w < waves; ++w) sum += counts[w * a.experts + x];
+        const int end = base + scan_threads(padded(sum, a.pad), tmp);
+        if (x < a.experts) {
+            int at = end - padded(sum, a.pad);
+            totals[x] = sum;
+            offsets[x] = at;
+            offsets[x + 1] = end;      // the same value as its neighbour's own
+            for (int w = 0; w < waves; ++w) {
+                const int n = counts[w * a.experts + x];
+                counts[w * a.experts + x] = at;
+                at += n;
+            }
+        }
+        base += tmp[blockDim.x - 1];
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) a.offsets[i] = offsets[i];
+    place_share(a, b, e, counts + wave * a.experts);
+    fill_padding(a, offsets, totals);
+}
+
+// The same over many workgroups, in three kernels.  Dynamic LDS: [experts].
+__global__ __launch_bounds__(kMaxSortThreads) void sort_count(SortArgs a) {
+    extern __shared__ int lds[];
+    for (int i = threadIdx.x; i < a.experts; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+    const uint32_t begin = blockIdx.x * a.chunk;
+    const uint32_t end = begin + a.chunk < a.slots ? begin + a.chunk : a.slots;
+    for (uint32_t s = begin + threadIdx.x; s < end; s += blockDim.x) {
+        const int e = slot_expert(a, s);
+        if (e < a.experts) atomicAdd(&lds[e], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.experts; i += blockDim.x) a.counts[blockIdx.x * a.experts + i] = lds[i];
+}
+
+// One workgroup: counts[b][e] become the place of workgroup b's first slot of
+// expert e, counts[blocks][e] the totals.  A thread takes one expert and one
+// of `parts` runs of workgroups.
+__global__ __launch_bounds__(kMaxSortThreads) void sort_scan(SortArgs a) {
+    __shared__ int sums[kMaxSortThreads], tmp[kMaxSortThreads], starts[kMaxSortThreads];
+    int wide = 1;
+    while (wide < a.experts || wide < 16) wide *= 2;
+    const int x = threadIdx.x % wide, part = threadIdx.x / wide, parts = kMaxSortThreads / wide;
+    const int per = (a.blocks + parts - 1) / parts;
+    const int b0 = part * per < a.blocks ? part * per : a.blocks, b1 = b0 + per < a.blocks ? b0 + per : a.blocks;
+    int sum = 0;
+    if (x < a.experts)
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += a.counts[b * a.experts + x];
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    int total = 0, before = 0;
+    for (int p = 0; p < parts; ++p) {
+        before = p == part ? total : before;
+        total += sums[p * wide + x];
+    }
+    const bool first = part == 0 && x < a.experts;
+    const int size = padded(total, a.pad);
+    const int end = scan_threads(first ? size : 0, tmp);
+    if (first) {
+        starts[x] = end - size;
+        a.offsets[x] = end - size;
+        if (x == a.experts - 1) a.offsets[a.experts] = end;
+        a.counts[a.blocks * a.experts + x] = total;
+    }
+    __syncthreads();
+    if (x < a.experts) {
+        int at = starts[x] + before;
+        for (int b = b0; b < b1; ++b) {
+            const int n = a.counts[b * a.experts + x];
+            a.counts[b * a.experts + x] = at;
+            at += n;
+        }
+    }
+}
+
+// Dynamic LDS: [waves][experts].
+__global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
+    extern __shared__ int lds[];
+    const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave;
+    for (int i = threadIdx.x; i < waves * a.experts; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+    const uint32_t begin = blockIdx.x * a.chunk;
+    const uint32_t end = begin + a.chunk < a.slots ? begin + a.chunk : a.slots;
+    uint32_t b, e;
+    wave_share(begin, end, wave, waves, &b, &e);
+    count_share(a, b, e, lds + wave * a.experts);
+    __syncthreads();
+    for (int x = threadIdx.x; x < a.experts; x += blockDim.x) {
+        int at = a.counts[blockIdx.x * a.experts + x];
+        for (int w = 0; w < waves; ++w) {
+            const int n = lds[w * a.experts + x];
+            lds[w * a.experts + x] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    place_share(a, b, e, lds + wave * a.experts);
+    fill_padding(a, a.offsets, a.counts + static_cast<size_t>(a.blocks) * a.experts);
+}
+
+// --------------------------------------------------------------------- rows
+
+// Picks of a token whose rows are in flight together.
+constexpr int kPicks = 8;
+
+// Rows of a sorted buffer that stand for no slot, set to zero: sorted rows
+// [r0, r0 + kPadRows) of a workgroup of kExpertThreads.
+constexpr int kPadRows = 8;
+
+struct Padding {
+    const int32_t *order, *offsets;
+    uint32_t rows;
+    int experts;
+};
+
+__device__ __forceinline__ void zero_row(char *row, size_t bytes) {
+    const size_t whole = bytes / 16;
+    for (size_t i = threadIdx.x; i < whole; i += kExpertThreads)
+        *reinterpret_cast<u32x4_byte *>(row + 16 * i) = u32x4{0, 0, 0, 0};
+    for (size_t i = 16 * whole + threadIdx.x; i < bytes; i += kExpertThreads) row[i] = 0;
+}
+
+template <class F>
+__device__ __forceinline__ void for_padding(const Padding &q, uint32_t r0, F f) {
+    const uint32_t used = static_cast<uint32_t>(q.offsets[q.experts]);
+    const uint32_t end = used < q.rows ? used : q.rows;
+    for (uint32_t p = r0; p < r0 + kPadRows && p < end; ++p)
+        if (q.order[p] < 0) f(p);
+}
+
+struct GatherArgs {
+    const char *in, *scales;
+    char *out, *scales_out;
+    const int32_t *pos;
+    size_t row_bytes, in_stride, out_stride;                 // bytes
+    size_t scale_bytes, scales_stride, scales_out_stride;
+    Padding pad;
+    uint32_t tokens, rows;
+    uint32_t pad_groups;     // leading workgroups, for the padding
+    uint32_t splits;         // workgroups that share a token's row
+    uint32_t units, scale_units;
+    int k;
+};
+
+// A 16-byte unit of a row.  The last unit of a row that is not a whole number
+// of them starts 16 bytes before the row's end: the bytes that it shares with
+// its neighbour are written twice, with the same value.
+__device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
+    const size_t o = 16 * static_cast<size_t>(i);
+    return o + 16 <= bytes ? o : bytes - 16;
+}
+
+// L lanes per token (L = kExpertThreads: its units are also split over
+// workgroups), one unit per lane and step.
+template <int L>
+__global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
+    if (blockIdx.x < a.pad_groups) {
+        for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
+            zero_row(a.out + p * a.out_stride, a.row_bytes);
+            if (a.scales_out != nullptr) zero_row(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
+        });
+        return;
+    }
+    const uint32_t group = blockIdx.x - a.pad_groups;
+    constexpr uint32_t kTokens = kExpertThreads / L;
+    const uint32_t t = L == kExpertThreads ? group / a.splits : group * kTokens + threadIdx.x / L;
+    const uint32_t split = L == kExpertThreads ? group % a.splits : 0;
+    if (t >= a.tokens) return;
+    const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
+    const uint32_t units = a.units + a.scale_units;
+    const uint32_t step = L == kExpertThreads ? kExpertThreads * a.splits : L;
+    for (uint32_t i = split * kExpertThreads + threadIdx.x % L; i < units; i += step) {
+        const bool data = i < a.units;
+        const size_t bytes = data ? a.row_bytes : a.scale_bytes;
+        const char *src = data ? a.in + t * a.in_stride : a.scales + t * a.scales_stride;
+        char *dst = data ? a.out : a.scales_out;
+        const size_t stride = data ? a.out_stride : a.scales_out_stride;
+        const uint32_t u = data ? i : i - a.units;
+        // the places first: they lie in memory that the stores could be thought
+        // to change, and would be waited for one by one
+        for (int j0 = 0; j0 < a.k; j0 += kPicks) {
+            uint32_t p[kPicks];
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) p[j] = j0 + j < a.k ? static_cast<uint32_t>(pos[j0 + j]) : ~0u;
+            if (bytes >= 16) {
+                const size_t o = unit_at(u, bytes);
+                const u32x4 v = *reinterpret_cast<const u32x4_byte *>(src + o);
+#pragma unroll
+                for (int j = 0; j < kPicks; ++j)
+                    if (p[j] < a.rows) *reinterpret_cast<u32x4_byte *>(dst + p[j] * stride + o) = v;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPicks; ++j)
+                    if (p[j] < a.rows)
+                        for (size_t o = 0; o < bytes; ++o) dst[p[j] * stride + o] = src[o];
+            }
+        }
+    }
+}
+
+struct CombineArgs {
+    const uint16_t *z, *addend;
+    uint16_t *out;
+    const int32_t *pos;
+    const float *weights;
+    size_t z_stride, addend_stride, out_stride;              // values
+    uint32_t tokens, rows;
+    uint32_t splits;
+    int k, hidden;
+};
+
+// The sum is binary32 and runs in pick order, the addend first; one rounding.
+template <class E, int L, bool TAIL>
+__global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
+    constexpr uint32_t kTokens = kExpertThreads / L;
+    const uint32_t t = L == kExpertThreads ? blockIdx.x / a.splits : blockIdx.x * kTokens + threadIdx.x / L;
+    const uint32_t split = L == kExpertThreads ? blockIdx.x % a.splits : 0;
+    if (t >= a.tokens) return;
+    const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
+    const float *weights = a.weights != nullptr ? a.weights + static_cast<size_t>(t) * a.k : nullptr;
+    const int units = (a.hidden + 7) / 8;
+    const int step = L == kExpertThreads ? static_cast<int>(kExpertThreads * a.splits) : L;
+    for (int i = static_cast<int>(split * kExpertThreads + threadIdx.x % L); i < units; i += step) {
+        float sum[8];
+        if (a.addend != nullptr) {
+            Wide<E>::widen(load_unit<TAIL>(a.addend + t * a.addend_stride, i, a.hidden), sum);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+        }
+        for (int j0 = 0; j0 < a.k; j0 += kPicks) {
+            u32x4 z[kPicks];
+            float w[kPicks];
+            bool there[kPicks];
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) {
+                there[j] = false;
+                if (j0 + j < a.k) {
+                    const uint32_t p = static_cast<uint32_t>(pos[j0 + j]);
+                    there[j] = p < a.rows;
+                    if (there[j]) {
+                        z[j] = load_unit<TAIL>(a.z + p * a.z_stride, i, a.hidden);
+                        w[j] = weights != nullptr ? weights[j0 + j] : 1.0f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) {
+                if (there[j]) {
+                    float f[8];
+                    Wide<E>::widen(z[j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[j], f[e], sum[e]);
+                }
+            }
+        }
+        store_unit<TAIL>(a.out + t * a.out_stride, i, a.hidden, Wide<E>::narrow(sum));
+    }
+}
+
+struct CombineGradArgs {
+    const uint16_t *dy, *z;
+    uint16_t *dz;
+    const int32_t *pos;
+    const float *weights;
+    float *dweights;
+    size_t dy_stride, z_stride, dz_stride;                   // values
+    Padding pad;
+    uint32_t tokens, rows;
+    uint32_t pad_groups;
+    int k, hidden;
+};
+
+// L lanes per token over all of its row, since the weights' gradients are sums
+// over it; kPicks of them at a time in registers.
+template <class E, int L, bool TAIL>
+__global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
+    __shared__ float sums[kExpertThreads / kWave][kPicks];
+    if (blockIdx.x < a.pad_groups) {
+        for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
+            zero_row(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
+        });
+        return;
+    }
+    constexpr uint32_t kTokens = kExpertThreads / L;
+    const uint32_t group = blockIdx.x - a.pad_groups;
+    const uint32_t t = group * kTokens + (L == kExpertThreads ? 0 : threadIdx.x / L);
+    const int lane = static_cast<int>(threadIdx.x) % L;
+    const bool here = t < a.tokens;
+    const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
+    const int units = here ? (a.hidden + 7) / 8 : 0;
+    for (int j0 = 0; j0 < a.k; j0 += kPicks) {
+        uint32_t p[kPicks];
+        float w[kPicks], dot[kPicks];
+#pragma unroll
+        for (int j = 0; j < kPicks; ++j) {
+            p[j] = ~0u;
+            w[j] = 1.0f;
+            dot[j] = 0.0f;
+            if (here && j0 + j < a.k) {
+                p[j] = static_cast<uint32_t>(pos[j0 + j]);
+                if (a.weights != nullptr) w[j] = a.weights[static_cast<size_t>(t) * a.k + j0 + j];
+            }
+        }
+        for (int i = lane; i < units; i += L) {
+            float d[8];
+            u32x4 z[kPicks];
+            Wide<E>::widen(load_unit<TAIL>(a.dy + t * a.dy_stride, i, a.hidden), d);
+            if (a.dweights != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kPicks; ++j)
+                    if (p[j] < a.rows) z[j] = load_unit<TAIL>(a.z + p[j] * a.z_stride, i, a.hidden);
+            }
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) {
+                if (p[j] < a.rows) {
+                    float f[8];
+                    if (a.dweights != nullptr) {
+                        Wide<E>::widen(z[j], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                    }
+                    if (a.dz != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = d[e] * w[j];
+                        store_unit<TAIL>(a.dz + p[j] * a.dz_stride, i, a.hidden, Wide<E>::narrow(f));
+                    }
+                }
+            }
+        }
+        if (a.dweights == nullptr) continue;
+        if constexpr (L <= kWave) {
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) {
+                dot[j] = sum_lanes<L>(dot[j]);
+                if (here && lane == j && j0 + j < a.k) a.dweights[static_cast<size_t>(t) * a.k + j0 + j] = dot[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPicks; ++j) {
+                dot[j] = sum_lanes<kWave>(dot[j]);
+                if (threadIdx.x % kWave == 0) sums[threadIdx.x / kWave][j] = dot[j];
+            }
+            __syncthreads();
+            if (here && threadIdx.x < kPicks && j0 + static_cast<int>(threadIdx.x) < a.k) {
+                float s = sums[0][threadIdx.x];
+#pragma unroll
+                for (int v = 1; v < kExpertThreads / kWave; ++v) s += sums[v][threadIdx.x];
+                a.dweights[static_cast<size_t>(t) * a.k + j0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+namespace {
+
+constexpr size_t kMaxCount = 0x7FFFFFFF;
+// A launch has fewer than 2^32 work-items.
+constexpr size_t kMaxGroups = 0xFFFFFFFFu / kExpertThreads;
+// Up to this many slots one workgroup sorts by itself.
+constexpr size_t kSortOnce = 8192;
+constexpr size_t kSortBlocks = 256;
+constexpr size_t kSortChunk = 2048;
+
+uint32_t sort_chunk(size_t slots) {
+    const size_t c = (slots + kSortBlocks - 1) / kSortBlocks;
+    return static_cast<uint32_t>(c < kSortChunk ? kSortChunk : (c + kWave - 1) / kWave * kWave);
+}
+
+bool picks_ok(size_t tokens, int k, size_t *slots) {
+    return k >= 1 && !__builtin_mul_overflow(tokens, static_cast<size_t>(k), slots);
+}
+
+// Lanes that a row of `units` 16-byte units keeps busy.
+int lanes_for(size_t units) { return units <= 16 ? 16 : units <= 64 ? 64 : kExpertThreads; }
+
+template <class K16, class K64, class K256, class A>
+hipError_t launch_lanes(int lanes, unsigned grid, hipStream_t s, K16 k16, K64 k64, K256 k256, const A &a) {
+    if (lanes == 16)
+        hipLaunchKernelGGL(k16, dim3(grid), dim3(kExpertThreads), 0, s, a);
+    else if (lanes == 64)
+        hipLaunchKernelGGL(k64, dim3(grid), dim3(kExpertThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL(k256, dim3(grid), dim3(kExpertThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// Workgroups of the padding: none where the sorted buffer has no room for any
+// (a sort with padding takes a buffer larger than its slots).
+uint32_t padding_groups(const Padding &q, size_t slots) {
+    return q.order != nullptr && q.rows > slots ? (q.rows + kPadRows - 1) / kPadRows : 0;
+}
+
+template <class E>
+hr_status combine_impl(const hr_experts_combine_args *q, hr_stream_t stream) {
+    size_t slots = 0;
+    if (q == nullptr || q->hidden == 0 || q->k > HR_EXPERTS_MAX_K || !picks_ok(q->tokens, q->k, &slots))
+        return HR_ERR_INVALID_ARG;
+    if (slots > kMaxCount || q->rows > kMaxCount || q->hidden > kMaxCount / 16) return HR_ERR_TOO_LARGE;
+    if (q->tokens == 0) return HR_OK;
+    if (q->pos == nullptr || q->out == nullptr || (q->z == nullptr && q->rows > 0)) return HR_ERR_INVALID_ARG;
+    CombineArgs a{};
+    a.z_stride = q->z_stride;
+    a.addend_stride = q->addend_stride;
+    a.out_stride = q->out_stride;
+    if (!row_stride(q->rows, q->hidden, &a.z_stride, 2) || !row_stride(q->tokens, q->hidden, &a.addend_stride, 2) ||
+        !row_stride(q->tokens, q->hidden, &a.out_stride, 2))
+        return HR_ERR_INVALID_ARG;
+    if (!aligned(q->z, 2) || !aligned(q->addend, 2) || !aligned(q->out, 2) || !aligned(q->pos, 4) ||
+        !aligned(q->weights, 4))
+        return HR_ERR_ALIGNMENT;
+    const size_t width = q->hidden * 2, per = static_cast<size_t>(q->k) * 4;
+    const Region out = {q->out, q->tokens, width, a.out_stride * 2};
+    const Region addend = {q->addend, q->tokens, width, a.addend_stride * 2};
+    if (regions_overlap(out, {q->z, q->rows, width, a.z_stride * 2}) ||
+        regions_overlap(out, {q->pos, q->tokens, per, per}) || regions_overlap(out, {q->weights, q->tokens, per, per}) ||
+        (regions_overlap(out, addend) && !regions_same(out, addend)))
+        return HR_ERR_INVALID_ARG;
+    a.z = static_cast<const uint16_t *>(q->z);
+    a.addend = static_cast<const uint16_t *>(q->addend);
+    a.out = static_cast<uint16_t *>(q->out);
+    a.pos = q->pos;
+    a.weights = q->weights;
+    a.tokens = static_cast<uint32_t>(q->tokens);
+    a.rows = static_cast<uint32_t>(q->rows);
+    a.k = q->k;
+    a.hidden = static_cast<int>(q->hidden);
+    const size_t units = (q->hidden + 7) / 8;
+    const int lanes = lanes_for(units);
+    a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + kExpertThreads - 1) / kExpertThreads) : 1;
+    const size_t grid = lanes == kExpertThreads ? q->tokens * a.splits
+                                                : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
+    if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const unsigned g = static_cast<unsigned>(grid);
+    const hipError_t e = q->hidden % 8 != 0
+                             ? launch_lanes(lanes, g, s, combine_rows<E, 16, true>, combine_rows<E, 64, true>,
+                                            combine_rows<E, kExpertThreads, true>, a)
+                             : launch_lanes(lanes, g, s, combine_rows<E, 16, false>, combine_rows<E, 64, false>,
+                                            combine_rows<E, kExpertThreads, false>, a);
+    return e == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+template <class E>
+hr_status combine_grad_impl(const hr_experts_combine_grad_args *q, hr_stream_t stream) {
+    size_t slots = 0;
+    if (q == nullptr || q->hidden == 0 || q->k > HR_EXPERTS_MAX_K || !picks_ok(q->tokens, q->k, &slots))
+        return HR_ERR_INVALID_ARG;
+    if (q->dz == nullptr && q->dweights == nullptr) return q->tokens == 0 ? HR_OK : HR_ERR_INVALID_ARG;
+    if (slots > kMaxCount || q->rows > kMaxCount || q->hidden > kMaxCount / 16) return HR_ERR_TOO_LARGE;
+    if (q->order != nullptr && (q->offsets == nullptr || q->experts < 1)) return HR_ERR_INVALID_ARG;
+    if (q->tokens == 0) return HR_OK;
+    if (q->pos == nullptr || q->dy == nullptr) return HR_ERR_INVALID_ARG;
+    if (q->dweights != nullptr && q->z == nullptr && q->rows > 0) return HR_ERR_INVALID_ARG;
+    CombineGradArgs a{};
+    a.dy_stride = q->dy_stride;
+    a.z_stride = q->z_stride;
+    a.dz_stride = q->dz_stride;
+    if (!row_stride(q->tokens, q->hidden, &a.dy_stride, 2) || !row_stride(q->rows, q->hidden, &a.z_stride, 2) ||
+        !row_stride(q->rows, q->hidden, &a.dz_stride, 2))
+        return HR_ERR_INVALID_ARG;
+    if (!aligned(q->dy, 2) || !aligned(q->z, 2) || !aligned(q->dz, 2) || !aligned(q->pos, 4) ||
+        !aligned(q->weights, 4) || !aligned(q->dweights, 4) || !aligned(q->order, 4) || !aligned(q->offsets, 4))
+        return HR_ERR_ALIGNMENT;
+    const size_t width = q->hidden * 2, per = static_cast<size_t>(q->k) * 4;
+    const Region dz = {q->dz, q->rows, width, a.dz_stride * 2}, dw = {q->dweights, q->tokens, per, per};
+    const Region z = {q->dweights != nullptr ? q->z : nullptr, q->rows, width, a.z_stride * 2};
+    const Region ins[] = {{q->dy, q->tokens, width, a.dy_stride * 2},
+                          {q->pos, q->tokens, per, per},
+                          {q->weights, q->tokens, per, per},
+                          {q->order, 1, q->rows * 4, 0},
+                          {q->offsets, 1, (static_cast<size_t>(q->experts > 0 ? q->experts : 0) + 1) * 4, 0}};
+    for (const Region &r : ins)
+        if (regions_overlap(dz, r) || regions_overlap(dw, r)) return HR_ERR_INVALID_ARG;
+    if (regions_overlap(dz, dw) || regions_overlap(dw, z) || (regions_overlap(dz, z) && !regions_same(dz, z)))
+        return HR_ERR_INVALID_ARG;
+    a.dy = static_cast<const uint16_t *>(q->dy);
+    a.z = static_cast<const uint16_t *>(q->z);
+    a.dz = static_cast<uint16_t *>(q->dz);
+    a.pos = q->pos;
+    a.weights = q->weights;
+    a.dweights = q->dweights;
+    a.pad = Padding{q->dz != nullptr ? q->order : nullptr, q->offsets, static_cast<uint32_t>(q->rows), q->experts};
+    a.tokens = static_cast<uint32_t>(q->tokens);
+    a.rows = static_cast<uint32_t>(q->rows);
+    a.k = q->k;
+    a.hidden = static_cast<int>(q->hidden);
+    a.pad_groups = padding_groups(a.pad, slots);
+    const int lanes = lanes_for((q->hidden + 7) / 8);
+    const size_t grid = a.pad_groups + (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
+    if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const unsigned g = static_cast<unsigned>(grid);
+    const hipError_t e = q->hidden % 8 != 0
+                             ? launch_lanes(lanes, g, s, combine_grad_rows<E, 16, true>, combine_grad_rows<E, 64, true>,
+                                            combine_grad_rows<E, kExpertThreads, true>, a)
+                             : launch_lanes(lanes, g, s, combine_grad_rows<E, 16, false>,
+                                            combine_grad_rows<E, 64, false>,
+                                            combine_grad_rows<E, kExpertThreads, false>, a);
+    return e == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+}  // namespace
+
+}  // namespace hr
+
+using namespace hr;
+
+extern "C" HR_API size_t hr_experts_rows(size_t tokens, int k, int experts, int pad) {
+    size_t slots = 0, extra = 0, rows = 0;
+    if (!picks_ok(tokens, k, &slots) || experts < 1 || pad < 1) return 0;
+    const size_t segments = static_cast<size_t>(experts) < slots ? static_cast<size_t>(experts) : slots;
+    if (__builtin_mul_overflow(segments, static_cast<size_t>(pad - 1), &extra) ||
+        __builtin_add_overflow(slots, extra, &rows))
+        return 0;
+    return rows;
+}
+
+extern "C" HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int experts) {
+    size_t slots = 0;
+    if (!picks_ok(tokens, k, &slots) || experts < 1 || experts > HR_EXPERTS_MAX || slots > kMaxCount) return 0;
+    if (slots <= kSortOnce) return 0;
+    const size_t chunk = sort_chunk(slots);
+    return ((slots + chunk - 1) / chunk + 1) * static_cast<size_t>(experts) * 4;
+}
+
+extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, int k, int first, int experts, int pad,
+                                            int32_t *offsets, int32_t *order, size_t rows, int32_t *pos,
+                                            void *workspace, size_t workspace_bytes, hr_stream_t stream) {
+    size_t slots = 0;
+    if (!picks_ok(tokens, k, &slots) || first < 0 || experts < 1 || pad < 1) return HR_ERR_INVALID_ARG;
+    if (experts > HR_EXPERTS_MAX || k > HR_EXPERTS_MAX_K || slots > kMaxCount || rows > kMaxCount)
+        return HR_ERR_TOO_LARGE;
+    const size_t most = hr_experts_rows(tokens, k, experts, pad);
+    if (rows < most || (most == 0 && slots > 0)) return HR_ERR_INVALID_ARG;
+    if (offsets == nullptr || (rows > 0 && order == nullptr) || (slots > 0 && (ids == nullptr || pos == nullptr)))
+        return HR_ERR_INVALID_ARG;
+    const size_t need = hr_experts_sort_workspace(tokens, k, experts);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return HR_ERR_INVALID_ARG;
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(pos, 4) || !aligned(workspace, 4))
+        return HR_ERR_ALIGNMENT;
+    const Region all[] = {{ids, 1, slots * 4, 0},
+                          {offsets, 1, (static_cast<size_t>(experts) + 1) * 4, 0},
+                          {order, 1, rows * 4, 0},
+                          {pos, 1, slots * 4, 0},
+                          {workspace, 1, need, 0}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (regions_overlap(all[i], all[j])) return HR_ERR_INVALID_ARG;
+
+    SortArgs a{};
+    a.ids = ids;
+    a.offsets = offsets;
+    a.order = order;
+    a.pos = pos;
+    a.counts = static_cast<int32_t *>(workspace);
+    a.slots = static_cast<uint32_t>(slots);
+    a.rows = static_cast<uint32_t>(rows);
+    a.first = first;
+    a.experts = experts;
+    a.pad = pad;
+    while ((1 << a.bits) <= experts) ++a.bits;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    // 16 waves' counts of up to 512 experts, or 8 waves' of up to 1024
+    const int threads = experts <= 512 ? 1024 : 512;
+    const size_t counts = static_cast<size_t>(threads / kWave) * experts * 4;
+    if (slots <= kSortOnce) {
+        const size_t lds = counts + (2 * static_cast<size_t>(experts) + 1 + threads) * 4;
+        hipLaunchKernelGGL(sort_once, dim3(1), dim3(threads), lds, s, a);
+        return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
+    }
+    a.chunk = sort_chunk(slots);
+    a.blocks = static_cast<int>((slots + a.chunk - 1) / a.chunk);
+    hipLaunchKernelGGL(sort_count, dim3(a.blocks), dim3(kMaxSortThreads), static_cast<size_t>(experts) * 4, s, a);
+    if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
+    hipLaunchKernelGGL(sort_scan, dim3(1), dim3(kMaxSortThreads), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
+    hipLaunchKernelGGL(sort_place, dim3(a.blocks), dim3(threads), counts, s, a);
+    return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+extern "C" HR_API hr_status hr_experts_gather(const hr_experts_gather_args *q, hr_stream_t stream) {
+    size_t slots = 0;
+    if (q == nullptr || q->row_bytes == 0 || q->k > HR_EXPERTS_MAX_K || !picks_ok(q->tokens, q->k, &slots))
+        return HR_ERR_INVALID_ARG;
+    if (slots > kMaxCount || q->rows > kMaxCount || q->row_bytes > kMaxCount || q->scales_width > kMaxCount / 4)
+        return HR_ERR_TOO_LARGE;
+    if ((q->scales == nullptr) != (q->scales_out == nullptr) && q->tokens > 0 && q->rows > 0) return HR_ERR_INVALID_ARG;
+    if (q->scales != nullptr && q->scales_width == 0) return HR_ERR_INVALID_ARG;
+    if (q->order != nullptr && (q->offsets == nullptr || q->experts < 1)) return HR_ERR_INVALID_ARG;
+    if (q->tokens == 0 || q->rows == 0) return HR_OK;
+    if (q->in == nullptr || q->out == nullptr || q->pos == nullptr) return HR_ERR_INVALID_ARG;
+    GatherArgs a{};
+    a.in_stride = q->in_stride;
+    a.out_stride = q->out_stride;
+    size_t ss = q->scales_stride, so = q->scales_out_stride;
+    if (!row_stride(q->tokens, q->row_bytes, &a.in_stride, 1) || !row_stride(q->rows, q->row_bytes, &a.out_stride, 1) ||
+        !row_stride(q->tokens, q->scales_width, &ss, 4) || !row_stride(q->rows, q->scales_width, &so, 4))
+        return HR_ERR_INVALID_ARG;
+    if (!aligned(q->pos, 4) || !aligned(q->scales, 4) || !aligned(q->scales_out, 4) || !aligned(q->order, 4) ||
+        !aligned(q->offsets, 4))
+        return HR_ERR_ALIGNMENT;
+    const size_t per = static_cast<size_t>(q->k) * 4;
+    const Region out = {q->out, q->rows, q->row_bytes, a.out_stride};
+    const Region sout = {q->scales_out, q->rows, q->scales_width * 4, so * 4};
+    const Region ins[] = {{q->in, q->tokens, q->row_bytes, a.in_stride},
+                          {q->scales, q->tokens, q->scales_width * 4, ss * 4},
+                          {q->pos, q->tokens, per, per},
+                          {q->order, 1, q->rows * 4, 0},
+                          {q->offsets, 1, (static_cast<size_t>(q->experts > 0 ? q->experts : 0) + 1) * 4, 0}};
+    for (const Region &r : ins)
+        if (regions_overlap(out, r) || regions_overlap(sout, r)) return HR_ERR_INVALID_ARG;
+    if (regions_overlap(out, sout)) return HR_ERR_INVALID_ARG;
+
+    a.in = static_cast<const char *>(q->in);
+    a.out = static_cast<char *>(q->out);
+    a.pos = q->pos;
+    a.row_bytes = q->row_bytes;
+    a.units = static_cast<uint32_t>((q->row_bytes + 15) / 16);
+    if (q->scales != nullptr) {
+        a.scales = reinterpret_cast<const char *>(q->scales);
+        a.scales_out = reinterpret_cast<char *>(q->scales_out);
+        a.scale_bytes = q->scales_width * 4;
+        a.scales_stride = ss * 4;
+        a.scales_out_stride = so * 4;
+        a.scale_units = static_cast<uint32_t>((a.scale_bytes + 15) / 16);
+    }
+    a.pad = Padding{q->order, q->offsets, static_cast<uint32_t>(q->rows), q->experts};
+    a.tokens = static_cast<uint32_t>(q->tokens);
+    a.rows = static_cast<uint32_t>(q->rows);
+    a.k = q->k;
+    a.pad_groups = padding_groups(a.pad, slots);
+    const size_t units = static_cast<size_t>(a.units) + a.scale_units;
+    const int lanes = lanes_for(units);
+    a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + kExpertThreads - 1) / kExpertThreads) : 1;
+    const size_t grid =
+        a.pad_groups + (lanes == kExpertThreads ? q->tokens * a.splits
+                                                : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes));
+    if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
+    const hipError_t e = launch_lanes(lanes, static_cast<unsigned>(grid), reinterpret_cast<hipStream_t>(stream),
+                                      gather_rows<16>, gather_rows<64>, gather_rows<kExpertThreads>, a);
+    return e == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+extern "C" HR_API hr_status hr_experts_combine_f16(const hr_experts_combine_args *args, hr_stream_t stream) {
+    return combine_impl<F16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_experts_combine_bf16(const hr_experts_combine_args *args, hr_stream_t stream) {
+    return combine_impl<BF16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_experts_combine_grad_f16(const hr_experts_combine_grad_args *args, hr_stream_t stream) {
+    return combine_grad_impl<F16>(args, stream);
+}
+
+extern "C" HR_API hr_status hr_experts_combine_grad_bf16(const hr_experts_combine_grad_args *args,
+                                                         hr_stream_t stream) {
+    return combine_grad_impl<BF16>(args, stream);
+}

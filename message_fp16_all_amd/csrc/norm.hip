@@ -452,13 +452,16 @@ struct NormGradKernel {
 
 constexpr size_t kMaxRows = 0x7FFFFFFF;
 
+size_t groups_of(size_t rows, const RowShape &s) {
+    const size_t per = s.lanes > 0 ? s.threads / s.lanes : 1;
+    return (rows + per - 1) / per;
+}
+
 // Workgroups of the gradient, hence partial sums: two per compute unit at most.
 constexpr int kGradGroupsPerCu = 2;
 
 size_t grad_groups(size_t rows, int hidden, int cus) {
-    const RowShape s = row_shape(hidden);
-    const size_t per = s.lanes > 0 ? s.threads / s.lanes : 1;
-    const size_t groups = (rows + per - 1) / per;
+    const size_t groups = groups_of(rows, row_shape(hidden));
     const size_t cap = static_cast<size_t>(cus) * kGradGroupsPerCu;
     return groups < cap ? groups : cap;
 }
@@ -483,6 +486,8 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     if (q->group != 0 && q->group != 32 && q->group != 64 && q->group != 128) return HR_ERR_INVALID_ARG;
     if (q->hidden > HR_RMSNORM_MAX_HIDDEN || q->rows > kMaxRows) return HR_ERR_TOO_LARGE;
     if (q->rows == 0) return HR_OK;
+    const RowShape s = row_shape(static_cast<int>(q->hidden));
+    if (groups_of(q->rows, s) > 0xFFFFFFFFu / s.threads) return HR_ERR_TOO_LARGE;   // work-items of a launch
     if (q->out == nullptr && q->residual_out == nullptr && q->codes == nullptr && q->rstd == nullptr)
         return HR_ERR_INVALID_ARG;
     if ((q->codes == nullptr) != (q->scales == nullptr)) return HR_ERR_INVALID_ARG;
@@ -544,9 +549,7 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     a.group_lanes = q->group / 8;
     a.eps = q->eps;
 
-    const RowShape s = row_shape(a.hidden);
-    const size_t per = s.lanes > 0 ? s.threads / s.lanes : 1;
-    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, static_cast<unsigned>((rows + per - 1) / per),
+    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, static_cast<unsigned>(groups_of(rows, s)),
                                                     reinterpret_cast<hipStream_t>(stream), a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }

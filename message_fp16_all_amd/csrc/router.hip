@@ -258,7 +258,7 @@ hipError_t launch_router(const RouterArgs &a, bool grad, hipStream_t s) {
 hr_status router_impl(RouterArgs &a, hr_dtype dtype, bool grad, hr_stream_t stream) {
     if (a.experts < 1 || a.k < 1 || a.k > a.experts) return HR_ERR_INVALID_ARG;
     if (dtype != HR_DTYPE_F16 && dtype != HR_DTYPE_BF16 && dtype != HR_DTYPE_F32) return HR_ERR_INVALID_ARG;
-    if (a.experts > HR_ROUTER_MAX_EXPERTS || a.k > HR_ROUTER_MAX_K || a.tokens > 0x7FFFFFFF) return HR_ERR_TOO_LARGE;
+    if (a.experts > HR_ROUTER_MAX_EXPERTS || a.k > HR_ROUTER_MAX_K || a.tokens > HR_ROUTER_MAX_TOKENS) return HR_ERR_TOO_LARGE;
     if (a.tokens == 0) return HR_OK;
     const bool reads = !grad || !a.renormalize;
     if (a.weights == nullptr || a.ids == nullptr || (reads && a.logits == nullptr)) return HR_ERR_INVALID_ARG;

@@ -13,6 +13,7 @@
 namespace hr {
 
 typedef u32x4 u32x4_row __attribute__((aligned(2)));
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_row __attribute__((aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -51,7 +51,9 @@ EXPORTS = ("hr_create_channel", "hr_allreduce_f16", "hr_reduce_f16", "hr_channel
            "hr_workspace_stride", "hr_exchange_algorithm", "hr_allreduce_group_f16",
            "hr_allreduce_group_bf16", "hr_allreduce_group_noalloc_f16", "hr_channel_timeout_info",
            "hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
-           "hr_rmsnorm_grad_workspace", "hr_router_topk", "hr_router_topk_grad")
+           "hr_rmsnorm_grad_workspace", "hr_router_topk", "hr_router_topk_grad", "hr_experts_rows",
+           "hr_experts_sort_workspace", "hr_experts_sort", "hr_experts_gather", "hr_experts_combine_f16",
+           "hr_experts_combine_bf16", "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16")
 
 HR_ROUTE_HOST = 0
 HR_DECLINE_DISABLED = 1
@@ -67,6 +69,9 @@ HR_DTYPE_F32 = 3
 HR_RMSNORM_MAX_HIDDEN = 32768
 HR_ROUTER_MAX_EXPERTS = 1024
 HR_ROUTER_MAX_K = 32
+HR_ROUTER_MAX_TOKENS = (1 << 26) - 4
+HR_EXPERTS_MAX = 1024
+HR_EXPERTS_MAX_K = 32
 
 
 class hr_channel_config(ctypes.Structure):
@@ -129,6 +134,29 @@ class hr_rmsnorm_grad_args(ctypes.Structure):
                 ("weight_f32", ctypes.c_int)]
 
 
+class hr_experts_gather_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("in_", "scales", "out", "scales_out", "pos", "order", "offsets")),
+                *((n, ctypes.c_size_t) for n in ("tokens", "rows", "row_bytes", "in_stride", "out_stride",
+                                                 "scales_width", "scales_stride", "scales_out_stride")),
+                ("k", ctypes.c_int),
+                ("experts", ctypes.c_int)]
+
+
+class hr_experts_combine_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("z", "addend", "out", "pos", "weights")),
+                *((n, ctypes.c_size_t) for n in ("tokens", "rows", "hidden", "z_stride", "addend_stride",
+                                                 "out_stride")),
+                ("k", ctypes.c_int)]
+
+
+class hr_experts_combine_grad_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("dy", "z", "dz", "pos", "weights", "dweights", "order",
+                                                 "offsets")),
+                *((n, ctypes.c_size_t) for n in ("tokens", "rows", "hidden", "dy_stride", "z_stride", "dz_stride")),
+                ("k", ctypes.c_int),
+                ("experts", ctypes.c_int)]
+
+
 class HrError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -181,14 +209,21 @@ def load() -> ctypes.CDLL:
     lib.hr_decode_numel.argtypes = [ctypes.c_size_t, ctypes.c_size_t, ctypes.c_size_t]
     lib.hr_workspace_stride.argtypes = [ctypes.c_size_t]
     # argument structs: byref of the ctypes struct, or its bytes
-    for name in ("hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16"):
+    for name in ("hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
+                 "hr_experts_gather", "hr_experts_combine_f16", "hr_experts_combine_bf16",
+                 "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16"):
         getattr(lib, name).argtypes = [vp, vp]
     lib.hr_rmsnorm_grad_workspace.argtypes = [ctypes.c_size_t, ctypes.c_size_t]
     lib.hr_router_topk.argtypes = [vp, ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
                                    ctypes.c_int, vp, vp, vp]
     lib.hr_router_topk_grad.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t,
                                         ctypes.c_int, ctypes.c_int, vp, ctypes.c_size_t, vp]
-    sizes = ("hr_decode_numel", "hr_workspace_stride", "hr_rmsnorm_grad_workspace")
+    lib.hr_experts_rows.argtypes = [ctypes.c_size_t, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    lib.hr_experts_sort_workspace.argtypes = [ctypes.c_size_t, ctypes.c_int, ctypes.c_int]
+    lib.hr_experts_sort.argtypes = [vp, ctypes.c_size_t, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp,
+                                    vp, ctypes.c_size_t, vp, vp, ctypes.c_size_t, vp]
+    sizes = ("hr_decode_numel", "hr_workspace_stride", "hr_rmsnorm_grad_workspace", "hr_experts_rows",
+             "hr_experts_sort_workspace")
     for name in sizes:
         getattr(lib, name).restype = ctypes.c_size_t
     for name in EXPORTS:
@@ -375,6 +410,48 @@ def hr_router_topk_grad(dweights_ptr, weights_ptr, ids_ptr, logits_ptr, dtype: i
                                       logits_stride, k, renormalize, dlogits_ptr, dlogits_stride, stream)
 
 
+def hr_experts_rows(tokens: int, k: int, experts: int, pad: int = 1) -> int:
+    """Rows that sorted tokens take at most (0 for arguments out of range)."""
+    return load().hr_experts_rows(tokens, k, experts, pad)
+
+
+def hr_experts_sort_workspace(tokens: int, k: int, experts: int) -> int:
+    """Bytes of workspace that a sort needs."""
+    return load().hr_experts_sort_workspace(tokens, k, experts)
+
+
+def hr_experts_sort(ids_ptr, tokens: int, k: int, first: int, experts: int, pad: int, offsets_ptr, order_ptr, rows: int,
+                    pos_ptr, workspace_ptr, workspace_bytes: int, stream: int) -> int:
+    """Raw call; returns the hr_status code."""
+    return load().hr_experts_sort(ids_ptr, tokens, k, first, experts, pad, offsets_ptr, order_ptr, rows, pos_ptr,
+                                  workspace_ptr, workspace_bytes, stream)
+
+
+def hr_experts_gather(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_gather_args.  Returns the hr_status code."""
+    return load().hr_experts_gather(ctypes.byref(args), stream)
+
+
+def hr_experts_combine_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_combine_args.  Returns the hr_status code."""
+    return load().hr_experts_combine_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_combine_bf16(args, stream: int) -> int:
+    """As hr_experts_combine_f16 for bfloat16 buffers."""
+    return load().hr_experts_combine_bf16(ctypes.byref(args), stream)
+
+
+def hr_experts_combine_grad_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_combine_grad_args.  Returns the hr_status code."""
+    return load().hr_experts_combine_grad_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_combine_grad_bf16(args, stream: int) -> int:
+    """As hr_experts_combine_grad_f16 for bfloat16 buffers."""
+    return load().hr_experts_combine_grad_bf16(ctypes.byref(args), stream)
+
+
 def workspace(G: int, numel: int, dtype=None, device=0):
     """A device buffer holding G contributions in the hr_workspace_stride
     layout; returns (buffer, [view of contribution g])."""
@@ -492,6 +569,9 @@ def allreduce_group_noalloc(ins, outs, status=None, stream=None):
 
 _NORM = struct.Struct("@23P8N3if")
 _NORM_GRAD = struct.Struct("@8P7Ni4x")
+_GATHER = struct.Struct("@7P8N2i")
+_COMBINE = struct.Struct("@5P6Ni4x")
+_COMBINE_GRAD = struct.Struct("@8P6N2i")
 _entries = {}
 
 
@@ -698,6 +778,143 @@ def router_topk_grad(dweights, weights, ids, dlogits, *, logits=None, renormaliz
     if st != HR_OK:
         raise HrError(st, "hr_router_topk_grad")
     return dlogits
+
+
+def experts_buffers(tokens: int, k: int, experts: int, pad: int = 1, device=0):
+    """Device tensors (offsets, order, pos) for experts_sort; order's length is
+    the rows that a gathered buffer needs."""
+    import torch
+    dev = torch.device("cuda", device) if isinstance(device, int) else device
+    rows = hr_experts_rows(tokens, k, experts, pad)
+    return tuple(torch.empty(shape, dtype=torch.int32, device=dev) for shape in ((experts + 1,), (rows,), (tokens, k)))
+
+
+def experts_sort(ids, offsets, order, pos, *, first: int = 0, pad: int = 1, workspace=None, stream=None):
+    """Where every pick goes (hr_experts_sort): ``ids`` (torch.int32, tokens x
+    k) sorted stably by expert, for the experts first .. first + n - 1 with n =
+    offsets.numel() - 1, every segment rounded up to ``pad`` rows.
+    ``workspace``: a device tensor of hr_experts_sort_workspace bytes; None
+    takes one from torch's allocator when the call needs one."""
+    if _torch is None:
+        _tm()
+    if ids.dim() != 2:
+        raise ValueError("ids: expected tokens x k")
+    tokens, k = ids.shape
+    i32 = _torch.int32
+    ip = _flat_ptr(ids, "ids", i32, tokens * k)
+    experts = offsets.numel() - 1
+    op = _flat_ptr(offsets, "offsets", i32, experts + 1)
+    rows = order.numel()
+    rp = _flat_ptr(order, "order", i32, rows)
+    pp = _flat_ptr(pos, "pos", i32, tokens * k)
+    lib = load()
+    kp = kb = 0
+    if workspace is None:
+        need = lib.hr_experts_sort_workspace(tokens, k, experts)
+        if need:
+            workspace = _scratch(need, ids, stream)
+    if workspace is not None:
+        kb = workspace.numel() * workspace.element_size()
+        kp = _flat_ptr(workspace, "workspace", workspace.dtype, workspace.numel())
+    st = lib.hr_experts_sort(ip, tokens, k, first, experts, pad, op, rp, rows, pp, kp, kb,
+                             _stream_handle(stream, ids))
+    if st != HR_OK:
+        raise HrError(st, "hr_experts_sort")
+    return offsets, order, pos
+
+
+def _pos_ptr(pos, tokens: int):
+    """(address, k) of a sort's pos."""
+    if pos.dim() != 2 or pos.shape[0] != tokens:
+        raise ValueError(f"pos: expected {tokens} x k")
+    k = pos.shape[1]
+    return _flat_ptr(pos, "pos", _torch.int32, tokens * k), k
+
+
+def _padding_ptrs(order, offsets, rows: int):
+    """(addresses of order and offsets, experts) of a sort, or of none."""
+    if order is None:
+        return 0, 0, 0
+    if offsets is None:
+        raise ValueError("order is given without offsets")
+    experts = offsets.numel() - 1
+    return (_flat_ptr(order, "order", _torch.int32, rows), _flat_ptr(offsets, "offsets", _torch.int32, experts + 1),
+            experts)
+
+
+def experts_gather(x, pos, out, *, offsets=None, order=None, scales=None, scales_out=None, stream=None):
+    """Every token's row to its sorted rows, and its scales with it
+    (hr_experts_gather): ``x`` and ``out`` of any one type, ``scales``
+    torch.float32.  With ``order`` and ``offsets`` the padding rows inside the
+    segments become zeros; rows past the last segment are not written."""
+    if _torch is None:
+        _tm()
+    dt = x.dtype
+    xp, tokens, width, xs = _row_view(x, "x", dt)
+    op, rows, _, os_ = _row_view(out, "out", dt, out.shape[0], width)
+    pp, k = _pos_ptr(pos, tokens)
+    rp, fp, experts = _padding_ptrs(order, offsets, rows)
+    sp = tp = sw = ss = ts = 0
+    if scales is not None or scales_out is not None:
+        if scales is None or scales_out is None:
+            raise ValueError("scales and scales_out go together")
+        f32 = _torch.float32
+        sw = scales.shape[-1]
+        sp, _, _, ss = _row_view(scales, "scales", f32, tokens, sw)
+        tp, _, _, ts = _row_view(scales_out, "scales_out", f32, rows, sw)
+    size = x.element_size()
+    args = _GATHER.pack(xp, sp, op, tp, pp, rp, fp, tokens, rows, width * size, xs * size, os_ * size, sw, ss, ts, k,
+                        experts)
+    st = load().hr_experts_gather(args, _stream_handle(stream, x))
+    if st != HR_OK:
+        raise HrError(st, "hr_experts_gather")
+    return out
+
+
+def experts_combine(z, pos, out, *, weights=None, addend=None, stream=None):
+    """out[t] = addend[t] + sum over j of weights[t, j] * z[pos[t, j]]
+    (hr_experts_combine); ``z`` holds sorted rows, torch.float16 or
+    torch.bfloat16.  Without weights, the gradient of experts_gather."""
+    dt = out.dtype
+    fn, name = _entry("hr_experts_combine", dt)
+    op, tokens, hidden, os_ = _row_view(out, "out", dt)
+    zp, rows, _, zs = _row_view(z, "z", dt, z.shape[0], hidden)
+    pp, k = _pos_ptr(pos, tokens)
+    wp = ap = as_ = 0
+    if weights is not None:
+        wp = _flat_ptr(weights, "weights", _torch.float32, tokens * k)
+    if addend is not None:
+        ap, _, _, as_ = _row_view(addend, "addend", dt, tokens, hidden)
+    args = _COMBINE.pack(zp, ap, op, pp, wp, tokens, rows, hidden, zs, as_, os_, k)
+    st = fn(args, _stream_handle(stream, out))
+    if st != HR_OK:
+        raise HrError(st, name)
+    return out
+
+
+def experts_combine_grad(dy, z, pos, weights=None, dz=None, dweights=None, *, offsets=None, order=None, stream=None):
+    """The gradient of experts_combine (hr_experts_combine_grad): ``dz`` of the
+    sorted rows and ``dweights`` (torch.float32, tokens x k), either of which
+    may be None.  With ``order`` and ``offsets`` the padding rows of dz become
+    zeros; rows past the last segment are not written."""
+    dt = dy.dtype
+    fn, name = _entry("hr_experts_combine_grad", dt)
+    yp, tokens, hidden, ys = _row_view(dy, "dy", dt)
+    zp, rows, _, zs = _row_view(z, "z", dt, z.shape[0], hidden)
+    pp, k = _pos_ptr(pos, tokens)
+    dp = ds = wp = gp = 0
+    if dz is not None:
+        dp, _, _, ds = _row_view(dz, "dz", dt, rows, hidden)
+    if weights is not None:
+        wp = _flat_ptr(weights, "weights", _torch.float32, tokens * k)
+    if dweights is not None:
+        gp = _flat_ptr(dweights, "dweights", _torch.float32, tokens * k)
+    rp, fp, experts = _padding_ptrs(order, offsets, rows)
+    args = _COMBINE_GRAD.pack(yp, zp, dp, pp, wp, gp, rp, fp, tokens, rows, hidden, ys, zs, ds, k, experts)
+    st = fn(args, _stream_handle(stream, dy))
+    if st != HR_OK:
+        raise HrError(st, name)
+    return dz, dweights
 
 
 class Channel:
