@@ -252,10 +252,11 @@ struct Padding {
     int experts;
 };
 
+template <bool NT>
 __device__ __forceinline__ void zero_row(char *row, size_t bytes) {
     const size_t whole = bytes / 16;
     for (size_t i = threadIdx.x; i < whole; i += kExpertThreads)
-        *reinterpret_cast<u32x4_byte *>(row + 16 * i) = u32x4{0, 0, 0, 0};
+        store_vec<NT>(u32x4{0, 0, 0, 0}, row + 16 * i);
     for (size_t i = 16 * whole + threadIdx.x; i < bytes; i += kExpertThreads) row[i] = 0;
 }
 
@@ -291,12 +292,12 @@ __device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
 
 // L lanes per token (L = kExpertThreads: its units are also split over
 // workgroups), one unit per lane and step.
-template <int L>
+template <int L, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (blockIdx.x < a.pad_groups) {
         for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
-            zero_row(a.out + p * a.out_stride, a.row_bytes);
-            if (a.scales_out != nullptr) zero_row(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
+            zero_row<NT>(a.out + p * a.out_stride, a.row_bytes);
+            if (a.scales_out != nullptr) zero_row<NT>(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
         });
         return;
     }
@@ -323,10 +324,10 @@ __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
             for (int j = 0; j < kPicks; ++j) p[j] = j0 + j < a.k ? static_cast<uint32_t>(pos[j0 + j]) : ~0u;
             if (bytes >= 16) {
                 const size_t o = unit_at(u, bytes);
-                const u32x4 v = *reinterpret_cast<const u32x4_byte *>(src + o);
+                const u32x4 v = load_vec<false>(src + o);
 #pragma unroll
                 for (int j = 0; j < kPicks; ++j)
-                    if (p[j] < a.rows) *reinterpret_cast<u32x4_byte *>(dst + p[j] * stride + o) = v;
+                    if (p[j] < a.rows) store_vec<NT>(v, dst + p[j] * stride + o);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPicks; ++j)
@@ -349,7 +350,7 @@ struct CombineArgs {
 };
 
 // The sum is binary32 and runs in pick order, the addend first; one rounding.
-template <class E, int L, bool TAIL>
+template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
     constexpr uint32_t kTokens = kExpertThreads / L;
     const uint32_t t = L == kExpertThreads ? blockIdx.x / a.splits : blockIdx.x * kTokens + threadIdx.x / L;
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
                     const uint32_t p = static_cast<uint32_t>(pos[j0 + j]);
                     there[j] = p < a.rows;
                     if (there[j]) {
-                        z[j] = load_unit<TAIL>(a.z + p * a.z_stride, i, a.hidden);
+                        z[j] = load_unit<TAIL, NT>(a.z + p * a.z_stride, i, a.hidden);
                         w[j] = weights != nullptr ? weights[j0 + j] : 1.0f;
                     }
                 }
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
                 }
             }
         }
-        store_unit<TAIL>(a.out + t * a.out_stride, i, a.hidden, Wide<E>::narrow(sum));
+        store_unit<TAIL, NT>(a.out + t * a.out_stride, i, a.hidden, Wide<E>::narrow(sum));
     }
 }
 
@@ -412,12 +413,12 @@ struct CombineGradArgs {
 
 // L lanes per token over all of its row, since the weights' gradients are sums
 // over it; kPicks of them at a time in registers.
-template <class E, int L, bool TAIL>
+template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
     __shared__ float sums[kExpertThreads / kWave][kPicks];
     if (blockIdx.x < a.pad_groups) {
         for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
-            zero_row(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
+            zero_row<NT>(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
         });
         return;
     }
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
             if (a.dweights != nullptr) {
 #pragma unroll
                 for (int j = 0; j < kPicks; ++j)
-                    if (p[j] < a.rows) z[j] = load_unit<TAIL>(a.z + p[j] * a.z_stride, i, a.hidden);
+                    if (p[j] < a.rows) z[j] = load_unit<TAIL, NT>(a.z + p[j] * a.z_stride, i, a.hidden);
             }
 #pragma unroll
             for (int j = 0; j < kPicks; ++j) {
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
                     if (a.dz != nullptr) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = d[e] * w[j];
-                        store_unit<TAIL>(a.dz + p[j] * a.dz_stride, i, a.hidden, Wide<E>::narrow(f));
+                        store_unit<TAIL, NT>(a.dz + p[j] * a.dz_stride, i, a.hidden, Wide<E>::narrow(f));
                     }
                 }
             }
@@ -514,14 +515,17 @@ bool picks_ok(size_t tokens, int k, size_t *slots) {
 // Lanes that a row of `units` 16-byte units keeps busy.
 int lanes_for(size_t units) { return units <= 16 ? 16 : units <= 64 ? 64 : kExpertThreads; }
 
-template <class K16, class K64, class K256, class A>
-hipError_t launch_lanes(int lanes, unsigned grid, hipStream_t s, K16 k16, K64 k64, K256 k256, const A &a) {
-    if (lanes == 16)
-        hipLaunchKernelGGL(k16, dim3(grid), dim3(kExpertThreads), 0, s, a);
-    else if (lanes == 64)
-        hipLaunchKernelGGL(k64, dim3(grid), dim3(kExpertThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL(k256, dim3(grid), dim3(kExpertThreads), 0, s, a);
+// Sorted rows of this many bytes or more pass the caches by (non-temporal
+// loads and stores).  Measured as a sort, a gather and a combine of 8 picks of
+// 4096 values in turn, on three sets of buffers: 33 MB of rows 24.8 us cached
+// and 25.1 us streamed, 67 MB 52.0 and 42.5 us, 134 MB 80.6 and 65.8 us, 537
+// MB 281 and 213 us.  (A combine alone over rows that the last-level cache
+// still holds is slower streamed, 13.0 against 14.0 us at 67 MB.)
+constexpr size_t kStreamBytes = size_t(1) << 26;
+
+template <class K, class A>
+hipError_t launch_k(K k, size_t grid, hipStream_t s, const A &a) {
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(grid)), dim3(kExpertThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -530,6 +534,11 @@ hipError_t launch_lanes(int lanes, unsigned grid, hipStream_t s, K16 k16, K64 k6
 uint32_t padding_groups(const Padding &q, size_t slots) {
     return q.order != nullptr && q.rows > slots ? (q.rows + kPadRows - 1) / kPadRows : 0;
 }
+
+// The variant of a kernel for a call's `tail` and `nt`.
+#define HR_VARIANT(K, L)                                                      \
+    (tail ? (nt ? K<E, L, true, true> : K<E, L, true, false>)                 \
+          : (nt ? K<E, L, false, true> : K<E, L, false, false>))
 
 template <class E>
 hr_status combine_impl(const hr_experts_combine_args *q, hr_stream_t stream) {
@@ -572,12 +581,10 @@ hr_status combine_impl(const hr_experts_combine_args *q, hr_stream_t stream) {
                                                 : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
     if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const unsigned g = static_cast<unsigned>(grid);
-    const hipError_t e = q->hidden % 8 != 0
-                             ? launch_lanes(lanes, g, s, combine_rows<E, 16, true>, combine_rows<E, 64, true>,
-                                            combine_rows<E, kExpertThreads, true>, a)
-                             : launch_lanes(lanes, g, s, combine_rows<E, 16, false>, combine_rows<E, 64, false>,
-                                            combine_rows<E, kExpertThreads, false>, a);
+    const bool nt = slots * width >= kStreamBytes, tail = q->hidden % 8 != 0;
+    const hipError_t e = lanes == 16   ? launch_k(HR_VARIANT(combine_rows, 16), grid, s, a)
+                         : lanes == 64 ? launch_k(HR_VARIANT(combine_rows, 64), grid, s, a)
+                                       : launch_k(HR_VARIANT(combine_rows, kExpertThreads), grid, s, a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
@@ -630,15 +637,14 @@ hr_status combine_grad_impl(const hr_experts_combine_grad_args *q, hr_stream_t s
     const size_t grid = a.pad_groups + (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
     if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const unsigned g = static_cast<unsigned>(grid);
-    const hipError_t e = q->hidden % 8 != 0
-                             ? launch_lanes(lanes, g, s, combine_grad_rows<E, 16, true>, combine_grad_rows<E, 64, true>,
-                                            combine_grad_rows<E, kExpertThreads, true>, a)
-                             : launch_lanes(lanes, g, s, combine_grad_rows<E, 16, false>,
-                                            combine_grad_rows<E, 64, false>,
-                                            combine_grad_rows<E, kExpertThreads, false>, a);
+    const bool nt = slots * width >= kStreamBytes, tail = q->hidden % 8 != 0;
+    const hipError_t e = lanes == 16   ? launch_k(HR_VARIANT(combine_grad_rows, 16), grid, s, a)
+                         : lanes == 64 ? launch_k(HR_VARIANT(combine_grad_rows, 64), grid, s, a)
+                                       : launch_k(HR_VARIANT(combine_grad_rows, kExpertThreads), grid, s, a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
+
+#undef HR_VARIANT
 
 }  // namespace
 
@@ -777,8 +783,12 @@ extern "C" HR_API hr_status hr_experts_gather(const hr_experts_gather_args *q, h
         a.pad_groups + (lanes == kExpertThreads ? q->tokens * a.splits
                                                 : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes));
     if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
-    const hipError_t e = launch_lanes(lanes, static_cast<unsigned>(grid), reinterpret_cast<hipStream_t>(stream),
-                                      gather_rows<16>, gather_rows<64>, gather_rows<kExpertThreads>, a);
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const bool nt = slots * (q->row_bytes + a.scale_bytes) >= kStreamBytes;
+    const hipError_t e = lanes == 16   ? launch_k(nt ? gather_rows<16, true> : gather_rows<16, false>, grid, s, a)
+                         : lanes == 64 ? launch_k(nt ? gather_rows<64, true> : gather_rows<64, false>, grid, s, a)
+                                       : launch_k(nt ? gather_rows<kExpertThreads, true>
+                                                     : gather_rows<kExpertThreads, false>, grid, s, a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 

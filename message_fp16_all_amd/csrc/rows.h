@@ -2,9 +2,9 @@
 // expert rows, router logits); not exported.
 //
 // A row is read and written in units of 8 values (16 bytes).  Rows may start
-// at any 2-byte address: gfx950 serves unaligned 16-byte global accesses, so
-// the unit type only promises the alignment of one value, and the same
-// instruction carries aligned and unaligned rows.  A last unit that the row
+// at any address of a value: gfx950 serves unaligned 16-byte global accesses,
+// so the unit type promises no alignment, and the same instruction carries
+// aligned and unaligned rows.  A last unit that the row
 // does not fill is moved value by value (the TAIL variants).
 #pragma once
 
@@ -12,7 +12,6 @@
 
 namespace hr {
 
-typedef u32x4 u32x4_row __attribute__((aligned(2)));
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_row __attribute__((aligned(1)));
@@ -86,13 +85,32 @@ struct Wide<BF16> {
     }
 };
 
+// NT: non-temporal, for what passes through once and would only push other
+// lines out of the caches.  Dirty lines cost twice: a call that leaves them
+// behind makes the next call's reads wait for their write-back.
+template <bool NT>
+__device__ __forceinline__ u32x4 load_vec(const void *p) {
+    if constexpr (NT)
+        return __builtin_nontemporal_load(static_cast<const u32x4_byte *>(p));
+    else
+        return *static_cast<const u32x4_byte *>(p);
+}
+
+template <bool NT>
+__device__ __forceinline__ void store_vec(u32x4 v, void *p) {
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, static_cast<u32x4_byte *>(p));
+    else
+        *static_cast<u32x4_byte *>(p) = v;
+}
+
 // Unit i of a row of n values; values past the row's end read as zero bits.
 // Offsets are unsigned 32-bit: added to a wave-uniform row address they need
 // one register.
-template <bool TAIL>
+template <bool TAIL, bool NT = false>
 __device__ __forceinline__ u32x4 load_unit(const uint16_t *row, int i, int n) {
     if (!TAIL || 8 * i + 8 <= n)
-        return *reinterpret_cast<const u32x4_row *>(reinterpret_cast<const char *>(row) + 16u * i);
+        return load_vec<NT>(reinterpret_cast<const char *>(row) + 16u * i);
     u32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -100,10 +118,10 @@ __device__ __forceinline__ u32x4 load_unit(const uint16_t *row, int i, int n) {
     return v;
 }
 
-template <bool TAIL>
+template <bool TAIL, bool NT = false>
 __device__ __forceinline__ void store_unit(uint16_t *row, int i, int n, u32x4 v) {
     if (!TAIL || 8 * i + 8 <= n) {
-        *reinterpret_cast<u32x4_row *>(reinterpret_cast<char *>(row) + 16u * i) = v;
+        store_vec<NT>(v, reinterpret_cast<char *>(row) + 16u * i);
         return;
     }
 #pragma unroll
