@@ -361,9 +361,10 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
     const int units = (a.hidden + 7) / 8;
     const int step = L == kExpertThreads ? static_cast<int>(kExpertThreads * a.splits) : L;
     for (int i = static_cast<int>(split * kExpertThreads + threadIdx.x % L); i < units; i += step) {
+        const Unit<TAIL> at(i, a.hidden);
         float sum[8];
         if (a.addend != nullptr) {
-            Wide<E>::widen(load_unit<TAIL>(a.addend + t * a.addend_stride, i, a.hidden), sum);
+            Wide<E>::widen(at.load(a.addend + t * a.addend_stride), sum);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
                     const uint32_t p = static_cast<uint32_t>(pos[j0 + j]);
                     there[j] = p < a.rows;
                     if (there[j]) {
-                        z[j] = load_unit<TAIL, NT>(a.z + p * a.z_stride, i, a.hidden);
+                        z[j] = at.template load<NT>(a.z + p * a.z_stride);
                         w[j] = weights != nullptr ? weights[j0 + j] : 1.0f;
                     }
                 }
@@ -394,7 +395,8 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
                 }
             }
         }
-        store_unit<TAIL, NT>(a.out + t * a.out_stride, i, a.hidden, Wide<E>::narrow(sum));
+        // its own values only: out may be the addend, which a neighbour reads
+        at.template store_own<NT>(a.out + t * a.out_stride, Wide<E>::narrow(sum));
     }
 }
 
@@ -443,13 +445,14 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
             }
         }
         for (int i = lane; i < units; i += L) {
+            const Unit<TAIL> at(i, a.hidden);
             float d[8];
             u32x4 z[kPicks];
-            Wide<E>::widen(load_unit<TAIL>(a.dy + t * a.dy_stride, i, a.hidden), d);
+            Wide<E>::widen(at.load(a.dy + t * a.dy_stride), d);
             if (a.dweights != nullptr) {
 #pragma unroll
                 for (int j = 0; j < kPicks; ++j)
-                    if (p[j] < a.rows) z[j] = load_unit<TAIL, NT>(a.z + p[j] * a.z_stride, i, a.hidden);
+                    if (p[j] < a.rows) z[j] = at.template load<NT>(a.z + p[j] * a.z_stride);
             }
 #pragma unroll
             for (int j = 0; j < kPicks; ++j) {
@@ -458,12 +461,13 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
                     if (a.dweights != nullptr) {
                         Wide<E>::widen(z[j], f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(at.own(e) ? d[e] : 0.0f, f[e], dot[j]);
                     }
                     if (a.dz != nullptr) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = d[e] * w[j];
-                        store_unit<TAIL, NT>(a.dz + p[j] * a.dz_stride, i, a.hidden, Wide<E>::narrow(f));
+                        // its own values only: dz may be z, which a neighbour reads
+                        at.template store_own<NT>(a.dz + p[j] * a.dz_stride, Wide<E>::narrow(f));
                     }
                 }
             }

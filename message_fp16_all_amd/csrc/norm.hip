@@ -40,15 +40,16 @@ struct NormArgs {
     float eps;
 };
 
-// The 8 weights of unit i; values past the end are 0, and 1 without a weight.
+// The 8 weights of a unit; values past the row's end are 0, and without a
+// weight all are 1.
 template <class E, bool TAIL>
-__device__ __forceinline__ void load_weight(const void *w, int f32, int i, int n, float (&f)[8]) {
+__device__ __forceinline__ void load_weight(const void *w, int f32, const Unit<TAIL> &u, float (&f)[8]) {
     if (w == nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 1.0f;
     } else if (f32) {
-        const float *p = reinterpret_cast<const float *>(static_cast<const char *>(w) + 32u * i);
-        if (!TAIL || 8 * i + 8 <= n) {
+        const float *p = reinterpret_cast<const float *>(static_cast<const char *>(w) + 4u * u.start);
+        if (!TAIL || u.n >= 8) {
             const f32x4 a = *reinterpret_cast<const f32x4_row *>(p), b = *reinterpret_cast<const f32x4_row *>(p + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -57,10 +58,10 @@ __device__ __forceinline__ void load_weight(const void *w, int f32, int i, int n
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 8 * i + e < n ? p[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) f[e] = e < u.n ? p[e] : 0.0f;
         }
     } else {
-        Wide<E>::widen(load_unit<TAIL>(static_cast<const uint16_t *>(w), i, n), f);
+        Wide<E>::widen(u.load(static_cast<const uint16_t *>(w)), f);
     }
 }
 
@@ -104,7 +105,7 @@ __device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
 // One row per workgroup (L = 0), or one row per L lanes of a workgroup.
 // Thread t of a row holds units t, t + threads, .. (U of them) from the fold's
 // loads to the stores, so every input byte is read once.
-template <class E, int U, int L, bool TAIL>
+template <class E, int U, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
     __shared__ float sums[kNormMaxWaves];
     __shared__ uint32_t maxs[kNormMaxWaves];
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
                 for (int u = 0; u < U; ++u) {
                     const int i = t + u * threads;
                     x[b][u] = u32x4{0, 0, 0, 0};
-                    if (there && i < units) x[b][u] = load_unit<TAIL>(p, i, hidden);
+                    if (there && i < units) x[b][u] = Unit<TAIL>(i, hidden).template load<NT>(p);
                 }
             }
         }
@@ -151,14 +152,18 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
     for (int u = 0; u < U; ++u) {
         float f[8];
         Wide<E>::widen(h[u], f);
+        const Unit<TAIL> at(t + u * threads, hidden);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+        for (int e = 0; e < 8; ++e) {
+            if (!at.own(e)) f[e] = 0.0f;
+            sum = fmaf(f[e], f[e], sum);
+        }
     }
     float w[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int i = t + u * threads;
-        if (i < units) load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w[u]);
+        if (i < units) load_weight<E>(a.weight, a.weight_f32, Unit<TAIL>(i, hidden), w[u]);
     }
     sum = sum_row<L>(sum, sums);
     const float rstd = 1.0f / sqrtf(sum / static_cast<float>(hidden) + a.eps);
@@ -171,19 +176,20 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
         const int i = t + u * threads;
         top[u] = 0;
         if (i >= units) continue;
+        const Unit<TAIL> at(i, hidden);
         Wide<E>::widen(h[u], y[u]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             y[u][e] = y[u][e] * rstd * w[u][e];
             // magnitudes compared as integers, so that a NaN is the largest
-            if (!TAIL || 8 * i + e < hidden) {
+            if (at.own(e)) {
                 const uint32_t m = __builtin_bit_cast(uint32_t, y[u][e]) & 0x7FFFFFFFu;
                 top[u] = top[u] > m ? top[u] : m;
             }
         }
         if (!there) continue;
-        if (a.h != nullptr) store_unit<TAIL>(a.h + row * a.h_stride, i, hidden, h[u]);
-        if (a.out != nullptr) store_unit<TAIL>(a.out + row * a.out_stride, i, hidden, Wide<E>::narrow(y[u]));
+        if (a.h != nullptr) at.template store<NT>(a.h + row * a.h_stride, h[u]);
+        if (a.out != nullptr) at.template store<NT>(a.out + row * a.out_stride, Wide<E>::narrow(y[u]));
     }
     if (a.codes == nullptr) return;
 
@@ -216,13 +222,18 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
             v = __builtin_amdgcn_cvt_pk_fp8_f32(y[u][4 * q + 2] * inv, y[u][4 * q + 3] * inv, v, true);
             c[q] = static_cast<uint32_t>(v);
         }
-        uint8_t *p = a.codes + row * a.codes_stride + 8 * static_cast<size_t>(i);
-        if (!TAIL || 8 * i + 8 <= hidden) {
-            *reinterpret_cast<u32x2_row *>(p) = c;
+        // a last unit's shared values may have another group's scale: its own only
+        const Unit<TAIL> at(i, hidden);
+        uint8_t *p = a.codes + row * a.codes_stride + at.start;
+        if (!TAIL || (hidden >= 8 && at.skip == 0)) {
+            if constexpr (NT)
+                __builtin_nontemporal_store(c, reinterpret_cast<u32x2_row *>(p));
+            else
+                *reinterpret_cast<u32x2_row *>(p) = c;
         } else {
 #pragma unroll
-            for (int e = 0; e < 7; ++e)
-                if (8 * i + e < hidden) p[e] = static_cast<uint8_t>(c[e / 4] >> (8 * (e & 3)));
+            for (int e = 0; e < 8; ++e)
+                if (at.own(e)) p[e] = static_cast<uint8_t>(c[e / 4] >> (8 * (e & 3)));
         }
     }
 }
@@ -243,7 +254,7 @@ struct NormGradArgs {
 // and this workgroup's sum over its rows of dy * u.  Rows are dealt out to the
 // workgroups (L = 0) or to groups of L lanes in turn; a thread keeps its
 // columns' sums in registers from its first row to its last.
-template <class E, int U, int L, bool TAIL>
+template <class E, int U, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a) {
     __shared__ float sums[2][kNormMaxWaves];
     const int threads = L > 0 ? L : static_cast<int>(blockDim.x);
@@ -269,7 +280,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
 #pragma unroll
             for (int e = 0; e < 8; ++e) kept[u][e] = 0.0f;
             if (t + u * threads < units)
-                load_weight<E, TAIL>(a.weight, a.weight_f32, t + u * threads, hidden, kept[u]);
+                load_weight<E>(a.weight, a.weight_f32, Unit<TAIL>(t + u * threads, hidden), kept[u]);
         }
     }
 
@@ -283,9 +294,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
             const int i = t + u * threads;
             d[u] = h[u] = r[u] = u32x4{0, 0, 0, 0};
             if (there && i < units) {
-                d[u] = load_unit<TAIL>(a.dy + row * a.dy_stride, i, hidden);
-                h[u] = load_unit<TAIL>(a.h + row * a.h_stride, i, hidden);
-                if (a.dres != nullptr) r[u] = load_unit<TAIL>(a.dres + row * a.dres_stride, i, hidden);
+                const Unit<TAIL> at(i, hidden);
+                d[u] = at.template load<NT>(a.dy + row * a.dy_stride);
+                h[u] = at.template load<NT>(a.h + row * a.h_stride);
+                if (a.dres != nullptr) r[u] = at.template load<NT>(a.dres + row * a.dres_stride);
             }
         };
         if constexpr (kKeep) {
@@ -296,6 +308,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = t + u * threads;
+            Unit<TAIL> at(i, hidden);
+            // (hidden from the compiler, which would keep every unit's masks)
+            if constexpr (!kKeep) asm volatile("" : "+v"(at.skip));
             float dy[8], unit[8], w[8];
             if constexpr (!kKeep) load(u);
             Wide<E>::widen(d[u], dy);
@@ -306,13 +321,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = 0.0f;
-                if (i < units) load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w);
+                if (i < units) load_weight<E>(a.weight, a.weight_f32, Unit<TAIL>(i, hidden), w);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 unit[e] *= rstd;
                 acc[u][e] = fmaf(dy[e], unit[e], acc[u][e]);
-                sum = fmaf(dy[e] * w[e], unit[e], sum);
+                const float g = at.own(e) ? dy[e] * w[e] : 0.0f;
+                sum = fmaf(g, unit[e], sum);
             }
             if constexpr (!kKeep) {
                 // one unit at a time: the empty statement stops the compiler
@@ -338,11 +354,17 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = kept[u][e];
             } else {
-                load_weight<E, TAIL>(a.weight, a.weight_f32, i, hidden, w);
+                load_weight<E>(a.weight, a.weight_f32, Unit<TAIL>(i, hidden), w);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] += rstd * (dy[e] * w[e] - unit[e] * rstd * mean);
-            store_unit<TAIL>(a.dx + row * a.dx_stride, i, hidden, Wide<E>::narrow(f));
+            // (rows that are read twice may be overwritten between the reads
+            // of a shared value)
+            const Unit<TAIL> at(i, hidden);
+            if constexpr (kKeep)
+                at.template store<NT>(a.dx + row * a.dx_stride, Wide<E>::narrow(f));
+            else
+                at.template store_own<NT>(a.dx + row * a.dx_stride, Wide<E>::narrow(f));
             if constexpr (!kKeep) asm volatile("" ::: "memory");
         }
     }
@@ -351,8 +373,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
     if constexpr (L > 0) {
         // the row groups of the workgroup, added in order
         __shared__ float cols[4 * kWave * 8];       // 256 threads at most (launch)
+        const Unit<TAIL> at(t, hidden);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cols[threadIdx.x * 8 + e] = acc[0][e];
+        for (int e = 0; e < 8; ++e)
+            if (t < units && at.own(e)) cols[threadIdx.x / L * (L * 8) + at.start + e] = acc[0][e];
         __syncthreads();
         for (int c = threadIdx.x; c < hidden; c += blockDim.x) {
             float s = 0.0f;
@@ -364,9 +388,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
         for (int u = 0; u < U; ++u) {
             const int i = t + u * threads;
             if (i >= units) continue;
+            const Unit<TAIL> at(i, hidden);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (!TAIL || 8 * i + e < hidden) part[8 * i + e] = acc[u][e];
+                if (at.own(e)) part[at.start + e] = acc[u][e];
         }
     }
 }
@@ -416,38 +441,42 @@ RowShape row_shape(int hidden) {
     return {0, per, threads};
 }
 
-template <template <class, int, int, bool> class K, class E, class... A>
-hipError_t launch_rows(const RowShape &s, bool tail, unsigned grid, hipStream_t stream, const A &...args) {
-#define HR_ROWS(U, L)                                                                                      \
-    if (tail)                                                                                              \
-        hipLaunchKernelGGL((K<E, U, L, true>::kernel), dim3(grid), dim3(s.threads), 0, stream, args...);   \
-    else                                                                                                   \
-        hipLaunchKernelGGL((K<E, U, L, false>::kernel), dim3(grid), dim3(s.threads), 0, stream, args...);
-    if (s.lanes == 16) {
-        HR_ROWS(1, 16)
-    } else if (s.lanes == 32) {
-        HR_ROWS(1, 32)
-    } else if (s.lanes == 64) {
-        HR_ROWS(1, 64)
-    } else if (s.units == 1) {
-        HR_ROWS(1, 0)
-    } else if (s.units == 2) {
-        HR_ROWS(2, 0)
-    } else {
-        HR_ROWS(4, 0)
+// A call that moves this many bytes or more passes the caches by
+// (non-temporal loads and stores).  Measured cached and streamed: the fold of
+// 8 contributions of 2048 x 8192 (369 MB) 71.0 and 61.6 us, one of 4999 x 5120
+// with both outputs (230 MB) 49.2 and 44.1, the gradient of 8192 x 4096 (268
+// MB) 53.3 and 49.4; the norm of 65536 x 128 (34 MB) 9.6 and 9.7, its gradient
+// of 65537 x 128 (50 MB) 13.3 and 14.4.
+constexpr size_t kStreamBytes = size_t(1) << 27;
+
+template <template <class, int, int, bool, bool> class K, class E, class A>
+hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, hipStream_t stream, const A &args) {
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(s.threads), 0, stream, args);
+        return hipGetLastError();
+    };
+#define HR_VARIANT(U, L)                                                                        \
+    (tail ? (nt ? K<E, U, L, true, true>::kernel : K<E, U, L, true, false>::kernel)             \
+          : (nt ? K<E, U, L, false, true>::kernel : K<E, U, L, false, false>::kernel))
+    switch (s.lanes) {
+        case 16: return go(HR_VARIANT(1, 16));
+        case 32: return go(HR_VARIANT(1, 32));
+        case 64: return go(HR_VARIANT(1, 64));
     }
-#undef HR_ROWS
-    return hipGetLastError();
+    if (s.units == 1) return go(HR_VARIANT(1, 0));
+    if (s.units == 2) return go(HR_VARIANT(2, 0));
+    return go(HR_VARIANT(4, 0));
+#undef HR_VARIANT
 }
 
-template <class E, int U, int L, bool TAIL>
+template <class E, int U, int L, bool TAIL, bool NT>
 struct NormKernel {
-    static constexpr auto kernel = norm_rows<E, U, L, TAIL>;
+    static constexpr auto kernel = norm_rows<E, U, L, TAIL, NT>;
 };
 
-template <class E, int U, int L, bool TAIL>
+template <class E, int U, int L, bool TAIL, bool NT>
 struct NormGradKernel {
-    static constexpr auto kernel = norm_grad_rows<E, U, L, TAIL>;
+    static constexpr auto kernel = norm_grad_rows<E, U, L, TAIL, NT>;
 };
 
 constexpr size_t kMaxRows = 0x7FFFFFFF;
@@ -549,8 +578,9 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     a.group_lanes = q->group / 8;
     a.eps = q->eps;
 
-    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, static_cast<unsigned>(groups_of(rows, s)),
-                                                    reinterpret_cast<hipStream_t>(stream), a);
+    const size_t arrays = a.n + (a.h != nullptr) + (a.out != nullptr) + (a.codes != nullptr);
+    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, rows * hidden * 2 * arrays >= kStreamBytes,
+                                                    groups_of(rows, s), reinterpret_cast<hipStream_t>(stream), a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
@@ -608,8 +638,9 @@ hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
     float *part = parts == 1 ? q->dweight : static_cast<float *>(q->workspace);
     a.part = q->dweight != nullptr ? part : nullptr;
     if (rows > 0) {
+        const size_t arrays = 3 + (a.dres != nullptr);
         const hipError_t e = launch_rows<NormGradKernel, E>(row_shape(a.hidden), hidden % 8 != 0,
-                                                            static_cast<unsigned>(parts), st, a);
+                                                            rows * hidden * 2 * arrays >= kStreamBytes, parts, st, a);
         if (e != hipSuccess) return HR_ERR_HIP;
     }
     if (q->dweight != nullptr && parts != 1) {

@@ -85,20 +85,38 @@ struct Logits16 {
     static __device__ __forceinline__ void load(const void *row, int e0, int n, float (&x)[R]) {
 #pragma unroll
         for (int q = 0; q < R / 8; ++q) {
-            float f[8];
-            Wide<E>::widen(load_unit<true>(static_cast<const uint16_t *>(row), e0 / 8 + q, n), f);
+            const int e = e0 + 8 * q;
+            u32x4 v = {0, 0, 0, 0};
+            const uint16_t *p = static_cast<const uint16_t *>(row) + e;
+            if (e + 8 <= n) {
+                v = load_vec<false>(p);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[8 * q + i] = e0 + 8 * q + i < n ? f[i] : -INFINITY;
+                for (int i = 0; i < 7; ++i) v[i / 2] |= e + i < n ? static_cast<uint32_t>(p[i]) << (16 * (i & 1)) : 0u;
+            }
+            float f[8];
+            Wide<E>::widen(v, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[8 * q + i] = e + i < n ? f[i] : -INFINITY;
         }
     }
     template <int R>
     static __device__ __forceinline__ void store(void *row, int e0, int n, const float (&x)[R]) {
 #pragma unroll
         for (int q = 0; q < R / 8; ++q) {
+            const int e = e0 + 8 * q;
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = x[8 * q + i];
-            store_unit<true>(static_cast<uint16_t *>(row), e0 / 8 + q, n, Wide<E>::narrow(f));
+            const u32x4 v = Wide<E>::narrow(f);
+            uint16_t *p = static_cast<uint16_t *>(row) + e;
+            if (e + 8 <= n) {
+                store_vec<false>(v, p);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (e + i < n) p[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+            }
         }
     }
 };

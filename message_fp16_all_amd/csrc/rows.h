@@ -15,6 +15,7 @@ namespace hr {
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_row __attribute__((aligned(1)));
+typedef uint32_t u32_row __attribute__((aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4_row __attribute__((aligned(4)));
@@ -104,30 +105,75 @@ __device__ __forceinline__ void store_vec(u32x4 v, void *p) {
         *static_cast<u32x4_byte *>(p) = v;
 }
 
-// Unit i of a row of n values; values past the row's end read as zero bits.
+// Where unit i of a row of n values lies.  The last unit of a row that is not
+// a whole number of units (TAIL) starts 8 values before the row's end: its
+// first `skip` values belong to its neighbour too.  So every unit is one
+// access, with nothing to put together value by value (a row of fewer than 8
+// values excepted), and both owners compute the same values for what they
+// share; only sums have to leave it out.
 // Offsets are unsigned 32-bit: added to a wave-uniform row address they need
 // one register.
-template <bool TAIL, bool NT = false>
-__device__ __forceinline__ u32x4 load_unit(const uint16_t *row, int i, int n) {
-    if (!TAIL || 8 * i + 8 <= n)
-        return load_vec<NT>(reinterpret_cast<const char *>(row) + 16u * i);
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (8 * i + e < n) v[e / 2] |= static_cast<uint32_t>(row[8 * i + e]) << (16 * (e & 1));
-    return v;
-}
-
-template <bool TAIL, bool NT = false>
-__device__ __forceinline__ void store_unit(uint16_t *row, int i, int n, u32x4 v) {
-    if (!TAIL || 8 * i + 8 <= n) {
-        store_vec<NT>(v, reinterpret_cast<char *>(row) + 16u * i);
-        return;
+template <bool TAIL>
+struct Unit {
+    uint32_t start;
+    int skip, n;
+    __device__ __forceinline__ Unit(int i, int n) : start(8u * i), skip(0), n(n) {
+        if constexpr (TAIL) {
+            if (8 * i + 8 > n && n >= 8) {
+                start = n - 8;
+                skip = 8 * i + 8 - n;
+            }
+        }
     }
+    // Value e of the unit is this unit's own.
+    __device__ __forceinline__ bool own(int e) const { return !TAIL || (e >= skip && static_cast<int>(start) + e < n); }
+
+    template <bool NT = false>
+    __device__ __forceinline__ u32x4 load(const uint16_t *row) const {
+        if (!TAIL || n >= 8) return load_vec<NT>(reinterpret_cast<const char *>(row) + 2u * start);
+        u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (8 * i + e < n) row[8 * i + e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
-}
+        for (int e = 0; e < 7; ++e) v[e / 2] |= e < n ? static_cast<uint32_t>(row[e]) << (16 * (e & 1)) : 0u;
+        return v;
+    }
+    // The whole unit: where no other thread still reads what it shares.
+    template <bool NT = false>
+    __device__ __forceinline__ void store(uint16_t *row, u32x4 v) const {
+        if (!TAIL || n >= 8)
+            store_vec<NT>(v, reinterpret_cast<char *>(row) + 2u * start);
+        else
+            store_own<false>(row, v);
+    }
+    // The unit's own values.
+    template <bool NT = false>
+    __device__ __forceinline__ void store_own(uint16_t *row, u32x4 v) const {
+        if (!TAIL || (n >= 8 && skip == 0)) {
+            store_vec<NT>(v, reinterpret_cast<char *>(row) + 2u * start);
+            return;
+        }
+        // n % 8 values, in pieces of 4, 2 and 1
+        uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+        const int rest = n & 7, drop = n >= 8 ? 16 * (8 - rest) : 0;
+        if (drop >= 64) {
+            lo = hi >> (drop - 64);
+        } else if (drop > 0) {
+            lo = lo >> drop | hi << (64 - drop);
+            hi >>= drop;
+        }
+        char *p = reinterpret_cast<char *>(row) + 2u * (n - rest);
+        if (rest & 4) {
+            *reinterpret_cast<u32x2_row *>(p) = u32x2{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32)};
+            lo = hi;
+            p += 8;
+        }
+        if (rest & 2) {
+            *reinterpret_cast<u32_row *>(p) = static_cast<uint32_t>(lo);
+            lo >>= 32;
+            p += 4;
+        }
+        if (rest & 1) *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(lo);
+    }
+};
 
 // Reductions over groups of L consecutive lanes (L a power of two up to 64),
 // every lane receiving the result: data-parallel primitives inside a row of
