@@ -592,6 +592,8 @@ HR_API size_t hr_decode_numel(size_t max_batch, size_t tokens_per_request, size_
 
 /* Largest row of hr_reduce_rmsnorm and its gradient, in values. */
 #define HR_RMSNORM_MAX_HIDDEN 32768u
+/* Up to this many rows the gradient needs no workspace, unless dx is dy or h. */
+#define HR_RMSNORM_GRAD_FEW_ROWS 256
 
 typedef struct {
     const void *inputs[HR_MAX_G]; /* G contributions, rows x hidden values each   */
@@ -655,7 +657,8 @@ typedef struct {
     void *dx;                 /* gradient of h                                    */
     float *dweight;           /* hidden sums; NULL = not wanted                   */
     void *workspace;          /* hr_rmsnorm_grad_workspace bytes, 4-byte aligned,
-                                 needed with dweight                              */
+                                 needed with dweight (but see
+                                 HR_RMSNORM_GRAD_FEW_ROWS)                        */
     size_t workspace_bytes;
     size_t rows, hidden;
     size_t dy_stride, h_stride, dresidual_stride, dx_stride;   /* values; 0 = hidden */

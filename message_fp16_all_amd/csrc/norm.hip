@@ -248,7 +248,48 @@ struct NormGradArgs {
     size_t dy_stride, h_stride, dres_stride, dx_stride;
     int hidden;
     int weight_f32;
+    uint32_t row_groups;             // workgroups for rows; the others sum columns
+    float *dweight;                  // of these others
 };
+
+// Few rows: dweight = sum over the rows of dy * h * rstd without partial sums
+// in memory.  A workgroup takes 128 columns (16 lanes of one unit), its groups
+// of 16 lanes every so many rows, and the groups' sums are added in order.
+// It reads dy and h once more, from the caches.
+constexpr int kColumns = 128;
+
+template <class E, bool TAIL>
+__device__ __forceinline__ void sum_few_rows(const NormGradArgs &a) {
+    extern __shared__ float cols[];                 // [groups][kColumns]
+    const int groups = blockDim.x / 16, group = threadIdx.x / 16;
+    const int i = static_cast<int>(blockIdx.x - a.row_groups) * 16 + threadIdx.x % 16;
+    const Unit<TAIL> at(i, a.hidden);
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    if (8 * i < a.hidden) {
+#pragma unroll 4
+        for (size_t row = group; row < a.rows; row += groups) {
+            float dy[8], h[8];
+            Wide<E>::widen(at.load(a.dy + row * a.dy_stride), dy);
+            Wide<E>::widen(at.load(a.h + row * a.h_stride), h);
+            const float rstd = a.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(dy[e], h[e] * rstd, acc[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cols[group * kColumns + (threadIdx.x % 16) * 8 + e] = acc[e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < kColumns; c += blockDim.x) {
+        float s = cols[c];
+        for (int g = 1; g < groups; ++g) s += cols[g * kColumns + c];
+        const int first = static_cast<int>(blockIdx.x - a.row_groups) * kColumns;
+        // a last unit lies before its place in the workgroup's columns
+        const Unit<TAIL> u(first / 8 + c / 8, a.hidden);
+        if (first / 8 * 8 + c / 8 * 8 < a.hidden && u.own(c % 8)) a.dweight[u.start + c % 8] = s;
+    }
+}
 
 // dx = rstd * (g - u * mean(g u)) + dres with g = dy * weight, u = h * rstd,
 // and this workgroup's sum over its rows of dy * u.  Rows are dealt out to the
@@ -256,11 +297,15 @@ struct NormGradArgs {
 // columns' sums in registers from its first row to its last.
 template <class E, int U, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a) {
+    if (blockIdx.x >= a.row_groups) {
+        sum_few_rows<E, TAIL>(a);
+        return;
+    }
     __shared__ float sums[2][kNormMaxWaves];
     const int threads = L > 0 ? L : static_cast<int>(blockDim.x);
     const int t = L > 0 ? static_cast<int>(threadIdx.x) % L : static_cast<int>(threadIdx.x);
     const int per = L > 0 ? static_cast<int>(blockDim.x) / (L > 0 ? L : 1) : 1;
-    const size_t step = static_cast<size_t>(gridDim.x) * per;
+    const size_t step = static_cast<size_t>(a.row_groups) * per;
     const int hidden = a.hidden;
     const int units = (hidden + 7) / 8;
 
@@ -396,26 +441,28 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
     }
 }
 
-// out[c] = sum over p of part[p][c], in a fixed order: 16 waves of a workgroup
-// take 64 columns, each wave every 16th row, and the waves' sums are added in
-// order.
-constexpr int kColumnWaves = 16;
+// out[c] = sum over p of part[p][c], in a fixed order: a workgroup takes C
+// columns, its groups of C lanes every so many rows, and the groups' sums are
+// added in order.  Fewer columns to a workgroup make more workgroups of short
+// rows.
+constexpr int kColumnThreads = 1024;
 
-__global__ __launch_bounds__(kColumnWaves *kWave) void sum_columns(const float *part, size_t parts, int hidden,
-                                                                   float *out) {
-    __shared__ float sums[kColumnWaves][kWave];
-    const int c = static_cast<int>(blockIdx.x) * kWave + threadIdx.x % kWave;
-    const int wave = threadIdx.x / kWave;
+template <int C>
+__global__ __launch_bounds__(kColumnThreads) void sum_columns(const float *part, size_t parts, int hidden, float *out) {
+    constexpr int kGroups = kColumnThreads / C;
+    __shared__ float sums[kGroups][C];
+    const int c = static_cast<int>(blockIdx.x) * C + threadIdx.x % C;
+    const int group = threadIdx.x / C;
     float s = 0.0f;
     if (c < hidden) {
 #pragma unroll 8
-        for (size_t p = wave; p < parts; p += kColumnWaves) s += part[p * hidden + c];
+        for (size_t p = group; p < parts; p += kGroups) s += part[p * hidden + c];
     }
-    sums[wave][threadIdx.x % kWave] = s;
+    sums[group][threadIdx.x % C] = s;
     __syncthreads();
-    if (wave == 0 && c < hidden) {
+    if (group == 0 && c < hidden) {
         s = sums[0][threadIdx.x];
-        for (int k = 1; k < kColumnWaves; ++k) s += sums[k][threadIdx.x];
+        for (int k = 1; k < kGroups; ++k) s += sums[k][threadIdx.x];
         out[c] = s;
     }
 }
@@ -450,9 +497,10 @@ RowShape row_shape(int hidden) {
 constexpr size_t kStreamBytes = size_t(1) << 27;
 
 template <template <class, int, int, bool, bool> class K, class E, class A>
-hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, hipStream_t stream, const A &args) {
+hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, size_t lds, hipStream_t stream,
+                       const A &args) {
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(s.threads), 0, stream, args);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(s.threads), lds, stream, args);
         return hipGetLastError();
     };
 #define HR_VARIANT(U, L)                                                                        \
@@ -486,12 +534,19 @@ size_t groups_of(size_t rows, const RowShape &s) {
     return (rows + per - 1) / per;
 }
 
-// Workgroups of the gradient, hence partial sums: two per compute unit at most.
-constexpr int kGradGroupsPerCu = 2;
-
+// Workgroups of the gradient, hence partial sums of dweight.  Up to four on a
+// compute unit and 16 waves (8 where a workgroup takes several rows at once),
+// but with eight rows or more to each, so that the partial sums stay small
+// beside the rows.  (16384 x 1024 with 512, 1024 and 2048 workgroups: 40, 30
+// and 34 us; 4097 x 5120 with 256 and 512: 41 and 35; 2048 x 8192 with 256, 512
+// and 1024: 32, 33 and 36.)
 size_t grad_groups(size_t rows, int hidden, int cus) {
-    const size_t groups = groups_of(rows, row_shape(hidden));
-    const size_t cap = static_cast<size_t>(cus) * kGradGroupsPerCu;
+    const RowShape s = row_shape(hidden);
+    const size_t groups = groups_of(rows, s);
+    const int fit = (s.lanes > 0 ? 8 : 16) * kWave / s.threads;
+    const size_t most = static_cast<size_t>(cus) * (fit < 1 ? 1 : fit < 4 ? fit : 4);
+    const size_t deep = groups / 8 > static_cast<size_t>(cus) ? groups / 8 : static_cast<size_t>(cus);
+    const size_t cap = deep < most ? deep : most;
     return groups < cap ? groups : cap;
 }
 
@@ -580,7 +635,7 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
 
     const size_t arrays = a.n + (a.h != nullptr) + (a.out != nullptr) + (a.codes != nullptr);
     const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, rows * hidden * 2 * arrays >= kStreamBytes,
-                                                    groups_of(rows, s), reinterpret_cast<hipStream_t>(stream), a);
+                                                    groups_of(rows, s), 0, reinterpret_cast<hipStream_t>(stream), a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
@@ -606,16 +661,20 @@ hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
         return HR_ERR_ALIGNMENT;
 
     int dev = 0, cus = 0;
-    const size_t need = hr_rmsnorm_grad_workspace(rows, hidden);
+    const Region dx = {q->dx, rows, hidden * 2, a.dx_stride * 2};
+    const Region dy = {q->dy, rows, hidden * 2, a.dy_stride * 2}, h = {q->h, rows, hidden * 2, a.h_stride * 2};
+    const bool few = q->dweight != nullptr && rows > 0 && rows <= HR_RMSNORM_GRAD_FEW_ROWS &&
+                     !regions_overlap(dx, dy) && !regions_overlap(dx, h);
+    const size_t need = few ? 0 : hr_rmsnorm_grad_workspace(rows, hidden);
     if (q->dweight != nullptr && need > 0 && (q->workspace == nullptr || q->workspace_bytes < need))
         return HR_ERR_INVALID_ARG;
     const size_t used = q->dweight != nullptr ? need : 0;
-    const Region ins[] = {{q->dy, rows, hidden * 2, a.dy_stride * 2},
-                          {q->h, rows, hidden * 2, a.h_stride * 2},
+    const Region ins[] = {dy,
+                          h,
                           {q->dresidual, rows, hidden * 2, a.dres_stride * 2},
                           {q->weight, 1, hidden * (q->weight_f32 ? 4 : 2), 0},
                           {q->rstd, rows, 4, 4}};
-    const Region outs[] = {{q->dx, rows, hidden * 2, a.dx_stride * 2},
+    const Region outs[] = {dx,
                            {q->dweight, 1, hidden * 4, 0},
                            {q->workspace, 1, used, 0}};
     if (any_overlap(outs, 3, ins, 5, 0x1)) return HR_ERR_INVALID_ARG;
@@ -633,20 +692,35 @@ hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
     a.dx = static_cast<uint16_t *>(q->dx);
     a.rows = rows;
     a.hidden = static_cast<int>(hidden);
+    const RowShape s = row_shape(a.hidden);
+    const bool tail = hidden % 8 != 0;
+    if (few) {
+        const size_t groups = groups_of(rows, s), columns = (hidden + kColumns - 1) / kColumns;
+        a.row_groups = static_cast<uint32_t>(groups);
+        a.dweight = q->dweight;
+        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, false, groups + columns,
+                                                            s.threads / 16 * kColumns * sizeof(float), st, a);
+        return e == hipSuccess ? HR_OK : HR_ERR_HIP;
+    }
     const size_t parts = grad_groups(rows, a.hidden, cus);
     // a single workgroup's sums are the result
     float *part = parts == 1 ? q->dweight : static_cast<float *>(q->workspace);
     a.part = q->dweight != nullptr ? part : nullptr;
+    a.row_groups = static_cast<uint32_t>(parts);
     if (rows > 0) {
         const size_t arrays = 3 + (a.dres != nullptr);
-        const hipError_t e = launch_rows<NormGradKernel, E>(row_shape(a.hidden), hidden % 8 != 0,
-                                                            rows * hidden * 2 * arrays >= kStreamBytes, parts, st, a);
+        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, rows * hidden * 2 * arrays >= kStreamBytes, parts,
+                                                            0, st, a);
         if (e != hipSuccess) return HR_ERR_HIP;
     }
     if (q->dweight != nullptr && parts != 1) {
-        hipLaunchKernelGGL(sum_columns, dim3(static_cast<unsigned>((hidden + kWave - 1) / kWave)),
-                           dim3(kColumnWaves * kWave), 0, st, static_cast<const float *>(q->workspace), parts, a.hidden,
-                           q->dweight);
+        const int columns = hidden >= 4096 ? 64 : 16;
+        const dim3 grid(static_cast<unsigned>((hidden + columns - 1) / columns));
+        const float *sums = static_cast<const float *>(q->workspace);
+        if (columns == 64)
+            hipLaunchKernelGGL(sum_columns<64>, grid, dim3(kColumnThreads), 0, st, sums, parts, a.hidden, q->dweight);
+        else
+            hipLaunchKernelGGL(sum_columns<16>, grid, dim3(kColumnThreads), 0, st, sums, parts, a.hidden, q->dweight);
         if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
     }
     return HR_OK;

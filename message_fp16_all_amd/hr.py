@@ -67,6 +67,7 @@ HR_DTYPE_OTHER = 2
 HR_DTYPE_F32 = 3
 
 HR_RMSNORM_MAX_HIDDEN = 32768
+HR_RMSNORM_GRAD_FEW_ROWS = 256
 HR_ROUTER_MAX_EXPERTS = 1024
 HR_ROUTER_MAX_K = 32
 HR_ROUTER_MAX_TOKENS = (1 << 26) - 4
@@ -712,7 +713,7 @@ def rmsnorm_grad(dy, h, rstd, dx, *, weight=None, dresidual=None, dweight=None, 
     wp, wf = _weight_ptr(weight, dt, hidden)
     if dweight is not None:
         gp = _flat_ptr(dweight, "dweight", _torch.float32, hidden)
-        if workspace is None:
+        if workspace is None and (rows > HR_RMSNORM_GRAD_FEW_ROWS or xp == yp or xp == hp):
             need = load().hr_rmsnorm_grad_workspace(rows, hidden)
             if need:
                 workspace = _scratch(need, h, stream)

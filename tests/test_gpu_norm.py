@@ -289,6 +289,28 @@ def test_grad_strides(dt, hidden, stride, offset):
 def test_grad_in_place(what):
     for hidden in (128, 4096, 20000):
         run_grad(3, "f16", 700, hidden, in_place=what)
+        run_grad(4, "bf16", 100, hidden + 1, in_place=what)
+        run_grad(5, "f16", 100, hidden, in_place=what, workspace=False)
+
+
+def test_grad_of_few_rows_takes_no_workspace():
+    """Up to HR_RMSNORM_GRAD_FEW_ROWS rows dweight is summed beside dx, and a row more is not."""
+    limit = hr.HR_RMSNORM_GRAD_FEW_ROWS
+    for rows in (1, 15, 17, limit - 1, limit):
+        for hidden in (7, 128, 129, 1000, 4100):
+            run_grad(rows, "bf16", rows, hidden, weight="f32", workspace=False)
+    h = torch.ones(limit + 1, 1024, dtype=torch.float16, device="cuda:0")
+    args = [t.data_ptr() for t in (h, h)]
+    a = hr.hr_rmsnorm_grad_args()
+    dx, dw, rstd = torch.empty_like(h), torch.empty(1024, device="cuda:0"), torch.ones(limit + 1, device="cuda:0")
+    a.dy, a.h, a.rstd, a.dx, a.dweight = *args, rstd.data_ptr(), dx.data_ptr(), dw.data_ptr()
+    a.hidden = 1024
+    for rows, into, status in ((limit, dx, hr.HR_OK), (limit + 1, dx, hr.HR_ERR_INVALID_ARG),
+                               (limit, h, hr.HR_ERR_INVALID_ARG)):
+        a.rows, a.dx = rows, into.data_ptr()
+        assert hr.hr_rmsnorm_grad_f16(a, torch.cuda.current_stream().cuda_stream) == status
+    torch.cuda.synchronize()
+    assert (dw == limit).all()
 
 
 def test_grad_is_the_same_every_time():
