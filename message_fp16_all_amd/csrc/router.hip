@@ -48,6 +48,7 @@ __device__ __forceinline__ float exp_down(float d) {
 // logits' order: 0 for a logit that is never picked.
 struct Logits32 {
     static constexpr size_t kBytes = 4;
+    static constexpr bool kPacked = false;
     template <int R>
     static __device__ __forceinline__ void load(const void *row, int e0, int n, float (&x)[R]) {
         const float *p = static_cast<const float *>(row) + e0;
@@ -81,6 +82,18 @@ struct Logits32 {
 template <class E>
 struct Logits16 {
     static constexpr size_t kBytes = 2;
+    static constexpr bool kPacked = true;
+    // The 16 bits that order_key's upper half came from.
+    static __device__ __forceinline__ float value(uint32_t u) {
+        const uint32_t b = u & 0x8000u ? u ^ 0x8000u : ~u & 0xFFFFu;
+        return Wide<E>::widen1(static_cast<uint16_t>(b));
+    }
+    // The order of a 16-bit logit, as order_key: 16 bits, 0 = never picked.
+    static __device__ __forceinline__ uint32_t order(float x) {
+        const uint32_t b = Wide<E>::narrow1(x + 0.0f);          // exact; -0 as +0
+        const uint32_t u = b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
+        return x > -INFINITY ? u : 0u;
+    }
     template <int R>
     static __device__ __forceinline__ void load(const void *row, int e0, int n, float (&x)[R]) {
 #pragma unroll
@@ -145,36 +158,64 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     for (int r = 0; r < R; ++r) x[r] = -INFINITY;
     if (there && e0 < a.experts)
         T::load(static_cast<const char *>(a.logits) + token * a.stride * T::kBytes, e0, a.experts, x);
-    uint32_t key[R];
+    // the picks, lane j keeping pick j, and the largest logit
+    float top = 0.0f, v = 0.0f;
+    int id = -1;
+    if constexpr (T::kPacked) {
+        // Order and index in one number, so that no two are equal.  The next
+        // pick is the largest key below the last one, that is the largest
+        // difference to it modulo 2^32: nothing has to be taken out.
+        uint32_t key[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) key[r] = order_key(x[r]);
-
-    uint32_t best = 0;         // the largest key: the softmax's reference
-    uint32_t my_key = 0;       // lane j keeps pick j
-    int my_id = -1;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t m = key[0];
+        for (int r = 0; r < R; ++r) {
+            const uint32_t u = T::order(x[r]);
+            key[r] = u != 0 ? u << 16 | (0xFFFFu - (e0 + r)) : 0u;
+        }
+        uint32_t last = 0, first = 0, mine = 0;
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t m = key[0] - last;
 #pragma unroll
-        for (int r = 1; r < R; ++r) m = m > key[r] ? m : key[r];
-        m = max_lanes<L>(m);
-        // the lowest index with that key: as the largest complement
-        uint32_t at = 0;
+            for (int r = 1; r < R; ++r) {
+                const uint32_t d = key[r] - last;
+                m = m > d ? m : d;
+            }
+            m = max_lanes<L>(m) + last;
+            last = j > 0 && last == 0 ? 0u : m;                 // nothing was left
+            first = j == 0 ? last : first;
+            mine = t == j ? last : mine;
+        }
+        top = T::value(first >> 16);
+        if (mine != 0) {
+            v = T::value(mine >> 16);
+            id = static_cast<int>(0xFFFFu - (mine & 0xFFFFu));
+        }
+    } else {
+        uint32_t key[R];
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) at = key[r] == m ? ~static_cast<uint32_t>(e0 + r) : at;
-        const int id = static_cast<int>(~max_lanes<L>(at));
+        for (int r = 0; r < R; ++r) key[r] = order_key(x[r]);
+        uint32_t best = 0, mine = 0;
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t m = key[0];
 #pragma unroll
-        for (int r = 0; r < R; ++r) key[r] = e0 + r == id ? 0u : key[r];
-        best = j == 0 ? m : best;
-        my_key = t == j ? m : my_key;
-        my_id = t == j && m != 0 ? id : my_id;
+            for (int r = 1; r < R; ++r) m = m > key[r] ? m : key[r];
+            m = max_lanes<L>(m);
+            // the lowest index with that key: as the largest complement
+            uint32_t at = 0;
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) at = key[r] == m ? ~static_cast<uint32_t>(e0 + r) : at;
+            const int e = static_cast<int>(~max_lanes<L>(at));
+#pragma unroll
+            for (int r = 0; r < R; ++r) key[r] = e0 + r == e ? 0u : key[r];
+            best = j == 0 ? m : best;
+            mine = t == j ? m : mine;
+            id = t == j && m != 0 ? e : id;
+        }
+        top = key_value(best);
+        v = key_value(mine);
     }
 
-    const float top = key_value(best);
     float w = 0.0f;
-    if (my_key != 0) {
-        const float v = key_value(my_key);
-        w = v == top ? 1.0f : exp_down(v - top);      // equal infinities share the weight
-    }
+    if (id >= 0) w = v == top ? 1.0f : exp_down(v - top);       // equal infinities share the weight
     float total = 0.0f;
     if (a.renormalize) {
         total = sum_lanes<L>(w);
@@ -185,8 +226,8 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
         total = sum_lanes<L>(total);
     }
     if (there && t < a.k) {
-        a.weights[token * a.k + t] = my_key != 0 ? w / total : 0.0f;
-        a.ids[token * a.k + t] = my_id;
+        a.weights[token * a.k + t] = id >= 0 ? w / total : 0.0f;
+        a.ids[token * a.k + t] = id;
     }
 }
 
@@ -226,13 +267,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
         for (int r = 0; r < R; ++r) x[r] = -INFINITY;
         if (there && e0 < a.experts)
             T::load(static_cast<const char *>(a.logits) + token * a.stride * T::kBytes, e0, a.experts, x);
-        uint32_t m = 0;
+        float top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t u = order_key(x[r]);
-            m = m > u ? m : u;
-        }
-        const float top = key_value(max_lanes<L>(m));
+        for (int r = 0; r < R; ++r) top = fmaxf(top, x[r]);     // a NaN is no maximum
+        top = reduce_lanes<L>(top, [](float p, float q) { return fmaxf(p, q); });
         float total = 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {

@@ -179,10 +179,12 @@ struct Unit {
 // every lane receiving the result: data-parallel primitives inside a row of
 // 16 lanes, lane-row swaps beyond.  The tree is fixed, so sums are the same
 // in every run.
+// (Every lane has a source in the patterns below, so the value for lanes
+// without one does not matter; 0 lets the compiler fold the move into the
+// operation that follows.)
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xF, 0xF, false));
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
 
 template <int L, class T, class F>
