@@ -12,6 +12,9 @@
 //   renormalised: weights_j * (dweights_j - c) at the picks, 0 elsewhere
 #include "rows.h"
 
+#include <cfloat>
+#include <type_traits>
+
 namespace hr {
 
 constexpr int kRouterThreads = 256;
@@ -44,25 +47,45 @@ __device__ __forceinline__ float exp_down(float d) {
     return fmaf(p, r * kLn2, p);
 }
 
-// R consecutive logits of one lane, as keys whose unsigned order is the
-// logits' order: 0 for a logit that is never picked.
+// The order of a binary32 logit as an unsigned number; 0 = never picked.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);      // -0 as +0
+    const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    return x > -INFINITY ? u : 0u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t u) {
+    return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+// R consecutive logits of one lane as they lie in memory (Raw), widened, and
+// as keys.  What lies past the last logit reads as -infinity.
 struct Logits32 {
     static constexpr size_t kBytes = 4;
     static constexpr bool kPacked = false;
     template <int R>
-    static __device__ __forceinline__ void load(const void *row, int e0, int n, float (&x)[R]) {
+    struct Raw {
+        float x[R];
+    };
+    template <int R>
+    static __device__ __forceinline__ void load(const void *row, int e0, int n, Raw<R> &raw) {
         const float *p = static_cast<const float *>(row) + e0;
         if (e0 + R <= n) {
 #pragma unroll
             for (int q = 0; q < R / 4; ++q) {
                 const f32x4 v = *reinterpret_cast<const f32x4_row *>(p + 4 * q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * q + i] = v[i];
+                for (int i = 0; i < 4; ++i) raw.x[4 * q + i] = v[i];
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) x[r] = e0 + r < n ? p[r] : -INFINITY;
+            for (int r = 0; r < R; ++r) raw.x[r] = e0 + r < n ? p[r] : -INFINITY;
         }
+    }
+    template <int R>
+    static __device__ __forceinline__ void widen(const Raw<R> &raw, float (&x)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] = raw.x[r];
     }
     template <int R>
     static __device__ __forceinline__ void store(void *row, int e0, int n, const float (&x)[R]) {
@@ -83,34 +106,38 @@ template <class E>
 struct Logits16 {
     static constexpr size_t kBytes = 2;
     static constexpr bool kPacked = true;
-    // The 16 bits that order_key's upper half came from.
-    static __device__ __forceinline__ float value(uint32_t u) {
-        const uint32_t b = u & 0x8000u ? u ^ 0x8000u : ~u & 0xFFFFu;
-        return Wide<E>::widen1(static_cast<uint16_t>(b));
-    }
-    // The order of a 16-bit logit, as order_key: 16 bits, 0 = never picked.
-    static __device__ __forceinline__ uint32_t order(float x) {
-        const uint32_t b = Wide<E>::narrow1(x + 0.0f);          // exact; -0 as +0
-        const uint32_t u = b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
-        return x > -INFINITY ? u : 0u;
+    static constexpr uint32_t kInf = std::is_same<E, F16>::value ? 0x7C00u : 0x7F80u;
+    static constexpr uint32_t kNone = (0x8000u | kInf) * 0x10001u;
+    template <int R>
+    struct Raw {
+        uint32_t w[R / 2];           // two logits to a word
+    };
+    template <int R>
+    static __device__ __forceinline__ void load(const void *row, int e0, int n, Raw<R> &raw) {
+        const uint16_t *p = static_cast<const uint16_t *>(row) + e0;
+        if (e0 + R <= n) {
+#pragma unroll
+            for (int q = 0; q < R / 8; ++q) {
+                const u32x4 v = load_vec<false>(p + 8 * q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) raw.w[4 * q + i] = v[i];
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; r += 2) {
+                const uint32_t lo = e0 + r < n ? p[r] : kNone & 0xFFFFu, hi = e0 + r + 1 < n ? p[r + 1] : kNone >> 16;
+                raw.w[r / 2] = lo | hi << 16;
+            }
+        }
     }
     template <int R>
-    static __device__ __forceinline__ void load(const void *row, int e0, int n, float (&x)[R]) {
+    static __device__ __forceinline__ void widen(const Raw<R> &raw, float (&x)[R]) {
 #pragma unroll
         for (int q = 0; q < R / 8; ++q) {
-            const int e = e0 + 8 * q;
-            u32x4 v = {0, 0, 0, 0};
-            const uint16_t *p = static_cast<const uint16_t *>(row) + e;
-            if (e + 8 <= n) {
-                v = load_vec<false>(p);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 7; ++i) v[i / 2] |= e + i < n ? static_cast<uint32_t>(p[i]) << (16 * (i & 1)) : 0u;
-            }
             float f[8];
-            Wide<E>::widen(v, f);
+            Wide<E>::widen(u32x4{raw.w[4 * q], raw.w[4 * q + 1], raw.w[4 * q + 2], raw.w[4 * q + 3]}, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[8 * q + i] = e + i < n ? f[i] : -INFINITY;
+            for (int i = 0; i < 8; ++i) x[8 * q + i] = f[i];
         }
     }
     template <int R>
@@ -132,17 +159,46 @@ struct Logits16 {
             }
         }
     }
+    // A logit's order in the upper half of a word and its index's complement in
+    // the lower, so that no two are equal; 0 = never picked.  `bits` holds the
+    // logit in its upper half and zeros below.
+    static __device__ __forceinline__ uint32_t key(uint32_t bits, int e) {
+        bits = bits == 0x80000000u ? 0u : bits;                 // -0 as +0
+        const uint32_t u = bits ^ (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 31) | 0x80000000u);
+        // above -infinity (whose order is 0x7FFF - kInf) and up to +infinity
+        constexpr uint32_t kLow = (0x8000u - kInf) << 16, kHigh = (0x8000u | kInf) << 16 | 0xFFFFu;
+        return u - kLow <= kHigh - kLow ? (u & 0xFFFF0000u) | (0xFFFFu - e) : 0u;
+    }
+    template <int R>
+    static __device__ __forceinline__ void keys(const Raw<R> &raw, int e0, uint32_t (&k)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) k[r] = key(r & 1 ? raw.w[r / 2] & 0xFFFF0000u : raw.w[r / 2] << 16, e0 + r);
+    }
+    static __device__ __forceinline__ float value(uint32_t key) {
+        const uint32_t u = key >> 16;
+        return Wide<E>::widen1(static_cast<uint16_t>(u & 0x8000u ? u ^ 0x8000u : ~u));
+    }
 };
 
-// The order of a binary32 logit as an unsigned number; 0 = never picked.
-__device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);      // -0 as +0
-    const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return x > -INFINITY ? u : 0u;
-}
-
-__device__ __forceinline__ float key_value(uint32_t u) {
-    return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
+// exp(x - top) of R logits and their sum: 0 for -infinity and NaN, and for
+// everything where top is -infinity (nothing to pick); where top is +infinity,
+// 1 for each +infinity.
+template <int R>
+__device__ __forceinline__ float exp_all(float (&x)[R], float top) {
+    if (top == INFINITY) {
+        // the largest number in infinity's place: its difference to itself is 0
+        top = FLT_MAX;
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] = x[r] == INFINITY ? FLT_MAX : -INFINITY;
+    }
+    float total = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        // (a difference that is NaN or -infinity ends as an exponent that gives 0)
+        x[r] = exp_down(x[r] - top);
+        total += x[r];
+    }
+    return total;
 }
 
 // One token per L lanes; lane t holds the R logits t * R, t * R + 1, ..
@@ -153,24 +209,18 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     const size_t token = static_cast<size_t>(blockIdx.x) * kTokens + threadIdx.x / L;
     const bool there = token < a.tokens;
     const int e0 = t * R;
-    float x[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) x[r] = -INFINITY;
-    if (there && e0 < a.experts)
-        T::load(static_cast<const char *>(a.logits) + token * a.stride * T::kBytes, e0, a.experts, x);
+    typename T::template Raw<R> raw;
+    T::load(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, e0,
+            there ? a.experts : 0, raw);
+
     // the picks, lane j keeping pick j, and the largest logit
     float top = 0.0f, v = 0.0f;
     int id = -1;
     if constexpr (T::kPacked) {
-        // Order and index in one number, so that no two are equal.  The next
-        // pick is the largest key below the last one, that is the largest
-        // difference to it modulo 2^32: nothing has to be taken out.
+        // The next pick is the largest key below the last one, that is the
+        // largest difference to it modulo 2^32: nothing has to be taken out.
         uint32_t key[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t u = T::order(x[r]);
-            key[r] = u != 0 ? u << 16 | (0xFFFFu - (e0 + r)) : 0u;
-        }
+        T::keys(raw, e0, key);
         uint32_t last = 0, first = 0, mine = 0;
         for (int j = 0; j < a.k; ++j) {
             uint32_t m = key[0] - last;
@@ -184,15 +234,15 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
             first = j == 0 ? last : first;
             mine = t == j ? last : mine;
         }
-        top = T::value(first >> 16);
+        top = first != 0 ? T::value(first) : -INFINITY;
         if (mine != 0) {
-            v = T::value(mine >> 16);
+            v = T::value(mine);
             id = static_cast<int>(0xFFFFu - (mine & 0xFFFFu));
         }
     } else {
         uint32_t key[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) key[r] = order_key(x[r]);
+        for (int r = 0; r < R; ++r) key[r] = order_key(raw.x[r]);
         uint32_t best = 0, mine = 0;
         for (int j = 0; j < a.k; ++j) {
             uint32_t m = key[0];
@@ -210,23 +260,20 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
             mine = t == j ? m : mine;
             id = t == j && m != 0 ? e : id;
         }
-        top = key_value(best);
+        top = best != 0 ? key_value(best) : -INFINITY;
         v = key_value(mine);
     }
 
-    float w = 0.0f;
-    if (id >= 0) w = v == top ? 1.0f : exp_down(v - top);       // equal infinities share the weight
-    float total = 0.0f;
-    if (a.renormalize) {
-        total = sum_lanes<L>(w);
-    } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (x[r] > -INFINITY) total += x[r] == top ? 1.0f : exp_down(x[r] - top);
-        total = sum_lanes<L>(total);
+    float w[1] = {id >= 0 ? v : -INFINITY};
+    float total = exp_all(w, top);
+    if (!a.renormalize) {
+        float x[R];
+        T::widen(raw, x);
+        total = exp_all(x, top);
     }
+    total = sum_lanes<L>(total);
     if (there && t < a.k) {
-        a.weights[token * a.k + t] = id >= 0 ? w / total : 0.0f;
+        a.weights[token * a.k + t] = id >= 0 ? w[0] / total : 0.0f;
         a.ids[token * a.k + t] = id;
     }
 }
@@ -240,6 +287,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
     const size_t token = static_cast<size_t>(blockIdx.x) * kTokens + slot;
     const bool there = token < a.tokens;
     const int e0 = t * R;
+    typename T::template Raw<R> raw;
+    if (!a.renormalize)
+        T::load(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, e0,
+                there ? a.experts : 0, raw);
 #pragma unroll
     for (int r = 0; r < R; ++r) picked[slot][e0 + r] = 0.0f;
     int id = -1;
@@ -263,21 +314,12 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = picked[slot][e0 + r];
     } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = -INFINITY;
-        if (there && e0 < a.experts)
-            T::load(static_cast<const char *>(a.logits) + token * a.stride * T::kBytes, e0, a.experts, x);
+        T::widen(raw, x);
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < R; ++r) top = fmaxf(top, x[r]);     // a NaN is no maximum
         top = reduce_lanes<L>(top, [](float p, float q) { return fmaxf(p, q); });
-        float total = 0.0f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = x[r] > -INFINITY ? (x[r] == top ? 1.0f : exp_down(x[r] - top)) : 0.0f;
-            total += x[r];
-        }
-        total = sum_lanes<L>(total);
+        const float total = sum_lanes<L>(exp_all(x, top));
         const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = x[r] * inv * (picked[slot][e0 + r] - c);

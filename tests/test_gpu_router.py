@@ -133,6 +133,8 @@ def test_masked_and_special(dt, renormalize):
     x[10, 39] = big
     x[11, :39] = -inf
     run(x, 6, renormalize, "special")
+    x[:, 1], x[:, 30] = inf, big                                # the largest finite value beside an infinity
+    run(x, 6, renormalize, "largest")
 
 
 @pytest.mark.parametrize("dt,stride,offset", [("f16", 201, 1), ("bf16", 256, 3), ("f32", 199, 1), ("f32", 203, 2)])
