@@ -23,7 +23,7 @@ constexpr int kMaxSortThreads = 1024;
 struct SortArgs {
     const int32_t *ids;
     int32_t *offsets, *order, *pos;
-    int32_t *counts;         // [blocks][experts], then [experts]: totals
+    int32_t *counts;         // [blocks][experts]
     uint32_t slots, rows;
     uint32_t chunk;          // slots per workgroup
     int first, experts, pad;
@@ -88,19 +88,26 @@ __device__ __forceinline__ void place_share(const SortArgs &a, uint32_t begin, u
     }
 }
 
-// Inclusive sums of v over the workgroup's threads, through `tmp` (a value per
-// thread); every thread of the workgroup calls it.
-__device__ __forceinline__ int scan_threads(int v, int *tmp) {
-    const int t = threadIdx.x, n = blockDim.x;
-    tmp[t] = v;
-    __syncthreads();
-    for (int d = 1; d < n; d *= 2) {
-        const int before = t >= d ? tmp[t - d] : 0;
-        __syncthreads();
-        tmp[t] += before;
-        __syncthreads();
+// Inclusive sums of v over the workgroup's threads, and their total; `tmp`
+// holds a value per wave.  Every thread of the workgroup calls it, with a
+// barrier between two calls on the same `tmp`.
+__device__ __forceinline__ int scan_threads(int v, int *tmp, int *total) {
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int before = __shfl_up(v, d);
+        v += lane >= d ? before : 0;
     }
-    return tmp[t];
+    if (lane == kWave - 1) tmp[wave] = v;
+    __syncthreads();
+    int sum = 0;
+    for (int w = 0; w < waves; ++w) {
+        const int n = tmp[w];
+        v += w < wave ? n : 0;
+        sum += n;
+    }
+    *total = sum;
+    return v;
 }
 
 __device__ __forceinline__ int padded(int count, int pad) { return (count + pad - 1) / pad * pad; }
@@ -119,7 +126,7 @@ __device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offse
 }
 
 // Everything in one workgroup.  Dynamic LDS: [waves][experts] counts, then
-// [experts + 1] offsets, [experts] totals and [threads] for the scan.
+// [experts + 1] offsets, [experts] totals and [waves] for the scan.
 __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
     extern __shared__ int lds[];
     const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave;
@@ -136,7 +143,8 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
         int sum = 0;
         if (x < a.experts)
             for (int w = 0; w < waves; ++w) sum += counts[w * a.experts + x];
-        const int end = base + scan_threads(padded(sum, a.pad), tmp);
+        int all = 0;
+        const int end = base + scan_threads(padded(sum, a.pad), tmp, &all);
         if (x < a.experts) {
             int at = end - padded(sum, a.pad);
             totals[x] = sum;
@@ -148,7 +156,7 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
                 at += n;
             }
         }
-        base += tmp[blockDim.x - 1];
+        base += all;
         __syncthreads();
     }
     for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) a.offsets[i] = offsets[i];
@@ -156,7 +164,7 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
     fill_padding(a, offsets, totals);
 }
 
-// The same over many workgroups, in three kernels.  Dynamic LDS: [experts].
+// The same over many workgroups: counts, then places.  Dynamic LDS: [experts].
 __global__ __launch_bounds__(kMaxSortThreads) void sort_count(SortArgs a) {
     extern __shared__ int lds[];
     for (int i = threadIdx.x; i < a.experts; i += blockDim.x) lds[i] = 0;
@@ -171,61 +179,67 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_count(SortArgs a) {
     for (int i = threadIdx.x; i < a.experts; i += blockDim.x) a.counts[blockIdx.x * a.experts + i] = lds[i];
 }
 
-// One workgroup: counts[b][e] become the place of workgroup b's first slot of
-// expert e, counts[blocks][e] the totals.  A thread takes one expert and one
-// of `parts` runs of workgroups.
-__global__ __launch_bounds__(kMaxSortThreads) void sort_scan(SortArgs a) {
-    __shared__ int sums[kMaxSortThreads], tmp[kMaxSortThreads], starts[kMaxSortThreads];
-    int wide = 1;
-    while (wide < a.experts || wide < 16) wide *= 2;
-    const int x = threadIdx.x % wide, part = threadIdx.x / wide, parts = kMaxSortThreads / wide;
-    const int per = (a.blocks + parts - 1) / parts;
-    const int b0 = part * per < a.blocks ? part * per : a.blocks, b1 = b0 + per < a.blocks ? b0 + per : a.blocks;
-    int sum = 0;
-    if (x < a.experts)
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) sum += a.counts[b * a.experts + x];
-    sums[threadIdx.x] = sum;
-    __syncthreads();
-    int total = 0, before = 0;
-    for (int p = 0; p < parts; ++p) {
-        before = p == part ? total : before;
-        total += sums[p * wide + x];
-    }
-    const bool first = part == 0 && x < a.experts;
-    const int size = padded(total, a.pad);
-    const int end = scan_threads(first ? size : 0, tmp);
-    if (first) {
-        starts[x] = end - size;
-        a.offsets[x] = end - size;
-        if (x == a.experts - 1) a.offsets[a.experts] = end;
-        a.counts[a.blocks * a.experts + x] = total;
-    }
-    __syncthreads();
-    if (x < a.experts) {
-        int at = starts[x] + before;
-        for (int b = b0; b < b1; ++b) {
-            const int n = a.counts[b * a.experts + x];
-            a.counts[b * a.experts + x] = at;
-            at += n;
-        }
-    }
-}
-
-// Dynamic LDS: [waves][experts].
+// Every workgroup adds the counts of all of them up by itself.  Measured
+// against a kernel of one workgroup between the two: 65528 slots of 128
+// experts 10.4 against 12.9 us, 2^20 slots of 256 experts 18.5 against 27.7.
+// Dynamic LDS: [waves][experts] counts, then [experts + 1] offsets, [experts]
+// totals, [experts] firsts, [threads] sums and [waves].
 __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
     extern __shared__ int lds[];
-    const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave;
-    for (int i = threadIdx.x; i < waves * a.experts; i += blockDim.x) lds[i] = 0;
+    const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave, threads = blockDim.x;
+    int *offsets = lds + waves * a.experts, *totals = offsets + a.experts + 1, *firsts = totals + a.experts,
+        *sums = firsts + a.experts, *tmp = sums + threads;
+    for (int i = threadIdx.x; i < waves * a.experts; i += threads) lds[i] = 0;
     __syncthreads();
     const uint32_t begin = blockIdx.x * a.chunk;
     const uint32_t end = begin + a.chunk < a.slots ? begin + a.chunk : a.slots;
     uint32_t b, e;
     wave_share(begin, end, wave, waves, &b, &e);
     count_share(a, b, e, lds + wave * a.experts);
-    __syncthreads();
-    for (int x = threadIdx.x; x < a.experts; x += blockDim.x) {
-        int at = a.counts[blockIdx.x * a.experts + x];
+
+    // a thread takes one expert and a run [b0, b1) of workgroups, `parts` runs
+    // to an expert; more experts than threads take turns
+    int wide = 16;
+    while (wide < a.experts && wide < threads) wide *= 2;
+    const int part = threadIdx.x / wide, parts = threads / wide, per = (a.blocks + parts - 1) / parts;
+    const int b0 = part * per < a.blocks ? part * per : a.blocks, b1 = b0 + per < a.blocks ? b0 + per : a.blocks;
+    for (int e0 = 0, base = 0; e0 < a.experts; e0 += wide) {
+        const int x = e0 + threadIdx.x % wide;
+        int sum = 0, mine = 0;       // mine: of the workgroups before this one
+        if (x < a.experts) {
+#pragma unroll 8
+            for (int i = b0; i < b1; ++i) {
+                const int n = a.counts[i * a.experts + x];
+                sum += n;
+                mine += i < static_cast<int>(blockIdx.x) ? n : 0;
+            }
+        }
+        sums[threadIdx.x] = sum;
+        __syncthreads();
+        const bool first = part == 0 && x < a.experts;
+        int total = 0, all = 0;
+        if (first)
+            for (int p = 0; p < parts; ++p) total += sums[p * wide + x - e0];
+        const int size = padded(total, a.pad);
+        const int to = base + scan_threads(first ? size : 0, tmp, &all);
+        base += all;
+        __syncthreads();             // sums have been read
+        sums[threadIdx.x] = mine;
+        __syncthreads();
+        if (first) {
+            int at = to - size;
+            offsets[x] = at;
+            offsets[x + 1] = to;     // the same value as its neighbour's own
+            totals[x] = total;
+            for (int p = 0; p < parts; ++p) at += sums[p * wide + x - e0];
+            firsts[x] = at;
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= a.experts; i += threads) a.offsets[i] = offsets[i];
+    for (int x = threadIdx.x; x < a.experts; x += threads) {
+        int at = firsts[x];
         for (int w = 0; w < waves; ++w) {
             const int n = lds[w * a.experts + x];
             lds[w * a.experts + x] = at;
@@ -234,7 +248,7 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
     }
     __syncthreads();
     place_share(a, b, e, lds + wave * a.experts);
-    fill_padding(a, a.offsets, a.counts + static_cast<size_t>(a.blocks) * a.experts);
+    fill_padding(a, offsets, totals);
 }
 
 // --------------------------------------------------------------------- rows
@@ -671,7 +685,7 @@ extern "C" HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int exp
     if (!picks_ok(tokens, k, &slots) || experts < 1 || experts > HR_EXPERTS_MAX || slots > kMaxCount) return 0;
     if (slots <= kSortOnce) return 0;
     const size_t chunk = sort_chunk(slots);
-    return ((slots + chunk - 1) / chunk + 1) * static_cast<size_t>(experts) * 4;
+    return (slots + chunk - 1) / chunk * static_cast<size_t>(experts) * 4;
 }
 
 extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, int k, int first, int experts, int pad,
@@ -712,20 +726,22 @@ extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, i
     while ((1 << a.bits) <= experts) ++a.bits;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     // 16 waves' counts of up to 512 experts, or 8 waves' of up to 1024
-    const int threads = experts <= 512 ? 1024 : 512;
-    const size_t counts = static_cast<size_t>(threads / kWave) * experts * 4;
+    const int most_threads = experts <= 512 ? 1024 : 512;
+    const auto lds_for = [&](int threads, int arrays, int more) {
+        return (static_cast<size_t>(threads / kWave + arrays) * experts + 1 + more + threads / kWave) * sizeof(int);
+    };
     if (slots <= kSortOnce) {
-        const size_t lds = counts + (2 * static_cast<size_t>(experts) + 1 + threads) * 4;
-        hipLaunchKernelGGL(sort_once, dim3(1), dim3(threads), lds, s, a);
+        // a wave for every 64 slots, but no fewer than 4
+        int threads = 256;
+        while (threads < most_threads && threads < static_cast<int>(slots)) threads *= 2;
+        hipLaunchKernelGGL(sort_once, dim3(1), dim3(threads), lds_for(threads, 2, 0), s, a);
         return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
     }
     a.chunk = sort_chunk(slots);
     a.blocks = static_cast<int>((slots + a.chunk - 1) / a.chunk);
     hipLaunchKernelGGL(sort_count, dim3(a.blocks), dim3(kMaxSortThreads), static_cast<size_t>(experts) * 4, s, a);
     if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
-    hipLaunchKernelGGL(sort_scan, dim3(1), dim3(kMaxSortThreads), 0, s, a);
-    if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
-    hipLaunchKernelGGL(sort_place, dim3(a.blocks), dim3(threads), counts, s, a);
+    hipLaunchKernelGGL(sort_place, dim3(a.blocks), dim3(most_threads), lds_for(most_threads, 3, most_threads), s, a);
     return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 

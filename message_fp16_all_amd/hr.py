@@ -573,6 +573,7 @@ _NORM_GRAD = struct.Struct("@8P7Ni4x")
 _GATHER = struct.Struct("@7P8N2i")
 _COMBINE = struct.Struct("@5P6Ni4x")
 _COMBINE_GRAD = struct.Struct("@8P6N2i")
+_NULLS = [0] * HR_MAX_G
 _entries = {}
 
 
@@ -612,6 +613,15 @@ def _row_view(t, name: str, dtype, rows=None, width=None):
     if rows is not None and (r != rows or w != width):
         raise ValueError(f"{name}: {r} rows of {w} values, expected {rows} of {width}")
     return t.data_ptr(), r, w, sr
+
+
+def _rows_like(t, name: str, dtype, shape, rows: int, width: int):
+    """(address, row stride) of a device tensor of rows x width values; a
+    contiguous one of ``shape`` takes the short way."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr(), 0
+    p, _, _, s = _row_view(t, name, dtype, rows, width)
+    return p, s
 
 
 def _flat_ptr(t, name: str, dtype, numel: int) -> int:
@@ -662,23 +672,24 @@ def reduce_rmsnorm(tensors, out=None, *, residual=None, residual_out=None, weigh
     if len(tensors) > HR_MAX_G:
         raise ValueError(f"{len(tensors)} contributions, at most {HR_MAX_G}")
     p0, rows, hidden, stride = _row_view(first, "tensors[0]", dt)
+    shape = first.shape
     ptrs = [p0]
     for i in range(1, len(tensors)):
-        p, _, _, s = _row_view(tensors[i], f"tensors[{i}]", dt, rows, hidden)
+        p, s = _rows_like(tensors[i], f"tensors[{i}]", dt, shape, rows, hidden)
         if s != stride and (s or hidden) != (stride or hidden):
             raise ValueError(f"tensors[{i}]: row stride {s}, tensors[0] has {stride}")
         ptrs.append(p)
-    ptrs += [0] * (HR_MAX_G - len(ptrs))
+    ptrs += _NULLS[len(ptrs):]
     rp = hp = op = cp = sp = tp = 0
     rs = hs = os_ = cs = ss = 0
     if residual is not None:
-        rp, _, _, rs = _row_view(residual, "residual", dt, rows, hidden)
+        rp, rs = _rows_like(residual, "residual", dt, shape, rows, hidden)
     if residual_out is not None:
-        hp, _, _, hs = _row_view(residual_out, "residual_out", dt, rows, hidden)
+        hp, hs = _rows_like(residual_out, "residual_out", dt, shape, rows, hidden)
     if out is not None:
-        op, _, _, os_ = _row_view(out, "out", dt, rows, hidden)
+        op, os_ = _rows_like(out, "out", dt, shape, rows, hidden)
     if out8 is not None:
-        cp, _, _, cs = _row_view(out8, "out8", _torch.float8_e4m3fn, rows, hidden)
+        cp, cs = _rows_like(out8, "out8", _torch.float8_e4m3fn, shape, rows, hidden)
     if scales is not None:
         groups = -(-hidden // group) if group else 1
         if scales.dim() == 1 and groups == 1:
@@ -704,12 +715,13 @@ def rmsnorm_grad(dy, h, rstd, dx, *, weight=None, dresidual=None, dweight=None, 
     dt = h.dtype
     fn, name = _entry("hr_rmsnorm_grad", dt)
     hp, rows, hidden, hs = _row_view(h, "h", dt)
-    yp, _, _, ys = _row_view(dy, "dy", dt, rows, hidden)
-    xp, _, _, xs = _row_view(dx, "dx", dt, rows, hidden)
+    shape = h.shape
+    yp, ys = _rows_like(dy, "dy", dt, shape, rows, hidden)
+    xp, xs = _rows_like(dx, "dx", dt, shape, rows, hidden)
     tp = _flat_ptr(rstd, "rstd", _torch.float32, rows)
     rp = rs = gp = kp = kb = 0
     if dresidual is not None:
-        rp, _, _, rs = _row_view(dresidual, "dresidual", dt, rows, hidden)
+        rp, rs = _rows_like(dresidual, "dresidual", dt, shape, rows, hidden)
     wp, wf = _weight_ptr(weight, dt, hidden)
     if dweight is not None:
         gp = _flat_ptr(dweight, "dweight", _torch.float32, hidden)

@@ -27,7 +27,7 @@ def test_sizes():
     assert rows(5, 2, 8, 16) == 10 + 8 * 15
     assert ws(1024, 8, 128) == 0 and ws(1025, 8, 128) > 0
     assert ws(1 << 31, 1, 128) == 0 and ws(1 << 20, 8, 1025) == 0
-    assert ws(1 << 27, 8, 128) == 257 * 128 * 4                 # bounded by the workgroups
+    assert ws(1 << 27, 8, 128) == 256 * 128 * 4                 # bounded by the workgroups
 
 
 def sort(ids=at(0), tokens=2000, k=8, first=0, experts=64, pad=16, offsets=at(1), order=at(2), rows=None, pos=at(3),
