@@ -33,18 +33,107 @@ struct RouterArgs {
     int renormalize;
 };
 
-// exp(d) for d <= 0, to about two units in the last place: d * log2(e) as a
-// rounded product and its remainder, 2^x of the first by the hardware, the
-// second to first order.  Below -200 the result is 0 in binary32 all the same.
-__device__ __forceinline__ float exp_down(float d) {
-    constexpr float kLog2e = 1.44269504088896341f;              // rounded to binary32
-    constexpr float kLog2eLow = 1.92596299112661746e-8f;        // log2(e) - kLog2e
-    constexpr float kLn2 = 0.693147180559945309f;
-    d = fmaxf(d, -200.0f);
-    const float a = d * kLog2e;
-    const float r = fmaf(d, kLog2e, -a) + d * kLog2eLow;
-    const float p = __builtin_amdgcn_exp2f(a);
-    return fmaf(p, r * kLn2, p);
+// Keys.  A logit and its index in one number, so that no two are equal and
+// their order is "by logit downward, then by index upward": a 16-bit logit's
+// order in the upper half of a word and the index's complement in the lower; a
+// binary32 logit as binary64, the index in the bits that its fraction leaves
+// free.  The smallest key stands for a logit that is never picked.
+//
+// Up to 8 picks of binary32 logits come from lists: every lane sorts its keys,
+// and lists of the 8 largest are merged lane by lane.  Taking one pick after
+// the other out of 256 binary32 logits costs about 100 instructions each, the
+// lists 300 in all (32768 tokens, k=8: 15.1 against 11.4 us); out of 16-bit
+// logits it costs 40 each, and lists were no faster (9.8 us either way).
+template <int CTRL>
+__device__ __forceinline__ double dpp_wide(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp<CTRL>(static_cast<uint32_t>(b)), hi = dpp<CTRL>(static_cast<uint32_t>(b >> 32));
+    return __builtin_bit_cast(double, lo | hi << 32);
+}
+
+// The values of the lower and of the upper of two groups of D lanes (16 or
+// 32), in the lanes of both.
+template <int D>
+__device__ __forceinline__ void both(double v, double &low, double &high) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t w[2] = {static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32)};
+    uint64_t l = 0, h = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false)
+                               : __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        l |= static_cast<uint64_t>(r0) << (32 * i);
+        h |= static_cast<uint64_t>(r1) << (32 * i);
+    }
+    low = __builtin_bit_cast(double, l);
+    high = __builtin_bit_cast(double, h);
+}
+
+constexpr int kList = 8;
+
+__device__ __forceinline__ void order2(double &a, double &b) {
+    const double hi = __builtin_fmax(a, b);
+    b = __builtin_fmin(a, b);
+    a = hi;
+}
+
+// Eight keys downward: an odd-even merge network of 19 comparators.
+__device__ __forceinline__ void sort8(double *k) {
+    order2(k[0], k[1]); order2(k[2], k[3]); order2(k[4], k[5]); order2(k[6], k[7]);
+    order2(k[0], k[2]); order2(k[1], k[3]); order2(k[4], k[6]); order2(k[5], k[7]);
+    order2(k[1], k[2]); order2(k[5], k[6]);
+    order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
+    order2(k[2], k[4]); order2(k[3], k[5]);
+    order2(k[1], k[2]); order2(k[3], k[4]); order2(k[5], k[6]);
+}
+
+// Eight keys that fall and rise, downward: 12 comparators.
+__device__ __forceinline__ void sort_bitonic8(double (&k)[kList]) {
+#pragma unroll
+    for (int d = 4; d >= 1; d /= 2)
+#pragma unroll
+        for (int i = 0; i < kList; ++i)
+            if ((i & d) == 0) order2(k[i], k[i + d]);
+}
+
+// The eight largest of two lists: the larger of one's i-th from the top and the
+// other's i-th from the bottom.
+template <int CTRL>
+__device__ __forceinline__ void merge_lanes(double (&k)[kList]) {
+    double m[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) m[i] = __builtin_fmax(k[i], dpp_wide<CTRL>(k[kList - 1 - i]));
+#pragma unroll
+    for (int i = 0; i < kList; ++i) k[i] = m[i];
+    sort_bitonic8(k);
+}
+
+template <int D>
+__device__ __forceinline__ void merge_groups(double (&k)[kList]) {
+    double low[kList], high[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) both<D>(k[i], low[i], high[i]);
+#pragma unroll
+    for (int i = 0; i < kList; ++i) k[i] = __builtin_fmax(low[i], high[kList - 1 - i]);
+    sort_bitonic8(k);
+}
+
+// The eight largest keys of L lanes with R each, downward, in every lane: each
+// lane sorts its own, then lists are merged lane by lane.
+template <int L, int R>
+__device__ __forceinline__ void eight_largest(double (&key)[R], double (&list)[kList]) {
+#pragma unroll
+    for (int i = 0; i < R; i += kList) sort8(key + i);
+#pragma unroll
+    for (int i = 0; i < kList; ++i) list[i] = R == kList ? key[i] : __builtin_fmax(key[i], key[R - 1 - i]);
+    if constexpr (R > kList) sort_bitonic8(list);
+    merge_lanes<0xB1>(list);
+    merge_lanes<0x4E>(list);
+    merge_lanes<0x141>(list);
+    if constexpr (L >= 16) merge_lanes<0x140>(list);
+    if constexpr (L >= 32) merge_groups<16>(list);
+    if constexpr (L >= 64) merge_groups<32>(list);
 }
 
 // The order of a binary32 logit as an unsigned number; 0 = never picked.
@@ -58,28 +147,54 @@ __device__ __forceinline__ float key_value(uint32_t u) {
     return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
-// R consecutive logits of one lane as they lie in memory (Raw), widened, and
-// as keys.  What lies past the last logit reads as -infinity.
+// R logits of lane t of L as they lie in memory (Raw), widened, and as keys:
+// kVec consecutive ones (16 bytes) at a time, the lanes side by side, so that
+// an access of the lanes covers whole lines.  (With a lane's R logits side by
+// side the gradient of 32768 x 256 binary32 logits took 18.0 us against 11.4,
+// of bfloat16 ones renormalised 6.4 against 5.2.)  What lies past the last
+// logit reads as -infinity.
+template <class T, int L>
+__device__ __forceinline__ int logit_at(int r, int t) {
+    return (r / T::kVec * L + t) * T::kVec + r % T::kVec;
+}
+
 struct Logits32 {
     static constexpr size_t kBytes = 4;
+    static constexpr int kVec = 4;
     static constexpr bool kPacked = false;
+    static __device__ __forceinline__ double key(float x, int e) {
+        // a finite value beyond binary32 in infinity's place, which has no fraction
+        const double d = x == INFINITY ? 0x1p200 : static_cast<double>(x + 0.0f);      // -0 as +0
+        const uint64_t b = __builtin_bit_cast(uint64_t, d) | static_cast<uint32_t>(x >= 0.0f ? 0xFFFF - e : e);
+        return x > -INFINITY ? __builtin_bit_cast(double, b) : -static_cast<double>(INFINITY);
+    }
+    static __device__ __forceinline__ bool picked(double key) { return key > -static_cast<double>(INFINITY); }
+    static __device__ __forceinline__ float value(double key) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, key) & ~0xFFFFull;
+        return static_cast<float>(__builtin_bit_cast(double, b));     // 2^200 becomes infinity again
+    }
+    static __device__ __forceinline__ int index(double key) {
+        const int e = static_cast<int>(__builtin_bit_cast(uint64_t, key) & 0xFFFF);
+        return key < 0.0 ? e : 0xFFFF - e;
+    }
     template <int R>
     struct Raw {
         float x[R];
     };
-    template <int R>
-    static __device__ __forceinline__ void load(const void *row, int e0, int n, Raw<R> &raw) {
-        const float *p = static_cast<const float *>(row) + e0;
-        if (e0 + R <= n) {
+    template <int L, int R>
+    static __device__ __forceinline__ void load(const void *row, int t, int n, Raw<R> &raw) {
+        const float *p = static_cast<const float *>(row);
 #pragma unroll
-            for (int q = 0; q < R / 4; ++q) {
-                const f32x4 v = *reinterpret_cast<const f32x4_row *>(p + 4 * q);
+        for (int q = 0; q < R / 4; ++q) {
+            const int e = logit_at<Logits32, L>(4 * q, t);
+            if (e + 4 <= n) {
+                const f32x4 v = *reinterpret_cast<const f32x4_row *>(p + e);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) raw.x[4 * q + i] = v[i];
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) raw.x[r] = e0 + r < n ? p[r] : -INFINITY;
+                for (int i = 0; i < 4; ++i) raw.x[4 * q + i] = e + i < n ? p[e + i] : -INFINITY;
+            }
         }
     }
     template <int R>
@@ -87,17 +202,19 @@ struct Logits32 {
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = raw.x[r];
     }
-    template <int R>
-    static __device__ __forceinline__ void store(void *row, int e0, int n, const float (&x)[R]) {
-        float *p = static_cast<float *>(row) + e0;
-        if (e0 + R <= n) {
+    template <int L, int R>
+    static __device__ __forceinline__ void store(void *row, int t, int n, const float (&x)[R]) {
+        float *p = static_cast<float *>(row);
 #pragma unroll
-            for (int q = 0; q < R / 4; ++q)
-                *reinterpret_cast<f32x4_row *>(p + 4 * q) = f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-        } else {
+        for (int q = 0; q < R / 4; ++q) {
+            const int e = logit_at<Logits32, L>(4 * q, t);
+            if (e + 4 <= n) {
+                *reinterpret_cast<f32x4_row *>(p + e) = f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (e0 + r < n) p[r] = x[r];
+                for (int i = 0; i < 3; ++i)
+                    if (e + i < n) p[e + i] = x[4 * q + i];
+            }
         }
     }
 };
@@ -105,6 +222,7 @@ struct Logits32 {
 template <class E>
 struct Logits16 {
     static constexpr size_t kBytes = 2;
+    static constexpr int kVec = 8;
     static constexpr bool kPacked = true;
     static constexpr uint32_t kInf = std::is_same<E, F16>::value ? 0x7C00u : 0x7F80u;
     static constexpr uint32_t kNone = (0x8000u | kInf) * 0x10001u;
@@ -112,21 +230,23 @@ struct Logits16 {
     struct Raw {
         uint32_t w[R / 2];           // two logits to a word
     };
-    template <int R>
-    static __device__ __forceinline__ void load(const void *row, int e0, int n, Raw<R> &raw) {
-        const uint16_t *p = static_cast<const uint16_t *>(row) + e0;
-        if (e0 + R <= n) {
+    template <int L, int R>
+    static __device__ __forceinline__ void load(const void *row, int t, int n, Raw<R> &raw) {
+        const uint16_t *p = static_cast<const uint16_t *>(row);
 #pragma unroll
-            for (int q = 0; q < R / 8; ++q) {
-                const u32x4 v = load_vec<false>(p + 8 * q);
+        for (int q = 0; q < R / 8; ++q) {
+            const int e = logit_at<Logits16, L>(8 * q, t);
+            if (e + 8 <= n) {
+                const u32x4 v = load_vec<false>(p + e);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) raw.w[4 * q + i] = v[i];
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; r += 2) {
-                const uint32_t lo = e0 + r < n ? p[r] : kNone & 0xFFFFu, hi = e0 + r + 1 < n ? p[r + 1] : kNone >> 16;
-                raw.w[r / 2] = lo | hi << 16;
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t lo = e + i < n ? p[e + i] : kNone & 0xFFFFu;
+                    const uint32_t hi = e + i + 1 < n ? p[e + i + 1] : kNone >> 16;
+                    raw.w[4 * q + i / 2] = lo | hi << 16;
+                }
             }
         }
     }
@@ -140,11 +260,11 @@ struct Logits16 {
             for (int i = 0; i < 8; ++i) x[8 * q + i] = f[i];
         }
     }
-    template <int R>
-    static __device__ __forceinline__ void store(void *row, int e0, int n, const float (&x)[R]) {
+    template <int L, int R>
+    static __device__ __forceinline__ void store(void *row, int t, int n, const float (&x)[R]) {
 #pragma unroll
         for (int q = 0; q < R / 8; ++q) {
-            const int e = e0 + 8 * q;
+            const int e = logit_at<Logits16, L>(8 * q, t);
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = x[8 * q + i];
@@ -159,9 +279,7 @@ struct Logits16 {
             }
         }
     }
-    // A logit's order in the upper half of a word and its index's complement in
-    // the lower, so that no two are equal; 0 = never picked.  `bits` holds the
-    // logit in its upper half and zeros below.
+    // `bits` holds the logit in its upper half and zeros below.
     static __device__ __forceinline__ uint32_t key(uint32_t bits, int e) {
         bits = bits == 0x80000000u ? 0u : bits;                 // -0 as +0
         const uint32_t u = bits ^ (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 31) | 0x80000000u);
@@ -169,11 +287,13 @@ struct Logits16 {
         constexpr uint32_t kLow = (0x8000u - kInf) << 16, kHigh = (0x8000u | kInf) << 16 | 0xFFFFu;
         return u - kLow <= kHigh - kLow ? (u & 0xFFFF0000u) | (0xFFFFu - e) : 0u;
     }
-    template <int R>
-    static __device__ __forceinline__ void keys(const Raw<R> &raw, int e0, uint32_t (&k)[R]) {
+    template <int L, int R>
+    static __device__ __forceinline__ void keys(const Raw<R> &raw, int t, uint32_t (&k)[R]) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) k[r] = key(r & 1 ? raw.w[r / 2] & 0xFFFF0000u : raw.w[r / 2] << 16, e0 + r);
+        for (int r = 0; r < R; ++r)
+            k[r] = key(r & 1 ? raw.w[r / 2] & 0xFFFF0000u : raw.w[r / 2] << 16, logit_at<Logits16, L>(r, t));
     }
+    static __device__ __forceinline__ int index(uint32_t key) { return static_cast<int>(0xFFFFu - (key & 0xFFFFu)); }
     static __device__ __forceinline__ float value(uint32_t key) {
         const uint32_t u = key >> 16;
         return Wide<E>::widen1(static_cast<uint16_t>(u & 0x8000u ? u ^ 0x8000u : ~u));
@@ -182,45 +302,55 @@ struct Logits16 {
 
 // exp(x - top) of R logits and their sum: 0 for -infinity and NaN, and for
 // everything where top is -infinity (nothing to pick); where top is +infinity,
-// 1 for each +infinity.
+// 1 for each +infinity.  The exponent (x - top) log2(e) is rounded twice to 24
+// bits: at most 2^-23 of itself, so the terms that weigh, with exponents above
+// -16, are off by less than 2^-19.
 template <int R>
 __device__ __forceinline__ float exp_all(float (&x)[R], float top) {
-    if (top == INFINITY) {
-        // the largest number in infinity's place: its difference to itself is 0
-        top = FLT_MAX;
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = x[r] == INFINITY ? FLT_MAX : -INFINITY;
-    }
-    float total = 0.0f;
+    constexpr float kLog2e = 1.44269504088896341f;
+    // NaN and infinities show in the sum; a wave without them does not look
+    // at every logit for them
+    const float from = top == -INFINITY ? 0.0f : top;
+    float y[R], total = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        // (a difference that is NaN or -infinity ends as an exponent that gives 0)
-        x[r] = exp_down(x[r] - top);
-        total += x[r];
+        y[r] = __builtin_amdgcn_exp2f((x[r] - from) * kLog2e);
+        total += y[r];
     }
+    if (__ballot(!(total < INFINITY)) != 0) {
+        total = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float one = x[r] == INFINITY ? 1.0f : 0.0f;
+            const float e = x[r] > -INFINITY ? __builtin_amdgcn_exp2f((x[r] - from) * kLog2e) : 0.0f;
+            y[r] = top == INFINITY ? one : e;
+            total += y[r];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = y[r];
     return total;
 }
 
-// One token per L lanes; lane t holds the R logits t * R, t * R + 1, ..
-template <class T, int L, int R>
+// LIST: up to 8 picks of binary32 logits.
+template <class T, int L, int R, bool LIST>
 __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;
     const int t = threadIdx.x % L;
     const size_t token = static_cast<size_t>(blockIdx.x) * kTokens + threadIdx.x / L;
     const bool there = token < a.tokens;
-    const int e0 = t * R;
     typename T::template Raw<R> raw;
-    T::load(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, e0,
-            there ? a.experts : 0, raw);
+    T::template load<L>(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, t,
+                        there ? a.experts : 0, raw);
 
     // the picks, lane j keeping pick j, and the largest logit
-    float top = 0.0f, v = 0.0f;
+    float top = -INFINITY, v = 0.0f;
     int id = -1;
     if constexpr (T::kPacked) {
         // The next pick is the largest key below the last one, that is the
         // largest difference to it modulo 2^32: nothing has to be taken out.
         uint32_t key[R];
-        T::keys(raw, e0, key);
+        T::template keys<L>(raw, t, key);
         uint32_t last = 0, first = 0, mine = 0;
         for (int j = 0; j < a.k; ++j) {
             uint32_t m = key[0] - last;
@@ -234,10 +364,23 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
             first = j == 0 ? last : first;
             mine = t == j ? last : mine;
         }
-        top = first != 0 ? T::value(first) : -INFINITY;
+        if (first != 0) top = T::value(first);
         if (mine != 0) {
             v = T::value(mine);
-            id = static_cast<int>(0xFFFFu - (mine & 0xFFFFu));
+            id = T::index(mine);
+        }
+    } else if constexpr (LIST) {
+        double key[R], list[kList];
+#pragma unroll
+        for (int r = 0; r < R; ++r) key[r] = T::key(raw.x[r], logit_at<T, L>(r, t));
+        eight_largest<L>(key, list);
+        double mine = list[0];
+#pragma unroll
+        for (int i = 1; i < kList; ++i) mine = t == i ? list[i] : mine;
+        if (T::picked(list[0])) top = T::value(list[0]);
+        if (t < a.k && T::picked(mine)) {
+            v = T::value(mine);
+            id = T::index(mine);
         }
     } else {
         uint32_t key[R];
@@ -252,15 +395,15 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
             // the lowest index with that key: as the largest complement
             uint32_t at = 0;
 #pragma unroll
-            for (int r = R - 1; r >= 0; --r) at = key[r] == m ? ~static_cast<uint32_t>(e0 + r) : at;
+            for (int r = R - 1; r >= 0; --r) at = key[r] == m ? ~static_cast<uint32_t>(logit_at<T, L>(r, t)) : at;
             const int e = static_cast<int>(~max_lanes<L>(at));
 #pragma unroll
-            for (int r = 0; r < R; ++r) key[r] = e0 + r == e ? 0u : key[r];
+            for (int r = 0; r < R; ++r) key[r] = logit_at<T, L>(r, t) == e ? 0u : key[r];
             best = j == 0 ? m : best;
             mine = t == j ? m : mine;
             id = t == j && m != 0 ? e : id;
         }
-        top = best != 0 ? key_value(best) : -INFINITY;
+        if (best != 0) top = key_value(best);
         v = key_value(mine);
     }
 
@@ -281,18 +424,19 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
 template <class T, int L, int R>
 __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;
-    __shared__ float picked[kTokens][L * R];
+    // by fours of a lane's logits, the lanes side by side: no two lanes of an
+    // access share a bank (with a lane's logits side by side, four did)
+    __shared__ f32x4 picked[kTokens][R / 4][L];
     const int t = threadIdx.x % L;
     const int slot = threadIdx.x / L;
     const size_t token = static_cast<size_t>(blockIdx.x) * kTokens + slot;
     const bool there = token < a.tokens;
-    const int e0 = t * R;
     typename T::template Raw<R> raw;
     if (!a.renormalize)
-        T::load(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, e0,
-                there ? a.experts : 0, raw);
+        T::template load<L>(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, t,
+                            there ? a.experts : 0, raw);
 #pragma unroll
-    for (int r = 0; r < R; ++r) picked[slot][e0 + r] = 0.0f;
+    for (int q = 0; q < R / 4; ++q) picked[slot][q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     int id = -1;
     float g = 0.0f, w = 0.0f;
     if (there && t < a.k) {
@@ -306,13 +450,23 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
     }
     const float c = sum_lanes<L>(id >= 0 ? g * w : 0.0f);
     __syncthreads();
-    if (id >= 0) picked[slot][id] = a.renormalize ? w * (g - c) : g;
+    if (id >= 0) {
+        const int r = id / (T::kVec * L) * T::kVec + id % T::kVec, lane = id / T::kVec % L;
+        picked[slot][r / 4][lane][r % 4] = a.renormalize ? w * (g - c) : g;
+    }
     __syncthreads();
+    float at[R];
+#pragma unroll
+    for (int q = 0; q < R / 4; ++q) {
+        const f32x4 p = picked[slot][q][t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[4 * q + i] = p[i];
+    }
 
     float x[R];
     if (a.renormalize) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = picked[slot][e0 + r];
+        for (int r = 0; r < R; ++r) x[r] = at[r];
     } else {
         T::widen(raw, x);
         float top = -INFINITY;
@@ -322,10 +476,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
         const float total = sum_lanes<L>(exp_all(x, top));
         const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = x[r] * inv * (picked[slot][e0 + r] - c);
+        for (int r = 0; r < R; ++r) x[r] = x[r] * inv * (at[r] - c);
     }
-    if (there && e0 < a.experts)
-        T::store(static_cast<char *>(a.dlogits) + token * a.dstride * T::kBytes, e0, a.experts, x);
+    if (there) T::template store<L>(static_cast<char *>(a.dlogits) + token * a.dstride * T::kBytes, t, a.experts, x);
 }
 
 namespace {
@@ -336,8 +489,12 @@ hipError_t launch_router(const RouterArgs &a, bool grad, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>((a.tokens + kTokens - 1) / kTokens);
     if (grad)
         hipLaunchKernelGGL((router_topk_grad<T, L, R>), dim3(grid), dim3(kRouterThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((router_topk<T, L, R>), dim3(grid), dim3(kRouterThreads), 0, s, a);
+    else if constexpr (T::kPacked)
+        hipLaunchKernelGGL((router_topk<T, L, R, false>), dim3(grid), dim3(kRouterThreads), 0, s, a);
+    else if (L == 8 || a.k <= kList)
+        hipLaunchKernelGGL((router_topk<T, L, R, true>), dim3(grid), dim3(kRouterThreads), 0, s, a);
+    else if constexpr (L > 8)
+        hipLaunchKernelGGL((router_topk<T, L, R, false>), dim3(grid), dim3(kRouterThreads), 0, s, a);
     return hipGetLastError();
 }
 
