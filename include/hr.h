@@ -748,6 +748,7 @@ HR_API hr_status hr_router_topk_grad(const float *dweights, const float *weights
  */
 #define HR_EXPERTS_MAX 1024     /* experts of one sort */
 #define HR_EXPERTS_MAX_K 32     /* picks per token */
+#define HR_EXPERTS_SORT_FEW 8192 /* slots that a sort needs no workspace for */
 
 /* Rows that sorted tokens take at most: tokens * k, and pad - 1 more for every
  * segment that can hold a slot.  0 when an argument is out of range. */

@@ -516,8 +516,6 @@ namespace {
 constexpr size_t kMaxCount = 0x7FFFFFFF;
 // A launch has fewer than 2^32 work-items.
 constexpr size_t kMaxGroups = 0xFFFFFFFFu / kExpertThreads;
-// Up to this many slots one workgroup sorts by itself.
-constexpr size_t kSortOnce = 8192;
 constexpr size_t kSortBlocks = 256;
 constexpr size_t kSortChunk = 2048;
 
@@ -683,7 +681,7 @@ extern "C" HR_API size_t hr_experts_rows(size_t tokens, int k, int experts, int 
 extern "C" HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int experts) {
     size_t slots = 0;
     if (!picks_ok(tokens, k, &slots) || experts < 1 || experts > HR_EXPERTS_MAX || slots > kMaxCount) return 0;
-    if (slots <= kSortOnce) return 0;
+    if (slots <= static_cast<size_t>(HR_EXPERTS_SORT_FEW)) return 0;
     const size_t chunk = sort_chunk(slots);
     return (slots + chunk - 1) / chunk * static_cast<size_t>(experts) * 4;
 }
@@ -730,7 +728,7 @@ extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, i
     const auto lds_for = [&](int threads, int arrays, int more) {
         return (static_cast<size_t>(threads / kWave + arrays) * experts + 1 + more + threads / kWave) * sizeof(int);
     };
-    if (slots <= kSortOnce) {
+    if (slots <= static_cast<size_t>(HR_EXPERTS_SORT_FEW)) {
         // a wave for every 64 slots, but no fewer than 4
         int threads = 256;
         while (threads < most_threads && threads < static_cast<int>(slots)) threads *= 2;

@@ -73,6 +73,7 @@ HR_ROUTER_MAX_K = 32
 HR_ROUTER_MAX_TOKENS = (1 << 26) - 4
 HR_EXPERTS_MAX = 1024
 HR_EXPERTS_MAX_K = 32
+HR_EXPERTS_SORT_FEW = 8192
 
 
 class hr_channel_config(ctypes.Structure):
@@ -590,6 +591,18 @@ def _entry(name: str, dtype):
     return got
 
 
+_raw_stream = None
+
+
+def _stream_of(stream, tensor) -> int:
+    """_stream_handle with torch's raw query looked up once."""
+    global _raw_stream
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(tensor.get_device())
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return _stream_handle(stream, tensor)
+
+
 def _row_view(t, name: str, dtype, rows=None, width=None):
     """(address, rows, row length, row stride) of a device tensor whose last
     dimension is a row: two dimensions with any row stride, or contiguous."""
@@ -626,13 +639,13 @@ def _rows_like(t, name: str, dtype, shape, rows: int, width: int):
 
 def _flat_ptr(t, name: str, dtype, numel: int) -> int:
     """Address of a contiguous device tensor of ``numel`` values."""
+    if t.dtype is dtype and t.is_cuda and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name}: expected a device tensor")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of {numel} values")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor of {numel} values")
 
 
 def _weight_ptr(t, dtype, hidden: int):
@@ -674,9 +687,14 @@ def reduce_rmsnorm(tensors, out=None, *, residual=None, residual_out=None, weigh
     p0, rows, hidden, stride = _row_view(first, "tensors[0]", dt)
     shape = first.shape
     ptrs = [p0]
+    packed = (stride or hidden) == hidden
     for i in range(1, len(tensors)):
-        p, s = _rows_like(tensors[i], f"tensors[{i}]", dt, shape, rows, hidden)
-        if s != stride and (s or hidden) != (stride or hidden):
+        t = tensors[i]
+        if packed and t.dtype is dt and t.shape == shape and t.is_cuda and t.is_contiguous():
+            ptrs.append(t.data_ptr())
+            continue
+        p, s = _rows_like(t, f"tensors[{i}]", dt, shape, rows, hidden)
+        if (s or hidden) != (stride or hidden):
             raise ValueError(f"tensors[{i}]: row stride {s}, tensors[0] has {stride}")
         ptrs.append(p)
     ptrs += _NULLS[len(ptrs):]
@@ -700,7 +718,7 @@ def reduce_rmsnorm(tensors, out=None, *, residual=None, residual_out=None, weigh
     wp, wf = _weight_ptr(weight, dt, hidden)
     args = _NORM.pack(*ptrs, rp, wp, hp, op, cp, sp, tp, rows, hidden, stride, rs, hs, os_, cs, ss,
                       len(tensors), wf, group, eps)
-    st = fn(args, _stream_handle(stream, first))
+    st = fn(args, _stream_of(stream, first))
     if st != HR_OK:
         raise HrError(st, name)
     return out
@@ -733,7 +751,7 @@ def rmsnorm_grad(dy, h, rstd, dx, *, weight=None, dresidual=None, dweight=None, 
             kb = workspace.numel() * workspace.element_size()
             kp = _flat_ptr(workspace, "workspace", workspace.dtype, workspace.numel())
     args = _NORM_GRAD.pack(yp, hp, tp, wp, rp, xp, gp, kp, kb, rows, hidden, ys, hs, rs, xs, wf)
-    st = fn(args, _stream_handle(stream, h))
+    st = fn(args, _stream_of(stream, h))
     if st != HR_OK:
         raise HrError(st, name)
     return dx
@@ -768,7 +786,7 @@ def router_topk(logits, weights, ids, *, renormalize: bool = False, stream=None)
     lp, tokens, experts, ls = _row_view(logits, "logits", logits.dtype)
     wp, ip, k = _picks(weights, ids, tokens)
     st = load().hr_router_topk(lp, code, tokens, experts, ls, k, 1 if renormalize else 0, wp, ip,
-                               _stream_handle(stream, logits))
+                               _stream_of(stream, logits))
     if st != HR_OK:
         raise HrError(st, "hr_router_topk")
     return weights, ids
@@ -787,7 +805,7 @@ def router_topk_grad(dweights, weights, ids, dlogits, *, logits=None, renormaliz
     if logits is not None and not renormalize:
         lp, _, _, ls = _row_view(logits, "logits", dt, tokens, experts)
     st = load().hr_router_topk_grad(gp, wp, ip, lp, code, tokens, experts, ls, k, 1 if renormalize else 0, dp, ds,
-                                    _stream_handle(stream, dlogits))
+                                    _stream_of(stream, dlogits))
     if st != HR_OK:
         raise HrError(st, "hr_router_topk_grad")
     return dlogits
@@ -810,9 +828,10 @@ def experts_sort(ids, offsets, order, pos, *, first: int = 0, pad: int = 1, work
     takes one from torch's allocator when the call needs one."""
     if _torch is None:
         _tm()
-    if ids.dim() != 2:
+    shape = ids.shape
+    if len(shape) != 2:
         raise ValueError("ids: expected tokens x k")
-    tokens, k = ids.shape
+    tokens, k = shape
     i32 = _torch.int32
     ip = _flat_ptr(ids, "ids", i32, tokens * k)
     experts = offsets.numel() - 1
@@ -822,7 +841,7 @@ def experts_sort(ids, offsets, order, pos, *, first: int = 0, pad: int = 1, work
     pp = _flat_ptr(pos, "pos", i32, tokens * k)
     lib = load()
     kp = kb = 0
-    if workspace is None:
+    if workspace is None and tokens * k > HR_EXPERTS_SORT_FEW:
         need = lib.hr_experts_sort_workspace(tokens, k, experts)
         if need:
             workspace = _scratch(need, ids, stream)
@@ -830,7 +849,7 @@ def experts_sort(ids, offsets, order, pos, *, first: int = 0, pad: int = 1, work
         kb = workspace.numel() * workspace.element_size()
         kp = _flat_ptr(workspace, "workspace", workspace.dtype, workspace.numel())
     st = lib.hr_experts_sort(ip, tokens, k, first, experts, pad, op, rp, rows, pp, kp, kb,
-                             _stream_handle(stream, ids))
+                             _stream_of(stream, ids))
     if st != HR_OK:
         raise HrError(st, "hr_experts_sort")
     return offsets, order, pos
@@ -838,9 +857,10 @@ def experts_sort(ids, offsets, order, pos, *, first: int = 0, pad: int = 1, work
 
 def _pos_ptr(pos, tokens: int):
     """(address, k) of a sort's pos."""
-    if pos.dim() != 2 or pos.shape[0] != tokens:
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != tokens:
         raise ValueError(f"pos: expected {tokens} x k")
-    k = pos.shape[1]
+    k = shape[1]
     return _flat_ptr(pos, "pos", _torch.int32, tokens * k), k
 
 
@@ -864,7 +884,9 @@ def experts_gather(x, pos, out, *, offsets=None, order=None, scales=None, scales
         _tm()
     dt = x.dtype
     xp, tokens, width, xs = _row_view(x, "x", dt)
-    op, rows, _, os_ = _row_view(out, "out", dt, out.shape[0], width)
+    op, rows, w, os_ = _row_view(out, "out", dt)
+    if w != width:
+        raise ValueError(f"out: rows of {w} values, x has {width}")
     pp, k = _pos_ptr(pos, tokens)
     rp, fp, experts = _padding_ptrs(order, offsets, rows)
     sp = tp = sw = ss = ts = 0
@@ -878,7 +900,7 @@ def experts_gather(x, pos, out, *, offsets=None, order=None, scales=None, scales
     size = x.element_size()
     args = _GATHER.pack(xp, sp, op, tp, pp, rp, fp, tokens, rows, width * size, xs * size, os_ * size, sw, ss, ts, k,
                         experts)
-    st = load().hr_experts_gather(args, _stream_handle(stream, x))
+    st = load().hr_experts_gather(args, _stream_of(stream, x))
     if st != HR_OK:
         raise HrError(st, "hr_experts_gather")
     return out
@@ -891,7 +913,9 @@ def experts_combine(z, pos, out, *, weights=None, addend=None, stream=None):
     dt = out.dtype
     fn, name = _entry("hr_experts_combine", dt)
     op, tokens, hidden, os_ = _row_view(out, "out", dt)
-    zp, rows, _, zs = _row_view(z, "z", dt, z.shape[0], hidden)
+    zp, rows, w, zs = _row_view(z, "z", dt)
+    if w != hidden:
+        raise ValueError(f"z: rows of {w} values, out has {hidden}")
     pp, k = _pos_ptr(pos, tokens)
     wp = ap = as_ = 0
     if weights is not None:
@@ -899,7 +923,7 @@ def experts_combine(z, pos, out, *, weights=None, addend=None, stream=None):
     if addend is not None:
         ap, _, _, as_ = _row_view(addend, "addend", dt, tokens, hidden)
     args = _COMBINE.pack(zp, ap, op, pp, wp, tokens, rows, hidden, zs, as_, os_, k)
-    st = fn(args, _stream_handle(stream, out))
+    st = fn(args, _stream_of(stream, out))
     if st != HR_OK:
         raise HrError(st, name)
     return out
@@ -913,7 +937,9 @@ def experts_combine_grad(dy, z, pos, weights=None, dz=None, dweights=None, *, of
     dt = dy.dtype
     fn, name = _entry("hr_experts_combine_grad", dt)
     yp, tokens, hidden, ys = _row_view(dy, "dy", dt)
-    zp, rows, _, zs = _row_view(z, "z", dt, z.shape[0], hidden)
+    zp, rows, w, zs = _row_view(z, "z", dt)
+    if w != hidden:
+        raise ValueError(f"z: rows of {w} values, dy has {hidden}")
     pp, k = _pos_ptr(pos, tokens)
     dp = ds = wp = gp = 0
     if dz is not None:
@@ -924,7 +950,7 @@ def experts_combine_grad(dy, z, pos, weights=None, dz=None, dweights=None, *, of
         gp = _flat_ptr(dweights, "dweights", _torch.float32, tokens * k)
     rp, fp, experts = _padding_ptrs(order, offsets, rows)
     args = _COMBINE_GRAD.pack(yp, zp, dp, pp, wp, gp, rp, fp, tokens, rows, hidden, ys, zs, ds, k, experts)
-    st = fn(args, _stream_handle(stream, dy))
+    st = fn(args, _stream_of(stream, dy))
     if st != HR_OK:
         raise HrError(st, name)
     return dz, dweights
