@@ -104,8 +104,12 @@ __device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
 
 // One row per workgroup (L = 0), or one row per L lanes of a workgroup.
 // Thread t of a row holds units t, t + threads, .. (U of them) from the fold's
-// loads to the stores, so every input byte is read once.
-template <class E, int U, int L, bool TAIL, bool NT>
+// loads to the stores, so every input byte is read once.  B operands are loaded
+// at once: few, because registers held for loads keep waves off the compute
+// unit (2048 x 8192 of one contribution with B = 9, 4 and 3: 26.7, 24.1 and
+// 23.6 us; of eight 61.6, 60.6 and 60.7), unless there are too few rows for
+// many waves anyway (kSpreadRows).
+template <class E, int U, int L, bool TAIL, bool NT, int B>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
     __shared__ float sums[kNormMaxWaves];
     __shared__ uint32_t maxs[kNormMaxWaves];
@@ -116,9 +120,6 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
     const int hidden = a.hidden;
     const int units = (hidden + 7) / 8;
     const bool there = L == 0 || row < a.rows;
-    // operands in flight at once: all of them for one unit per lane, and the
-    // eight contributions and residual of a full group for two
-    constexpr int B = U == 1 ? kOperands : U == 2 ? 9 : 4;
 
     u32x4 h[U];
 #pragma unroll
@@ -489,9 +490,10 @@ RowShape row_shape(int hidden, bool spread = false) {
 }
 
 // Few rows of many operands wait for their loads: one unit per thread, twice
-// the threads.  (In a graph, 64 x 6144 of eight contributions into e4m3 7.3
-// against 5.3 us, 512 x 6144 of eight 13.3 against 12.4; 1 x 8192 of two 3.4
-// against 3.8, 2048 x 8192 of eight 61.6 against 67.8.)
+// the threads, nine operands at once.  (In a graph, 64 x 6144 of eight
+// contributions 5.5 us with two units per thread, 4.8 with one and four
+// operands at once, 4.4 with nine; 2048 x 8192 of eight 61.6 with two units
+// and 67.8 with one.)
 constexpr size_t kSpreadRows = 512;
 constexpr int kSpreadOperands = 5;
 
@@ -526,7 +528,7 @@ hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, size_
 
 template <class E, int U, int L, bool TAIL, bool NT>
 struct NormKernel {
-    static constexpr auto kernel = norm_rows<E, U, L, TAIL, NT>;
+    static constexpr auto kernel = norm_rows<E, U, L, TAIL, NT, U == 4 ? 2 : 4>;
 };
 
 template <class E, int U, int L, bool TAIL, bool NT>
@@ -642,8 +644,16 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     a.eps = q->eps;
 
     const size_t arrays = a.n + (a.h != nullptr) + (a.out != nullptr) + (a.codes != nullptr);
-    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, rows * hidden * 2 * arrays >= kStreamBytes,
-                                                    groups_of(rows, s), 0, reinterpret_cast<hipStream_t>(stream), a);
+    const bool tail = hidden % 8 != 0, nt = rows * hidden * 2 * arrays >= kStreamBytes;
+    const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (spread && s.lanes == 0 && s.units == 1) {
+        hipLaunchKernelGGL((tail ? norm_rows<E, 1, 0, true, false, 9> : norm_rows<E, 1, 0, false, false, 9>),
+                           dim3(static_cast<unsigned>(rows)), dim3(s.threads), 0, st, a);
+        e = hipGetLastError();
+    } else {
+        e = launch_rows<NormKernel, E>(s, tail, nt, groups_of(rows, s), 0, st, a);
+    }
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
