@@ -254,21 +254,24 @@ struct NormGradArgs {
 };
 
 // Few rows: dweight = sum over the rows of dy * h * rstd without partial sums
-// in memory.  A workgroup takes 128 columns (16 lanes of one unit), its groups
-// of 16 lanes every so many rows, and the groups' sums are added in order.
-// It reads dy and h once more, from the caches.
-constexpr int kColumns = 128;
+// in memory.  A workgroup takes the columns of kColumnLanes units, its groups
+// of so many lanes every so many rows, and the groups' sums are added in order.
+// It reads dy and h once more, from the caches.  (In a graph, 4, 8 and 16
+// lanes: 256 x 1024 4.2, 5.6 and 8.5 us, 256 x 8192 8.4, 7.4 and 8.5, 1 x 4096
+// 3.8, 3.0 and 2.7.)
+constexpr int kColumnLanes = 8;
+constexpr int kColumns = 8 * kColumnLanes;
 
 template <class E, bool TAIL>
 __device__ __forceinline__ void sum_few_rows(const NormGradArgs &a) {
     extern __shared__ float cols[];                 // [groups][kColumns]
-    const int groups = blockDim.x / 16, group = threadIdx.x / 16;
-    const int i = static_cast<int>(blockIdx.x - a.row_groups) * 16 + threadIdx.x % 16;
-    const Unit<TAIL> at(i, a.hidden);
+    const int groups = blockDim.x / kColumnLanes, group = threadIdx.x / kColumnLanes;
+    const int lane = threadIdx.x % kColumnLanes, first = static_cast<int>(blockIdx.x - a.row_groups) * kColumnLanes;
+    const Unit<TAIL> at(first + lane, a.hidden);
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    if (8 * i < a.hidden) {
+    if (8 * (first + lane) < a.hidden) {
 #pragma unroll 4
         for (size_t row = group; row < a.rows; row += groups) {
             float dy[8], h[8];
@@ -280,15 +283,14 @@ __device__ __forceinline__ void sum_few_rows(const NormGradArgs &a) {
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cols[group * kColumns + (threadIdx.x % 16) * 8 + e] = acc[e];
+    for (int e = 0; e < 8; ++e) cols[group * kColumns + lane * 8 + e] = acc[e];
     __syncthreads();
     for (int c = threadIdx.x; c < kColumns; c += blockDim.x) {
         float s = cols[c];
         for (int g = 1; g < groups; ++g) s += cols[g * kColumns + c];
-        const int first = static_cast<int>(blockIdx.x - a.row_groups) * kColumns;
-        // a last unit lies before its place in the workgroup's columns
-        const Unit<TAIL> u(first / 8 + c / 8, a.hidden);
-        if (first / 8 * 8 + c / 8 * 8 < a.hidden && u.own(c % 8)) a.dweight[u.start + c % 8] = s;
+        // (a last unit lies before its place in the workgroup's columns)
+        const Unit<TAIL> u(first + c / 8, a.hidden);
+        if (8 * (first + c / 8) < a.hidden && u.own(c % 8)) a.dweight[u.start + c % 8] = s;
     }
 }
 
@@ -296,11 +298,15 @@ __device__ __forceinline__ void sum_few_rows(const NormGradArgs &a) {
 // and this workgroup's sum over its rows of dy * u.  Rows are dealt out to the
 // workgroups (L = 0) or to groups of L lanes in turn; a thread keeps its
 // columns' sums in registers from its first row to its last.
-template <class E, int U, int L, bool TAIL, bool NT>
+// FEW: further workgroups sum the columns (in kernels of their own, since that
+// takes registers).
+template <class E, int U, int L, bool TAIL, bool NT, bool FEW>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a) {
-    if (blockIdx.x >= a.row_groups) {
-        sum_few_rows<E, TAIL>(a);
-        return;
+    if constexpr (FEW) {
+        if (blockIdx.x >= a.row_groups) {
+            sum_few_rows<E, TAIL>(a);
+            return;
+        }
     }
     __shared__ float sums[2][kNormMaxWaves];
     const int threads = L > 0 ? L : static_cast<int>(blockDim.x);
@@ -505,16 +511,25 @@ constexpr int kSpreadOperands = 5;
 // of 65537 x 128 (50 MB) 13.3 and 14.4.
 constexpr size_t kStreamBytes = size_t(1) << 27;
 
-template <template <class, int, int, bool, bool> class K, class E, class A>
-hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, size_t lds, hipStream_t stream,
+// How a call's kernel differs beside its row's layout.
+enum Mode {
+    kCached,
+    kStreamed,
+    kSmall        // norm: spread (kSpreadRows); gradient: few rows
+};
+
+template <template <class, int, int, bool, Mode> class K, class E, class A>
+hipError_t launch_rows(const RowShape &s, bool tail, Mode mode, size_t grid, size_t lds, hipStream_t stream,
                        const A &args) {
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(s.threads), lds, stream, args);
         return hipGetLastError();
     };
-#define HR_VARIANT(U, L)                                                                        \
-    (tail ? (nt ? K<E, U, L, true, true>::kernel : K<E, U, L, true, false>::kernel)             \
-          : (nt ? K<E, U, L, false, true>::kernel : K<E, U, L, false, false>::kernel))
+#define HR_MODE(U, L, TAIL)                                        \
+    (mode == kCached     ? K<E, U, L, TAIL, kCached>::kernel       \
+     : mode == kStreamed ? K<E, U, L, TAIL, kStreamed>::kernel     \
+                         : K<E, U, L, TAIL, kSmall>::kernel)
+#define HR_VARIANT(U, L) (tail ? HR_MODE(U, L, true) : HR_MODE(U, L, false))
     switch (s.lanes) {
         case 16: return go(HR_VARIANT(1, 16));
         case 32: return go(HR_VARIANT(1, 32));
@@ -524,16 +539,18 @@ hipError_t launch_rows(const RowShape &s, bool tail, bool nt, size_t grid, size_
     if (s.units == 2) return go(HR_VARIANT(2, 0));
     return go(HR_VARIANT(4, 0));
 #undef HR_VARIANT
+#undef HR_MODE
 }
 
-template <class E, int U, int L, bool TAIL, bool NT>
+template <class E, int U, int L, bool TAIL, Mode M>
 struct NormKernel {
-    static constexpr auto kernel = norm_rows<E, U, L, TAIL, NT, U == 4 ? 2 : 4>;
+    static constexpr int kOperandsAtOnce = U == 4 ? 2 : U == 1 && L == 0 && M == kSmall ? 9 : 4;
+    static constexpr auto kernel = norm_rows<E, U, L, TAIL, M == kStreamed, kOperandsAtOnce>;
 };
 
-template <class E, int U, int L, bool TAIL, bool NT>
+template <class E, int U, int L, bool TAIL, Mode M>
 struct NormGradKernel {
-    static constexpr auto kernel = norm_grad_rows<E, U, L, TAIL, NT>;
+    static constexpr auto kernel = norm_grad_rows<E, U, L, TAIL, M == kStreamed, M == kSmall>;
 };
 
 constexpr size_t kMaxRows = 0x7FFFFFFF;
@@ -644,16 +661,9 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     a.eps = q->eps;
 
     const size_t arrays = a.n + (a.h != nullptr) + (a.out != nullptr) + (a.codes != nullptr);
-    const bool tail = hidden % 8 != 0, nt = rows * hidden * 2 * arrays >= kStreamBytes;
-    const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    hipError_t e;
-    if (spread && s.lanes == 0 && s.units == 1) {
-        hipLaunchKernelGGL((tail ? norm_rows<E, 1, 0, true, false, 9> : norm_rows<E, 1, 0, false, false, 9>),
-                           dim3(static_cast<unsigned>(rows)), dim3(s.threads), 0, st, a);
-        e = hipGetLastError();
-    } else {
-        e = launch_rows<NormKernel, E>(s, tail, nt, groups_of(rows, s), 0, st, a);
-    }
+    const Mode mode = rows * hidden * 2 * arrays >= kStreamBytes ? kStreamed : spread ? kSmall : kCached;
+    const hipError_t e = launch_rows<NormKernel, E>(s, hidden % 8 != 0, mode, groups_of(rows, s), 0,
+                                                    reinterpret_cast<hipStream_t>(stream), a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
@@ -716,8 +726,8 @@ hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
         const size_t groups = groups_of(rows, s), columns = (hidden + kColumns - 1) / kColumns;
         a.row_groups = static_cast<uint32_t>(groups);
         a.dweight = q->dweight;
-        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, false, groups + columns,
-                                                            s.threads / 16 * kColumns * sizeof(float), st, a);
+        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, kSmall, groups + columns,
+                                                            s.threads / kColumnLanes * kColumns * sizeof(float), st, a);
         return e == hipSuccess ? HR_OK : HR_ERR_HIP;
     }
     const size_t parts = grad_groups(rows, a.hidden, cus);
@@ -727,8 +737,8 @@ hr_status norm_grad_impl(const hr_rmsnorm_grad_args *q, hr_stream_t stream) {
     a.row_groups = static_cast<uint32_t>(parts);
     if (rows > 0) {
         const size_t arrays = 3 + (a.dres != nullptr);
-        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, rows * hidden * 2 * arrays >= kStreamBytes, parts,
-                                                            0, st, a);
+        const Mode mode = rows * hidden * 2 * arrays >= kStreamBytes ? kStreamed : kCached;
+        const hipError_t e = launch_rows<NormGradKernel, E>(s, tail, mode, parts, 0, st, a);
         if (e != hipSuccess) return HR_ERR_HIP;
     }
     if (q->dweight != nullptr && parts != 1) {
