@@ -34,6 +34,12 @@
  *    groups (same section).  All ranks of a channel may live in one process
  *    on one GPU ("loopback": concurrently running launches on W streams).
  *
+ * Further down, under "Around the combine", is what a layer does on either
+ * side of that sum on one GPU: the norm and quantisation that follow it
+ * (hr_reduce_rmsnorm), and the choice, sorting and weighted combination of
+ * experts whose result is a rank's contribution (hr_router_topk,
+ * hr_experts_*), with their gradients.
+ *
  * Conventions for every function:
  *  - Every function returns an hr_status; nothing throws across the ABI.
  *  - Device pointers are plain HIP device addresses (hipMalloc memory or any
@@ -71,8 +77,10 @@ typedef struct hr_channel_s *hr_channel;
 typedef enum {
     HR_OK = 0,
     HR_ERR_INVALID_ARG = 1,  /* null pointer, bad rank/G, partial overlap  */
-    HR_ERR_ALIGNMENT = 2,    /* a binary16 pointer that is not 2-byte aligned */
-    HR_ERR_TOO_LARGE = 3,    /* numel above the channel's max_numel          */
+    HR_ERR_ALIGNMENT = 2,    /* a pointer not aligned to its values' size: 2
+                                bytes for 16-bit values, 4 for 32-bit ones */
+    HR_ERR_TOO_LARGE = 3,    /* numel above the channel's max_numel, or a size
+                                above a function's documented largest      */
     HR_ERR_UNSUPPORTED = 4,  /* world_size outside 2..HR_MAX_WORLD, device unusable */
     HR_ERR_HIP = 5,          /* a HIP runtime call failed                    */
     HR_ERR_TIMEOUT = 6,      /* a wait for the peer exceeded timeout_us      */

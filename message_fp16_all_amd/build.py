@@ -2,8 +2,7 @@
 
 Run ``python -m message_fp16_all_amd.build`` or call ``build()``.  The
 library is compiled by hipcc for gfx950 only, without fast-math, and with
-packed FP32 instruction selection switched off (the kernels do binary16
-arithmetic; nothing in them wants packed FP32).
+packed FP32 instruction selection switched off.
 """
 from __future__ import annotations
 
@@ -32,7 +31,7 @@ FLAGS = [
     # kernels receive their first five arguments in SGPRs (the per-rank
     # exchange kernels put what their first loads need there)
     "-mllvm", "-amdgpu-kernarg-preload-count=5",
-    "-parallel-jobs=8",
+    "-parallel-jobs=8",   # the sources side by side
     "-I", INCLUDE,
     "-Wl,-rpath,/opt/rocm/lib",
 ]

@@ -565,9 +565,11 @@ def allreduce_group_noalloc(ins, outs, status=None, stream=None):
 
 # ------------------------------------------------------- around the combine
 #
-# The argument structs go over as packed bytes: one struct.pack costs a tenth
-# of a ctypes.Structure with as many fields (0.6 against 6 us), which is as
-# long as a small call's kernel runs.
+# The argument structs go over as packed bytes: a struct.pack of the norm's 35
+# fields takes 0.4 us, where filling a ctypes.Structure goes field by field.  A
+# small call is as long as its host time (MI355X host: the norm 7.2 us, of
+# which HIP's launch is 2.9), so the checks below keep to attribute reads and
+# take a short way for contiguous tensors.
 
 _NORM = struct.Struct("@23P8N3if")
 _NORM_GRAD = struct.Struct("@8P7Ni4x")
