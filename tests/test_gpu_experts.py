@@ -317,6 +317,22 @@ def test_grad_against_differences():
     within(dw, wref, torch.full_like(wref, hidden * 9 * 32 * F32), "dweights")
 
 
+@pytest.mark.parametrize("hidden", [9, 513, 1001, 2049])
+def test_grad_in_place_with_overflow(hidden):
+    """dz over z, dz beyond binary16's range: dweights are of z as it was."""
+    tokens, k = 40, 3
+    _, _, pos, o, ph, _ = buffers(hidden, tokens, k, 6, 1, drop=0.0)
+    m = Maker(hidden)
+    z, dy = m.normal(len(o), hidden, dtype=torch.float16), m.normal(tokens, hidden, sigma=2000.0, dtype=torch.float16)
+    w = torch.full((tokens, k), 1000.0)
+    dz, dw = z.to(DEV), torch.empty(tokens, k, device=DEV)
+    hr.experts_combine_grad(dy.to(DEV), dz, pos, w.to(DEV), dz, dw)
+    torch.cuda.synchronize()
+    assert torch.isinf(dz).any()
+    prod = dy.double()[:, None] * z.double()[torch.from_numpy(ph).long()]
+    within(dw, prod.sum(2), prod.abs().sum(2) * (hidden / 16 + 32) * F32, "dweights")
+
+
 def test_foreign_rows_are_left_out():
     """A pos outside the buffer is no row: nothing is read or written there."""
     pos = torch.tensor([[0, 5], [-1, 2], [-(1 << 31), (1 << 31) - 1]], dtype=torch.int32)

@@ -68,6 +68,8 @@ def test_structs_match_their_packed_form():
     (dict(out=at(3)), hr.HR_ERR_INVALID_ARG), (dict(rstd=at(7)), hr.HR_ERR_INVALID_ARG),
     # the same address with another stride is not in place
     (dict(out=at(0), out_stride=256), hr.HR_ERR_INVALID_ARG),
+    # one row: the weight is no input to take the place of
+    (dict(rows=1, out=at(3)), hr.HR_ERR_INVALID_ARG), (dict(rows=1, residual_out=at(3)), hr.HR_ERR_INVALID_ARG),
     # interleaved columns that meet
     (dict(input_stride=256, out=at(0) + 254, out_stride=256), hr.HR_ERR_INVALID_ARG),
 ])
@@ -105,6 +107,8 @@ def grad_args(**over):
     (dict(dx=at(0) + 2), hr.HR_ERR_INVALID_ARG), (dict(dx=at(6)), hr.HR_ERR_INVALID_ARG),
     (dict(dweight=at(3)), hr.HR_ERR_INVALID_ARG), (dict(workspace=at(5)), hr.HR_ERR_INVALID_ARG),
     (dict(workspace=at(1) + 8), hr.HR_ERR_INVALID_ARG),
+    # one row: neither the weight nor rstd is an input to take the place of
+    (dict(rows=1, dx=at(3)), hr.HR_ERR_INVALID_ARG), (dict(rows=1, hidden=2, dx=at(2)), hr.HR_ERR_INVALID_ARG),
 ])
 def test_grad_refusals(over, status):
     assert both(grad_args(**over), hr.hr_rmsnorm_grad_f16, hr.hr_rmsnorm_grad_bf16) == status
