@@ -734,8 +734,9 @@ HR_API hr_status hr_router_topk(const void *logits, hr_dtype dtype, size_t token
  *     dlogits_e = p_e * (dweights of e's pick, or 0, - c)
  *     with renormalize: weights * (dweights - c) at the picks, 0 elsewhere
  *
- * weights, ids: the forward call's.  An id outside 0..experts-1 is no pick,
- * and its dweights are not used.
+ * weights, ids: the forward call's; a pick's p is its weight where they are not
+ * renormalised.  An id outside 0..experts-1 is no pick, and its dweights are
+ * not used.
  * logits:  the forward call's; with renormalize not read, and may be NULL.
  * dlogits: tokens rows of dtype, dlogits_stride apart (0 = experts); it may be
  *          exactly logits.

@@ -542,11 +542,12 @@ bool picks_ok(size_t tokens, int k, size_t *slots) {
 int lanes_for(size_t units) { return units <= 16 ? 16 : units <= 64 ? 64 : kExpertThreads; }
 
 // Sorted rows of this many bytes or more pass the caches by (non-temporal
-// loads and stores).  Measured as a sort, a gather and a combine of 8 picks of
-// 4096 values in turn, on three sets of buffers: 33 MB of rows 24.8 us cached
-// and 25.1 us streamed, 67 MB 52.0 and 42.5 us, 134 MB 80.6 and 65.8 us, 537
-// MB 281 and 213 us.  (A combine alone over rows that the last-level cache
-// still holds is slower streamed, 13.0 against 14.0 us at 67 MB.)
+// loads and stores).  Measured cached and streamed, as a sort, a gather and a
+// combine of 8 picks of 4096 values on three sets of buffers in turn: 33 MB of
+// rows 23.7 and 24.2 us, 67 MB 51.3 and 41.7, 134 MB 77.2 and 62.9, 537 MB 277
+// and 209.  On one set, a copy in the place of the experts' products between
+// gather and combine: 33 MB 37 and 42 in all, 67 MB 58 and 64, 134 MB 135 and
+// 121, 537 MB 527 and 473.
 constexpr size_t kStreamBytes = size_t(1) << 26;
 
 template <class K, class A>

@@ -497,18 +497,23 @@ RowShape row_shape(int hidden, bool spread = false) {
 
 // Few rows of many operands wait for their loads: one unit per thread, twice
 // the threads, nine operands at once.  (In a graph, 64 x 6144 of eight
-// contributions 5.5 us with two units per thread, 4.8 with one and four
-// operands at once, 4.4 with nine; 2048 x 8192 of eight 61.6 with two units
+// contributions 5.6 us with two units per thread, 5.0 with one and four
+// operands at once, 4.2 with nine; 2048 x 8192 of eight 61.6 with two units
 // and 67.8 with one.)
 constexpr size_t kSpreadRows = 512;
 constexpr int kSpreadOperands = 5;
 
 // A call that moves this many bytes or more passes the caches by
-// (non-temporal loads and stores).  Measured cached and streamed: the fold of
-// 8 contributions of 2048 x 8192 (369 MB) 71.0 and 61.6 us, one of 4999 x 5120
-// with both outputs (230 MB) 49.2 and 44.1, the gradient of 8192 x 4096 (268
-// MB) 53.3 and 49.4; the norm of 65536 x 128 (34 MB) 9.6 and 9.7, its gradient
-// of 65537 x 128 (50 MB) 13.3 and 14.4.
+// (non-temporal loads and stores).  Measured cached and streamed over buffers
+// that the caches no longer hold (three sets in turn): the fold of 8
+// contributions of 2048 x 8192 (369 MB) 71.3 and 59.8 us, one of 4999 x 5120
+// with both outputs (230 MB) 46.2 and 40.8, the gradient of 8192 x 4096 (268
+// MB) 54.8 and 50.1, of 1024 x 8192 (67 MB) 16.8 and 20.4.  Between copies that
+// write its contributions and read its output, on one set: 2048 x 8192 of one
+// (134 MB) 42.3 and 47.0 in all, 32768 x 1024 of one (268 MB) 89.7 and 88.0,
+// 2048 x 8192 of eight 191 and 179; smaller ones keep what the caches hold
+// (1000 x 5121 of eight 60.9 and 72.1), though alone they would be faster
+// streamed (33.8 and 28.8).
 constexpr size_t kStreamBytes = size_t(1) << 27;
 
 // How a call's kernel differs beside its row's layout.

@@ -19,6 +19,9 @@ namespace hr {
 
 constexpr int kRouterThreads = 256;
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
 struct RouterArgs {
     const void *logits;
     size_t stride;
@@ -159,6 +162,7 @@ __device__ __forceinline__ int logit_at(int r, int t) {
 }
 
 struct Logits32 {
+    using Value = float;
     static constexpr size_t kBytes = 4;
     static constexpr int kVec = 4;
     static constexpr bool kPacked = false;
@@ -202,25 +206,22 @@ struct Logits32 {
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = raw.x[r];
     }
-    template <int L, int R>
-    static __device__ __forceinline__ void store(void *row, int t, int n, const float (&x)[R]) {
-        float *p = static_cast<float *>(row);
+    static __device__ __forceinline__ float narrow1(float v) { return v; }
+    static __device__ __forceinline__ u32x4 narrow(const float *x) {
+        return __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]});
+    }
+    // The last unit of a row of n, whose value e is the unit's first.
+    static __device__ __forceinline__ void store_part(void *row, int e, int n, u32x4 v) {
+        uint32_t *p = static_cast<uint32_t *>(row) + e;
 #pragma unroll
-        for (int q = 0; q < R / 4; ++q) {
-            const int e = logit_at<Logits32, L>(4 * q, t);
-            if (e + 4 <= n) {
-                *reinterpret_cast<f32x4_row *>(p + e) = f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-            } else {
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (e + i < n) p[e + i] = x[4 * q + i];
-            }
-        }
+        for (int i = 0; i < 3; ++i)
+            if (e + i < n) p[i] = v[i];
     }
 };
 
 template <class E>
 struct Logits16 {
+    using Value = uint16_t;
     static constexpr size_t kBytes = 2;
     static constexpr int kVec = 8;
     static constexpr bool kPacked = true;
@@ -260,43 +261,45 @@ struct Logits16 {
             for (int i = 0; i < 8; ++i) x[8 * q + i] = f[i];
         }
     }
+    static __device__ __forceinline__ uint16_t narrow1(float v) { return Wide<E>::narrow1(v); }
+    static __device__ __forceinline__ u32x4 narrow(const float *x) {
+        const float f[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+        return Wide<E>::narrow(f);
+    }
+    static __device__ __forceinline__ void store_part(void *row, int e, int n, u32x4 v) {
+        uint16_t *p = static_cast<uint16_t *>(row) + e;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (e + i < n) p[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+    }
+    // Two logits to their orders, 1 and up; 0 = never picked.  A negative w is
+    // at 2^16 - w, others at 2^15 + w, so that both zeros meet in 2^15, with
+    // kNaN NaNs above +infinity and kNaN + 1 numbers up to -infinity.  Adding
+    // kNaN takes the upper NaNs round past zero, and a subtraction that stops
+    // at zero takes all of these away.
+    static constexpr uint16_t kNaN = 0x7FFF - kInf;
+    static __device__ __forceinline__ uint32_t orders(uint32_t w) {
+        const i16x2 v = __builtin_bit_cast(i16x2, w), sign = v >> 15;
+        const u16x2 flip = __builtin_bit_cast(u16x2, w ^ (__builtin_bit_cast(uint32_t, sign) | 0x80008000u));
+        const u16x2 u = flip - __builtin_bit_cast(u16x2, sign) + u16x2{kNaN, kNaN};
+        constexpr uint16_t kDrop = 2 * kNaN + 1;
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(u, u16x2{kDrop, kDrop}));
+    }
+    // Keys without the lane's part of the index: key(r, t) = k[r] - lane_key(t).
     template <int L, int R>
-    static __device__ __forceinline__ void store(void *row, int t, int n, const float (&x)[R]) {
+    static __device__ __forceinline__ void keys(const Raw<R> &raw, uint32_t (&k)[R]) {
 #pragma unroll
-        for (int q = 0; q < R / 8; ++q) {
-            const int e = logit_at<Logits16, L>(8 * q, t);
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = x[8 * q + i];
-            const u32x4 v = Wide<E>::narrow(f);
-            uint16_t *p = static_cast<uint16_t *>(row) + e;
-            if (e + 8 <= n) {
-                store_vec<false>(v, p);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 7; ++i)
-                    if (e + i < n) p[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
-            }
+        for (int r = 0; r < R; ++r) {
+            const uint32_t o = orders(raw.w[r / 2]);
+            k[r] = (r & 1 ? o & 0xFFFF0000u : o << 16) + (0xFFFFu - logit_at<Logits16, L>(r, 0));
         }
     }
-    // `bits` holds the logit in its upper half and zeros below.
-    static __device__ __forceinline__ uint32_t key(uint32_t bits, int e) {
-        bits = bits == 0x80000000u ? 0u : bits;                 // -0 as +0
-        const uint32_t u = bits ^ (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 31) | 0x80000000u);
-        // above -infinity (whose order is 0x7FFF - kInf) and up to +infinity
-        constexpr uint32_t kLow = (0x8000u - kInf) << 16, kHigh = (0x8000u | kInf) << 16 | 0xFFFFu;
-        return u - kLow <= kHigh - kLow ? (u & 0xFFFF0000u) | (0xFFFFu - e) : 0u;
-    }
-    template <int L, int R>
-    static __device__ __forceinline__ void keys(const Raw<R> &raw, int t, uint32_t (&k)[R]) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            k[r] = key(r & 1 ? raw.w[r / 2] & 0xFFFF0000u : raw.w[r / 2] << 16, logit_at<Logits16, L>(r, t));
-    }
+    static __device__ __forceinline__ uint32_t lane_key(int t) { return kVec * t; }
+    static __device__ __forceinline__ bool picked(uint32_t key) { return key > 0xFFFFu; }
     static __device__ __forceinline__ int index(uint32_t key) { return static_cast<int>(0xFFFFu - (key & 0xFFFFu)); }
     static __device__ __forceinline__ float value(uint32_t key) {
-        const uint32_t u = key >> 16;
-        return Wide<E>::widen1(static_cast<uint16_t>(u & 0x8000u ? u ^ 0x8000u : ~u));
+        const uint32_t u = (key >> 16) + kNaN + 1;
+        return Wide<E>::widen1(static_cast<uint16_t>(u >= 0x8000u ? u ^ 0x8000u : 0x10000u - u));
     }
 };
 
@@ -332,9 +335,13 @@ __device__ __forceinline__ float exp_all(float (&x)[R], float top) {
     return total;
 }
 
-// LIST: up to 8 picks of binary32 logits.  Bound by instructions: 32768 tokens
-// of 256, k=8, bfloat16 9.5 us, about 600 a wave of four tokens (keys 150, picks
-// 45 each, exponentials 110), where the logits' way from memory takes 3.
+// LIST: up to 8 picks of binary32 logits.  32768 tokens of 256, k=8: bfloat16
+// 9.1 us, 7.9 renormalised, where the logits' way from memory takes 3.  Bound by
+// instructions, about 480 a wave of four tokens: keys 85 (made one by one they
+// were 190, and it took 9.4 and 8.7 us), picks 37 each, exponentials 64 and as
+// much again for their quarter rate.  (The exponent as one fused operation, x
+// log2(e) - top log2(e), needs a case of its own for large logits and was
+// slower, 9.6.)
 template <class T, int L, int R, bool LIST>
 __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;
@@ -351,23 +358,27 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     if constexpr (T::kPacked) {
         // The next pick is the largest key below the last one, that is the
         // largest difference to it modulo 2^32: nothing has to be taken out.
+        // (Keys of what is never picked differ too, and there are k keys at least.)
         uint32_t key[R];
-        T::template keys<L>(raw, t, key);
-        uint32_t last = 0, first = 0, mine = 0;
-        for (int j = 0; j < a.k; ++j) {
-            uint32_t m = key[0] - last;
+        T::template keys<L>(raw, key);
+        uint32_t m = key[0];
+#pragma unroll
+        for (int r = 1; r < R; ++r) m = m > key[r] ? m : key[r];
+        const uint32_t first = max_lanes<L>(m - T::lane_key(t));
+        uint32_t last = first, mine = t == 0 ? first : 0;
+        for (int j = 1; j < a.k; ++j) {
+            const uint32_t base = last + T::lane_key(t);
+            m = key[0] - base;
 #pragma unroll
             for (int r = 1; r < R; ++r) {
-                const uint32_t d = key[r] - last;
+                const uint32_t d = key[r] - base;
                 m = m > d ? m : d;
             }
-            m = max_lanes<L>(m) + last;
-            last = j > 0 && last == 0 ? 0u : m;                 // nothing was left
-            first = j == 0 ? last : first;
+            last += max_lanes<L>(m);
             mine = t == j ? last : mine;
         }
-        if (first != 0) top = T::value(first);
-        if (mine != 0) {
+        if (T::picked(first)) top = T::value(first);
+        if (T::picked(mine)) {
             v = T::value(mine);
             id = T::index(mine);
         }
@@ -423,14 +434,23 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     }
 }
 
-// 32768 tokens of 256, k=8: bfloat16 9.3 us, binary32 11.4 (67 MB, 5.9 TB/s from
+// A wave's accesses of LDS are carried out in order, so between lanes of one
+// wave it is only the compiler that has to keep it.
+__device__ __forceinline__ void order_lds() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// p * (0 - c) for every logit, put together in LDS, where the picks' own
+// weights * (dweights - c) take their places; a token's lanes are in one wave.
+// 32768 tokens of 256, k=8: bfloat16 9.1 us, binary32 11.2 (67 MB, 6.0 TB/s from
 // the last-level cache).
 template <class T, int L, int R>
 __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a) {
-    constexpr int kTokens = kRouterThreads / L;
-    // by fours of a lane's logits, the lanes side by side: no two lanes of an
+    constexpr int kTokens = kRouterThreads / L, kUnits = R / T::kVec;
+    // by units of a lane's logits, the lanes side by side: no two lanes of an
     // access share a bank (with a lane's logits side by side, four did)
-    __shared__ f32x4 picked[kTokens][R / 4][L];
+    __shared__ u32x4 out[kTokens][kUnits][L];
     const int t = threadIdx.x % L;
     const int slot = threadIdx.x / L;
     const size_t token = static_cast<size_t>(blockIdx.x) * kTokens + slot;
@@ -439,8 +459,6 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
     if (!a.renormalize)
         T::template load<L>(static_cast<const char *>(a.logits) + (there ? token : 0) * a.stride * T::kBytes, t,
                             there ? a.experts : 0, raw);
-#pragma unroll
-    for (int q = 0; q < R / 4; ++q) picked[slot][q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     int id = -1;
     float g = 0.0f, w = 0.0f;
     if (there && t < a.k) {
@@ -453,36 +471,40 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
         }
     }
     const float c = sum_lanes<L>(id >= 0 ? g * w : 0.0f);
-    __syncthreads();
-    if (id >= 0) {
-        const int r = id / (T::kVec * L) * T::kVec + id % T::kVec, lane = id / T::kVec % L;
-        picked[slot][r / 4][lane][r % 4] = a.renormalize ? w * (g - c) : g;
-    }
-    __syncthreads();
-    float at[R];
-#pragma unroll
-    for (int q = 0; q < R / 4; ++q) {
-        const f32x4 p = picked[slot][q][t];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[4 * q + i] = p[i];
-    }
-
-    float x[R];
     if (a.renormalize) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = at[r];
+        for (int q = 0; q < kUnits; ++q) out[slot][q][t] = u32x4{0, 0, 0, 0};
     } else {
+        float x[R];
         T::widen(raw, x);
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < R; ++r) top = fmaxf(top, x[r]);     // a NaN is no maximum
         top = reduce_lanes<L>(top, [](float p, float q) { return fmaxf(p, q); });
         const float total = sum_lanes<L>(exp_all(x, top));
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+        const float scale = total > 0.0f ? -c / total : -c;
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = x[r] * inv * (at[r] - c);
+        for (int r = 0; r < R; ++r) x[r] *= scale;
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) out[slot][q][t] = T::narrow(x + q * T::kVec);
     }
-    if (there) T::template store<L>(static_cast<char *>(a.dlogits) + token * a.dstride * T::kBytes, t, a.experts, x);
+    order_lds();
+    if (id >= 0) {
+        auto *unit = reinterpret_cast<typename T::Value *>(&out[slot][id / (T::kVec * L)][id / T::kVec % L]);
+        unit[id % T::kVec] = T::narrow1(w * (g - c));
+    }
+    order_lds();
+    if (!there) return;
+    char *row = static_cast<char *>(a.dlogits) + token * a.dstride * T::kBytes;
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+        const int e = logit_at<T, L>(q * T::kVec, t);
+        const u32x4 v = out[slot][q][t];
+        if (e + T::kVec <= a.experts)
+            store_vec<false>(v, row + e * T::kBytes);
+        else
+            T::store_part(row, e, a.experts, v);
+    }
 }
 
 namespace {

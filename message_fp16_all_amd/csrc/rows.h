@@ -31,6 +31,9 @@ struct Wide<F16> {
     static __device__ __forceinline__ float widen1(uint16_t v) {
         return static_cast<float>(__builtin_bit_cast(_Float16, v));
     }
+    static __device__ __forceinline__ uint16_t narrow1(float v) {
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    }
     static __device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -58,6 +61,9 @@ template <>
 struct Wide<BF16> {
     static __device__ __forceinline__ float widen1(uint16_t v) {
         return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
+    }
+    static __device__ __forceinline__ uint16_t narrow1(float v) {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
     static __device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
 #pragma unroll
