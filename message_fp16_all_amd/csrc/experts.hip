@@ -31,30 +31,41 @@ struct SortArgs {
     int blocks;
 };
 
-// The expert of a slot, counted from `first`; `experts` for a slot that goes
-// nowhere.
-__device__ __forceinline__ int slot_expert(const SortArgs &a, uint32_t s) {
-    const uint32_t e = static_cast<uint32_t>(a.ids[s]) - static_cast<uint32_t>(a.first);
-    return a.ids[s] >= a.first && e < static_cast<uint32_t>(a.experts) ? static_cast<int>(e) : a.experts;
+// The experts of N slots s, s + step, .. below end, their ids loaded together,
+// counted from `first`: `experts` for a slot that goes nowhere, -1 from end on.
+template <int N>
+__device__ __forceinline__ void load_experts(const SortArgs &a, uint32_t s, uint32_t step, uint32_t end,
+                                             int (&e)[N]) {
+    int id[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) id[i] = s + i * step < end ? a.ids[s + i * step] : 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t x = static_cast<uint32_t>(id[i]) - static_cast<uint32_t>(a.first);
+        const bool here = id[i] >= a.first && x < static_cast<uint32_t>(a.experts);
+        e[i] = s + i * step < end ? here ? static_cast<int>(x) : a.experts : -1;
+    }
 }
 
-// Lanes of the wave that hold the same number.
+// Lanes of the wave that hold the same number: those that agree in every bit.
 __device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
-    uint64_t mask = ~0ull;
+    uint32_t lo = ~0u, hi = ~0u;
     for (int b = 0; b < bits; ++b) {
-        const bool one = (e >> b) & 1;
-        const uint64_t ones = __ballot(one);
-        mask &= one ? ones : ~ones;
+        const uint32_t mine = static_cast<uint32_t>(__builtin_amdgcn_sbfe(e, b, 1));      // all ones or zeros
+        const uint64_t ones = __builtin_amdgcn_ballot_w64(mine != 0);
+        lo &= ~(static_cast<uint32_t>(ones) ^ mine);
+        hi &= ~(static_cast<uint32_t>(ones >> 32) ^ mine);
     }
-    return mask;
+    return lo | static_cast<uint64_t>(hi) << 32;
 }
 
-// counts[w][e] = slots of expert e among wave w's share of [begin, end).
-__device__ __forceinline__ void count_share(const SortArgs &a, uint32_t begin, uint32_t end, int *counts) {
-    for (uint32_t s = begin + threadIdx.x % kWave; s < end; s += kWave) {
-        const int e = slot_expert(a, s);
-        if (e < a.experts) atomicAdd(&counts[e], 1);     // whole numbers: the order does not matter
-    }
+// counts[e] += a lane's slots of expert e.
+template <int N>
+__device__ __forceinline__ void count_experts(const SortArgs &a, const int (&e)[N], int *counts) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        // whole numbers: the order does not matter
+        if (static_cast<uint32_t>(e[i]) < static_cast<uint32_t>(a.experts)) atomicAdd(&counts[e[i]], 1);
 }
 
 // The share of a workgroup's slots [begin, end) that a wave takes, in order.
@@ -64,26 +75,46 @@ __device__ __forceinline__ void wave_share(uint32_t begin, uint32_t end, int wav
     *e = *b + per < end ? *b + per : end;
 }
 
-// The wave's slots to their places: next[e] is the place of the next slot of
-// expert e in this wave's share.
-__device__ __forceinline__ void place_share(const SortArgs &a, uint32_t begin, uint32_t end, int *next) {
+// A wave's slots of [begin, end) counted, N of a lane at a time; `e` keeps the
+// last of them.
+template <int N>
+__device__ __forceinline__ void count_share(const SortArgs &a, uint32_t begin, uint32_t end, int *counts,
+                                            int (&e)[N]) {
+    for (uint32_t s = begin; s < end; s += kWave * N) {
+        load_experts(a, s + threadIdx.x % kWave, kWave, end, e);
+        count_experts(a, e, counts);
+    }
+}
+
+// The wave's slots to their places: next[x] is the place of the next slot of
+// expert x in this wave's share.  `e` is from count_share: the ids of a share of
+// up to N slots a lane are not loaded again.
+template <int N>
+__device__ __forceinline__ void place_share(const SortArgs &a, uint32_t begin, uint32_t end, int *next,
+                                            int (&e)[N]) {
     const uint32_t lane = threadIdx.x % kWave;
-    for (uint32_t s0 = begin; s0 < end; s0 += kWave) {
-        const uint32_t s = s0 + lane;
-        const int e = s < end ? slot_expert(a, s) : a.experts;
-        const uint64_t mask = same_lanes(e, a.bits);
-        const int rank = __builtin_popcountll(mask & ((1ull << lane) - 1));
-        int place = -1;
-        if (e < a.experts) place = next[e] + rank;
-        // every lane has read its expert's place before one of them moves it
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (e < a.experts && rank == 0) next[e] = place + __builtin_popcountll(mask);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (s < end) {
-            a.pos[s] = place;
-            if (place >= 0) a.order[place] = static_cast<int32_t>(s);
+    for (uint32_t s0 = begin; s0 < end; s0 += kWave * N) {
+        if (end - begin > kWave * N) load_experts(a, s0 + lane, kWave, end, e);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (s0 + i * kWave >= end) break;
+            const int x = e[i];
+            const bool goes = static_cast<uint32_t>(x) < static_cast<uint32_t>(a.experts);
+            const uint64_t mask = same_lanes(x, a.bits);
+            const int rank = __builtin_popcountll(mask & ((1ull << lane) - 1));
+            int place = -1;
+            if (goes) place = next[x] + rank;
+            // every lane has read its expert's place before one of them moves it
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (goes && rank == 0) next[x] = place + __builtin_popcountll(mask);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (x >= 0) {
+                const uint32_t s = s0 + i * kWave + lane;
+                a.pos[s] = place;
+                if (place >= 0) a.order[place] = static_cast<int32_t>(s);
+            }
         }
     }
 }
@@ -101,13 +132,31 @@ __device__ __forceinline__ int scan_threads(int v, int *tmp, int *total) {
     if (lane == kWave - 1) tmp[wave] = v;
     __syncthreads();
     int sum = 0;
-    for (int w = 0; w < waves; ++w) {
-        const int n = tmp[w];
-        v += w < wave ? n : 0;
-        sum += n;
+    for (int w = 0; w < waves; w += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = tmp[w + i];
+            v += w + i < wave ? n : 0;
+            sum += n;
+        }
     }
     *total = sum;
     return v;
+}
+
+// counts[w][x] of every wave w, to the place of expert x's first slot in that
+// wave's share, from `at` on.  (Four waves at a time, as LDS takes its time.)
+__device__ __forceinline__ void counts_to_places(int *counts, int experts, int x, int waves, int at) {
+    for (int w = 0; w < waves; w += 4) {
+        int n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[i] = counts[(w + i) * experts + x];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            counts[(w + i) * experts + x] = at;
+            at += n[i];
+        }
+    }
 }
 
 __device__ __forceinline__ int padded(int count, int pad) { return (count + pad - 1) / pad * pad; }
@@ -125,10 +174,12 @@ __device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offse
         a.order[p] = -1;
 }
 
-// Everything in one workgroup: 8 slots 3.0 us, 4096 slots of 128 experts 7.0, of
-// which a launch is 1.6; the rest are the barriers and, per wave, 64 slots after
-// another.  Dynamic LDS: [waves][experts] counts, then
-// [experts + 1] offsets, [experts] totals and [waves] for the scan.
+// Everything in one workgroup: 8 slots 3.0 us, 4096 slots of 128 experts 6.1,
+// 8192 8.2, of which a launch is 1.6; the rest are the barriers and, per wave,
+// 64 slots after another.  (Loading every 64 slots' ids when their turn comes,
+// and again to place them, took 7.1 and 10.9.)  Dynamic LDS: [waves][experts]
+// counts, then [experts + 1] offsets, [experts] totals and [waves] for the scan.
+template <int N>
 __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
     extern __shared__ int lds[];
     const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave;
@@ -138,54 +189,57 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_once(SortArgs a) {
     __syncthreads();
     uint32_t b, e;
     wave_share(0, a.slots, wave, waves, &b, &e);
-    count_share(a, b, e, counts + wave * a.experts);
+    int mine[N];
+    count_share(a, b, e, counts + wave * a.experts, mine);
     __syncthreads();
     for (int e0 = 0, base = 0; e0 < a.experts; e0 += blockDim.x) {
         const int x = e0 + threadIdx.x;
         int sum = 0;
         if (x < a.experts)
-            for (int w = 0; w < waves; ++w) sum += counts[w * a.experts + x];
+            for (int w = 0; w < waves; w += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += counts[(w + i) * a.experts + x];
         int all = 0;
         const int end = base + scan_threads(padded(sum, a.pad), tmp, &all);
         if (x < a.experts) {
-            int at = end - padded(sum, a.pad);
+            const int at = end - padded(sum, a.pad);
             totals[x] = sum;
             offsets[x] = at;
             offsets[x + 1] = end;      // the same value as its neighbour's own
-            for (int w = 0; w < waves; ++w) {
-                const int n = counts[w * a.experts + x];
-                counts[w * a.experts + x] = at;
-                at += n;
-            }
+            counts_to_places(counts, a.experts, x, waves, at);
         }
         base += all;
         __syncthreads();
     }
     for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) a.offsets[i] = offsets[i];
-    place_share(a, b, e, counts + wave * a.experts);
+    place_share(a, b, e, counts + wave * a.experts, mine);
     fill_padding(a, offsets, totals);
 }
 
 // The same over many workgroups: counts, then places.  Dynamic LDS: [experts].
+template <int N>
 __global__ __launch_bounds__(kMaxSortThreads) void sort_count(SortArgs a) {
     extern __shared__ int lds[];
     for (int i = threadIdx.x; i < a.experts; i += blockDim.x) lds[i] = 0;
     __syncthreads();
     const uint32_t begin = blockIdx.x * a.chunk;
     const uint32_t end = begin + a.chunk < a.slots ? begin + a.chunk : a.slots;
-    for (uint32_t s = begin + threadIdx.x; s < end; s += blockDim.x) {
-        const int e = slot_expert(a, s);
-        if (e < a.experts) atomicAdd(&lds[e], 1);
+    for (uint32_t s = begin; s < end; s += N * blockDim.x) {
+        int e[N];
+        load_experts(a, s + threadIdx.x, blockDim.x, end, e);
+        count_experts(a, e, lds);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.experts; i += blockDim.x) a.counts[blockIdx.x * a.experts + i] = lds[i];
 }
 
-// Every workgroup adds the counts of all of them up by itself.  Measured
-// against a kernel of one workgroup between the two: 65528 slots of 128
-// experts 10.4 against 12.9 us, 2^20 slots of 256 experts 18.5 against 27.7.
+// Every workgroup adds the counts of all of them up by itself: both kernels take
+// 9.2 us for 65528 slots of 128 experts, 17.5 for 2^20 of 256.  (With a kernel of
+// one workgroup between the two, 12.9 against 10.4 and 27.7 against 18.5 when
+// these were measured.)
 // Dynamic LDS: [waves][experts] counts, then [experts + 1] offsets, [experts]
 // totals, [experts] firsts, [threads] sums and [waves].
+template <int N>
 __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
     extern __shared__ int lds[];
     const int waves = blockDim.x / kWave, wave = threadIdx.x / kWave, threads = blockDim.x;
@@ -197,7 +251,8 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
     const uint32_t end = begin + a.chunk < a.slots ? begin + a.chunk : a.slots;
     uint32_t b, e;
     wave_share(begin, end, wave, waves, &b, &e);
-    count_share(a, b, e, lds + wave * a.experts);
+    int slots[N];
+    count_share(a, b, e, lds + wave * a.experts, slots);
 
     // a thread takes one expert and a run [b0, b1) of workgroups, `parts` runs
     // to an expert; more experts than threads take turns
@@ -240,16 +295,9 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
     }
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i <= a.experts; i += threads) a.offsets[i] = offsets[i];
-    for (int x = threadIdx.x; x < a.experts; x += threads) {
-        int at = firsts[x];
-        for (int w = 0; w < waves; ++w) {
-            const int n = lds[w * a.experts + x];
-            lds[w * a.experts + x] = at;
-            at += n;
-        }
-    }
+    for (int x = threadIdx.x; x < a.experts; x += threads) counts_to_places(lds, a.experts, x, waves, firsts[x]);
     __syncthreads();
-    place_share(a, b, e, lds + wave * a.experts);
+    place_share(a, b, e, lds + wave * a.experts, slots);
     fill_padding(a, offsets, totals);
 }
 
@@ -528,6 +576,7 @@ constexpr size_t kMaxCount = 0x7FFFFFFF;
 constexpr size_t kMaxGroups = 0xFFFFFFFFu / kExpertThreads;
 constexpr size_t kSortBlocks = 256;
 constexpr size_t kSortChunk = 2048;
+constexpr int kSortBatch = 8;
 
 uint32_t sort_chunk(size_t slots) {
     const size_t c = (slots + kSortBlocks - 1) / kSortBlocks;
@@ -739,18 +788,26 @@ extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, i
     const auto lds_for = [&](int threads, int arrays, int more) {
         return (static_cast<size_t>(threads / kWave + arrays) * experts + 1 + more + threads / kWave) * sizeof(int);
     };
+    // The kernel for 1 or 2 slots of a thread where that many do: the code of
+    // eight costs small calls 0.3 us.
+    const auto launch = [&](auto one, auto two, auto many, size_t chunk, int blocks, int threads, size_t lds) {
+        const size_t each = (chunk + threads - 1) / threads;
+        hipLaunchKernelGGL(each <= 1 ? one : each <= 2 ? two : many, dim3(blocks), dim3(threads), lds, s, a);
+    };
     if (slots <= static_cast<size_t>(HR_EXPERTS_SORT_FEW)) {
         // a wave for every 64 slots, but no fewer than 4
         int threads = 256;
         while (threads < most_threads && threads < static_cast<int>(slots)) threads *= 2;
-        hipLaunchKernelGGL(sort_once, dim3(1), dim3(threads), lds_for(threads, 2, 0), s, a);
+        launch(sort_once<1>, sort_once<2>, sort_once<kSortBatch>, slots, 1, threads, lds_for(threads, 2, 0));
         return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
     }
     a.chunk = sort_chunk(slots);
     a.blocks = static_cast<int>((slots + a.chunk - 1) / a.chunk);
-    hipLaunchKernelGGL(sort_count, dim3(a.blocks), dim3(kMaxSortThreads), static_cast<size_t>(experts) * 4, s, a);
+    launch(sort_count<2>, sort_count<2>, sort_count<kSortBatch>, a.chunk, a.blocks, kMaxSortThreads,
+           static_cast<size_t>(experts) * 4);
     if (hipGetLastError() != hipSuccess) return HR_ERR_HIP;
-    hipLaunchKernelGGL(sort_place, dim3(a.blocks), dim3(most_threads), lds_for(most_threads, 3, most_threads), s, a);
+    launch(sort_place<2>, sort_place<2>, sort_place<kSortBatch>, a.chunk, a.blocks, most_threads,
+           lds_for(most_threads, 3, most_threads));
     return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
