@@ -162,12 +162,19 @@ __device__ __forceinline__ void counts_to_places(int *counts, int experts, int x
 __device__ __forceinline__ int padded(int count, int pad) { return (count + pad - 1) / pad * pad; }
 
 // order = -1 in the segments' padding, from their counts, and past the last
-// segment; the experts and the tail are dealt out to the workgroups.
+// segment; the experts and the tail are dealt out to the workgroups.  A lane
+// looks at an expert, and the wave fills the segments that want it in turn.
 __device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offsets, const int *counts) {
     if (a.pad > 1) {
-        const int waves = blockDim.x / kWave;
-        for (int e = blockIdx.x * waves + threadIdx.x / kWave; e < a.experts; e += gridDim.x * waves)
-            for (int p = offsets[e] + counts[e] + threadIdx.x % kWave; p < offsets[e + 1]; p += kWave) a.order[p] = -1;
+        const int waves = gridDim.x * (blockDim.x / kWave), lane = threadIdx.x % kWave;
+        for (int e = (blockIdx.x * blockDim.x + threadIdx.x) / kWave; e < a.experts; e += kWave * waves) {
+            const int x = e + lane * waves;
+            const int from = x < a.experts ? offsets[x] + counts[x] : 0, to = x < a.experts ? offsets[x + 1] : 0;
+            for (uint64_t m = __builtin_amdgcn_ballot_w64(from < to); m != 0; m &= m - 1) {
+                const int l = __builtin_ctzll(m), end = __builtin_amdgcn_readlane(to, l);
+                for (int p = __builtin_amdgcn_readlane(from, l) + lane; p < end; p += kWave) a.order[p] = -1;
+            }
+        }
     }
     for (size_t p = static_cast<size_t>(offsets[a.experts]) + blockIdx.x * blockDim.x + threadIdx.x; p < a.rows;
          p += static_cast<size_t>(gridDim.x) * blockDim.x)
@@ -306,30 +313,37 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
 // Picks of a token whose rows are in flight together.
 constexpr int kPicks = 8;
 
-// Rows of a sorted buffer that stand for no slot, set to zero: sorted rows
-// [r0, r0 + kPadRows) of a workgroup of kExpertThreads.
+// Rows of a sorted buffer that stand for no slot, set to zero: L lanes look at
+// `each` sorted rows, up to kPadRows.  (With a whole workgroup to 8 rows of
+// whatever length and number, 9627 tokens x 64 to 7 rows each took 11.0 us, not
+// 4.4, and 64 x 5120 bytes to 6 rows 3.7, not 2.8.)
 constexpr int kPadRows = 8;
 
 struct Padding {
     const int32_t *order, *offsets;
     uint32_t rows;
-    int experts;
+    int experts, each;
 };
 
-template <bool NT>
+template <int L, bool NT>
 __device__ __forceinline__ void zero_row(char *row, size_t bytes) {
     const size_t whole = bytes / 16;
-    for (size_t i = threadIdx.x; i < whole; i += kExpertThreads)
-        store_vec<NT>(u32x4{0, 0, 0, 0}, row + 16 * i);
-    for (size_t i = 16 * whole + threadIdx.x; i < bytes; i += kExpertThreads) row[i] = 0;
+    for (size_t i = threadIdx.x % L; i < whole; i += L) store_vec<NT>(u32x4{0, 0, 0, 0}, row + 16 * i);
+    for (size_t i = 16 * whole + threadIdx.x % L; i < bytes; i += L) row[i] = 0;
 }
 
-template <class F>
-__device__ __forceinline__ void for_padding(const Padding &q, uint32_t r0, F f) {
+template <int L, class F>
+__device__ __forceinline__ void for_padding(const Padding &q, uint32_t group, F f) {
+    constexpr uint32_t kStep = kExpertThreads / L;
     const uint32_t used = static_cast<uint32_t>(q.offsets[q.experts]);
-    const uint32_t end = used < q.rows ? used : q.rows;
-    for (uint32_t p = r0; p < r0 + kPadRows && p < end; ++p)
-        if (q.order[p] < 0) f(p);
+    const uint32_t end = used < q.rows ? used : q.rows, p = group * q.each * kStep + threadIdx.x / L;
+    if (group * q.each * kStep >= end) return;
+    bool padding[kPadRows];
+#pragma unroll
+    for (int i = 0; i < kPadRows; ++i) padding[i] = i < q.each && p + i * kStep < end && q.order[p + i * kStep] < 0;
+#pragma unroll
+    for (int i = 0; i < kPadRows; ++i)
+        if (padding[i]) f(p + i * kStep);
 }
 
 struct GatherArgs {
@@ -362,9 +376,9 @@ __device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
 template <int L, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (blockIdx.x < a.pad_groups) {
-        for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
-            zero_row<NT>(a.out + p * a.out_stride, a.row_bytes);
-            if (a.scales_out != nullptr) zero_row<NT>(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
+        for_padding<L>(a.pad, blockIdx.x, [&](uint32_t p) {
+            zero_row<L, NT>(a.out + p * a.out_stride, a.row_bytes);
+            if (a.scales_out != nullptr) zero_row<L, NT>(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
         });
         return;
     }
@@ -491,8 +505,8 @@ template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
     __shared__ float sums[kExpertThreads / kWave][kPicks];
     if (blockIdx.x < a.pad_groups) {
-        for_padding(a.pad, blockIdx.x * kPadRows, [&](uint32_t p) {
-            zero_row<NT>(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
+        for_padding<L>(a.pad, blockIdx.x, [&](uint32_t p) {
+            zero_row<L, NT>(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
         });
         return;
     }
@@ -578,6 +592,11 @@ constexpr size_t kSortBlocks = 256;
 constexpr size_t kSortChunk = 2048;
 constexpr int kSortBatch = 8;
 
+// Workgroups for the padding that are spread over before a lane takes a second
+// row.  (Gathers with 512, 1024 and 2048: 955 tokens x 512 bytes to 4 rows padded
+// to 64 3.6, 3.1 and 3.5 us; 64 x 4096 to 8 rows of 512 experts 5.7, 5.8 and 6.3.)
+constexpr size_t kPadGroups = 1024;
+
 uint32_t sort_chunk(size_t slots) {
     const size_t c = (slots + kSortBlocks - 1) / kSortBlocks;
     return static_cast<uint32_t>(c < kSortChunk ? kSortChunk : (c + kWave - 1) / kWave * kWave);
@@ -607,8 +626,11 @@ hipError_t launch_k(K k, size_t grid, hipStream_t s, const A &a) {
 
 // Workgroups of the padding: none where the sorted buffer has no room for any
 // (a sort with padding takes a buffer larger than its slots).
-uint32_t padding_groups(const Padding &q, size_t slots) {
-    return q.order != nullptr && q.rows > slots ? (q.rows + kPadRows - 1) / kPadRows : 0;
+uint32_t padding_groups(Padding &q, size_t slots, int lanes) {
+    const size_t at_once = kExpertThreads / lanes, each = q.rows / (at_once * kPadGroups) + 1;
+    q.each = each < kPadRows ? static_cast<int>(each) : kPadRows;
+    const size_t rows = at_once * q.each;
+    return q.order != nullptr && q.rows > slots ? static_cast<uint32_t>((q.rows + rows - 1) / rows) : 0;
 }
 
 // The variant of a kernel for a call's `tail` and `nt`.
@@ -703,13 +725,13 @@ hr_status combine_grad_impl(const hr_experts_combine_grad_args *q, hr_stream_t s
     a.pos = q->pos;
     a.weights = q->weights;
     a.dweights = q->dweights;
-    a.pad = Padding{q->dz != nullptr ? q->order : nullptr, q->offsets, static_cast<uint32_t>(q->rows), q->experts};
+    a.pad = Padding{q->dz != nullptr ? q->order : nullptr, q->offsets, static_cast<uint32_t>(q->rows), q->experts, 1};
     a.tokens = static_cast<uint32_t>(q->tokens);
     a.rows = static_cast<uint32_t>(q->rows);
     a.k = q->k;
     a.hidden = static_cast<int>(q->hidden);
-    a.pad_groups = padding_groups(a.pad, slots);
     const int lanes = lanes_for((q->hidden + 7) / 8);
+    a.pad_groups = padding_groups(a.pad, slots, lanes);
     const size_t grid = a.pad_groups + (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
     if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -857,13 +879,13 @@ extern "C" HR_API hr_status hr_experts_gather(const hr_experts_gather_args *q, h
         a.scales_out_stride = so * 4;
         a.scale_units = static_cast<uint32_t>((a.scale_bytes + 15) / 16);
     }
-    a.pad = Padding{q->order, q->offsets, static_cast<uint32_t>(q->rows), q->experts};
+    a.pad = Padding{q->order, q->offsets, static_cast<uint32_t>(q->rows), q->experts, 1};
     a.tokens = static_cast<uint32_t>(q->tokens);
     a.rows = static_cast<uint32_t>(q->rows);
     a.k = q->k;
-    a.pad_groups = padding_groups(a.pad, slots);
     const size_t units = static_cast<size_t>(a.units) + a.scale_units;
     const int lanes = lanes_for(units);
+    a.pad_groups = padding_groups(a.pad, slots, lanes);
     a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + kExpertThreads - 1) / kExpertThreads) : 1;
     const size_t grid =
         a.pad_groups + (lanes == kExpertThreads ? q->tokens * a.splits

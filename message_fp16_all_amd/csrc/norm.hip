@@ -110,7 +110,7 @@ __device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
 // at once: few, because registers held for loads keep waves off the compute
 // unit (2048 x 8192 of one contribution with B = 9, 4 and 3: 26.7, 24.1 and
 // 23.6 us; of eight 61.6, 60.6 and 60.7), unless there are too few rows for
-// many waves anyway (kSpreadRows).
+// many waves anyway (kSpreadGroups).
 template <class E, int U, int L, bool TAIL, bool NT, int B>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
     __shared__ float sums[kNormMaxWaves];
@@ -495,12 +495,13 @@ RowShape row_shape(int hidden, bool spread = false) {
     return {0, per, threads};
 }
 
-// Few rows of many operands wait for their loads: one unit per thread, twice
-// the threads, nine operands at once.  (In a graph, 64 x 6144 of eight
-// contributions 5.6 us with two units per thread, 5.0 with one and four
-// operands at once, 4.2 with nine; 2048 x 8192 of eight 61.6 with two units
-// and 67.8 with one.)
-constexpr size_t kSpreadRows = 512;
+// Few workgroups with many operands wait for their loads: nine operands at
+// once, and of long rows one unit per thread, twice the threads.  (In a graph,
+// 64 x 6144 of eight contributions 5.6 us with two units per thread, 5.0 with
+// one and four operands at once, 4.2 with nine; 2048 x 8192 of eight 61.6 with
+// two units and 67.8 with one; 8192 x 64 of sixteen 8.4 us with four operands at
+// once, 6.5 with nine, 32768 x 64 15.1 either way.)
+constexpr size_t kSpreadGroups = 512;
 constexpr int kSpreadOperands = 5;
 
 // A call that moves this many bytes or more passes the caches by
@@ -520,7 +521,7 @@ constexpr size_t kStreamBytes = size_t(1) << 27;
 enum Mode {
     kCached,
     kStreamed,
-    kSmall        // norm: spread (kSpreadRows); gradient: few rows
+    kSmall        // norm: spread (kSpreadGroups); gradient: few rows
 };
 
 template <template <class, int, int, bool, Mode> class K, class E, class A>
@@ -549,7 +550,7 @@ hipError_t launch_rows(const RowShape &s, bool tail, Mode mode, size_t grid, siz
 
 template <class E, int U, int L, bool TAIL, Mode M>
 struct NormKernel {
-    static constexpr int kOperandsAtOnce = U == 4 ? 2 : U == 1 && L == 0 && M == kSmall ? 9 : 4;
+    static constexpr int kOperandsAtOnce = U == 4 ? 2 : U == 1 && M == kSmall ? 9 : 4;
     static constexpr auto kernel = norm_rows<E, U, L, TAIL, M == kStreamed, kOperandsAtOnce>;
 };
 
@@ -568,15 +569,21 @@ size_t groups_of(size_t rows, const RowShape &s) {
 // Workgroups of the gradient, hence partial sums of dweight.  Up to four on a
 // compute unit and 16 waves (8 where a workgroup takes several rows at once),
 // but with eight rows or more to each, so that the partial sums stay small
-// beside the rows.  (16384 x 1024 with 512, 1024 and 2048 workgroups: 40, 30
-// and 34 us; 4097 x 5120 with 256 and 512: 41 and 35; 2048 x 8192 with 256, 512
-// and 1024: 32, 33 and 36.)
+// beside the rows: one on a compute unit at least, and where rows are short two
+// while each has two rows.  (16384 x 1024 with 512, 1024 and 2048 workgroups:
+// 40, 30 and 34 us; 4097 x 5120 with 256 and 512: 41 and 35; 2048 x 8192 with
+// 256, 512 and 1024: 31, 33 and 36; 2048 x 2048 with 256, 512 and 1024: 14.1,
+// 12.2 and 14.3; 759 x 4096 with 256 and 380: 10.8 and 13.3.)
+constexpr int kShortRow = 2048;
+
 size_t grad_groups(size_t rows, int hidden, int cus) {
     const RowShape s = row_shape(hidden);
-    const size_t groups = groups_of(rows, s);
+    const size_t groups = groups_of(rows, s), n = static_cast<size_t>(cus);
     const int fit = (s.lanes > 0 ? 8 : 16) * kWave / s.threads;
-    const size_t most = static_cast<size_t>(cus) * (fit < 1 ? 1 : fit < 4 ? fit : 4);
-    const size_t deep = groups / 8 > static_cast<size_t>(cus) ? groups / 8 : static_cast<size_t>(cus);
+    const size_t most = n * (fit < 1 ? 1 : fit < 4 ? fit : 4);
+    const size_t two = groups / 2 < 2 * n ? groups / 2 : 2 * n;
+    const size_t least = hidden <= kShortRow && two > n ? two : n;
+    const size_t deep = groups / 8 > least ? groups / 8 : least;
     const size_t cap = deep < most ? deep : most;
     return groups < cap ? groups : cap;
 }
@@ -601,7 +608,8 @@ hr_status norm_impl(const hr_rmsnorm_args *q, hr_stream_t stream) {
     if (q->group != 0 && q->group != 32 && q->group != 64 && q->group != 128) return HR_ERR_INVALID_ARG;
     if (q->hidden > HR_RMSNORM_MAX_HIDDEN || q->rows > kMaxRows) return HR_ERR_TOO_LARGE;
     if (q->rows == 0) return HR_OK;
-    const bool spread = q->rows <= kSpreadRows && q->G + (q->residual != nullptr) >= kSpreadOperands;
+    const bool spread = groups_of(q->rows, row_shape(static_cast<int>(q->hidden), true)) <= kSpreadGroups &&
+                        q->G + (q->residual != nullptr) >= kSpreadOperands;
     const RowShape s = row_shape(static_cast<int>(q->hidden), spread);
     if (groups_of(q->rows, s) > 0xFFFFFFFFu / s.threads) return HR_ERR_TOO_LARGE;   // work-items of a launch
     if (q->out == nullptr && q->residual_out == nullptr && q->codes == nullptr && q->rstd == nullptr)
