@@ -83,6 +83,40 @@ def test_sort(tokens, k, experts, pad):
     check_sort(ids, 0, experts, pad)
 
 
+# both sides of one, two and eight slots of a thread, and shares of a wave above
+# what it keeps: up to 512 experts a workgroup has 1024 threads, beyond them 512
+@pytest.mark.parametrize("slots,experts", [
+    (256, 384), (257, 384), (512, 600), (513, 600), (1024, 40), (1025, 40), (1024, 600), (1025, 600), (2048, 40),
+    (2049, 40), (4096, 600), (4097, 600), (8192, 600), (8192, 40), (525000, 40), (525000, 600), (1100000, 600),
+    (2200000, 40)])
+def test_sort_shares(slots, experts):
+    ids = np.random.default_rng(slots).integers(-1, experts + 2, (slots, 1))
+    check_sort(ids, 0, experts, 16)
+    ids[:] = experts - 1                                        # one expert takes all
+    check_sort(ids, 0, experts, 3)
+
+
+# few and many sorted rows: one to eight of them to the same lanes
+@pytest.mark.parametrize("tokens,k,experts,pad", [(9, 3, 384, 16), (900, 4, 60, 64), (3000, 6, 500, 40),
+                                                  (9000, 7, 512, 16)])
+@pytest.mark.parametrize("width", [64, 200, 1100])
+def test_padding_is_zero(tokens, k, experts, pad, width):
+    offsets, order, pos, o, ph, used = buffers(tokens, tokens, k, experts, pad)
+    m = Maker(width)
+    x = m.normal(tokens, width, dtype=torch.float16)
+    out = m.place(len(o), width, torch.float16, width + 4, 2)
+    print(f"padding {tokens}x{width} k={k} experts={experts} pad={pad}", flush=True)
+    hr.experts_gather(x.to(DEV), pos, out, offsets=offsets, order=order)
+    torch.cuda.synchronize()
+    want = torch.full((len(o), width), 7.0).half()
+    want[:used] = 0
+    want[torch.from_numpy(o >= 0)] = x[torch.from_numpy(o[o >= 0] // k)]
+    assert torch.equal(out.cpu(), want)
+    m.check_frames()
+    run_grad(m, torch.float16, tokens, width, k, pos, ph, offsets, order, o, weights=torch.rand(tokens, k, generator=m.g),
+             used=used)
+
+
 @pytest.mark.parametrize("tokens", [700, 40000])
 def test_sort_of_a_rank(tokens):
     """A rank's share of the experts, every id outside it of any value."""

@@ -102,6 +102,15 @@ def test_rows(rows):
         run_case(rows, "bf16", rows, 5120, 2, group=0)
 
 
+# both sides of 512 workgroups of 16, 8 and 4 rows and of one: how many operands
+# a thread loads at once
+@pytest.mark.parametrize("rows,hidden", [(8192, 72), (8193, 72), (4096, 200), (4097, 200), (2048, 511), (2049, 511),
+                                         (512, 1032), (513, 1032)])
+@pytest.mark.parametrize("G", [4, 10, 16])
+def test_few_and_many_workgroups(rows, hidden, G):
+    run_case(rows, "bf16", rows, hidden, G, group=64)
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("hidden,stride,offset", [(128, 130, 1), (500, 777, 3), (4096, 4099, 1), (5121, 5121, 5),
                                                   (9000, 9008, 7), (32768, 40001, 1)])
@@ -277,6 +286,13 @@ def test_grad_rows(rows):
     if rows < 8000:
         run_grad(rows, "f16", rows, 4096)
         run_grad(rows, "bf16", rows, 8200, weight="f32", workspace=False)
+
+
+# short and long rows, with one, two and more workgroups on a compute unit
+@pytest.mark.parametrize("rows,hidden", [(513, 2048), (514, 2048), (700, 2049), (1024, 2048), (1031, 2047), (2100, 1327),
+                                         (4100, 300), (8200, 200), (16400, 64), (40000, 65)])
+def test_grad_workgroups(rows, hidden):
+    run_grad(rows, "bf16", rows, hidden, weight="f32")
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
