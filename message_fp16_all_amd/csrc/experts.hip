@@ -13,6 +13,8 @@
 // or written once and its k expert rows are all in flight together.
 #include "rows.h"
 
+#include <type_traits>
+
 namespace hr {
 
 constexpr int kExpertThreads = 256;
@@ -369,10 +371,11 @@ __device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
 }
 
 // L lanes per token (L = kExpertThreads: its units are also split over
-// workgroups), one unit per lane and step.  The token's row is read once and
-// stored k times, so the traffic is nearly all writes: 8191 tokens x 4096 to 8
-// rows each 100 us, 6.0 TB/s.  Its own row is read through the caches:
-// non-temporal loads of it took 116 us.
+// workgroups), one unit per lane.  The token's row is read once and stored k
+// times, so the traffic is nearly all writes: 8191 tokens x 4096 to 8 rows each
+// 98 us, 6.1 TB/s; 8192 x 4096 with one pick in eight here 19 us, 7.0 TB/s (26 with
+// the places read through the scalar cache and looked at one by one).  Its own
+// row is read through the caches: non-temporal loads of it took 116 us, not 99.
 template <int L, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (blockIdx.x < a.pad_groups) {
@@ -389,32 +392,42 @@ __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (t >= a.tokens) return;
     const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
     const uint32_t units = a.units + a.scale_units;
-    const uint32_t step = L == kExpertThreads ? kExpertThreads * a.splits : L;
-    for (uint32_t i = split * kExpertThreads + threadIdx.x % L; i < units; i += step) {
-        const bool data = i < a.units;
-        const size_t bytes = data ? a.row_bytes : a.scale_bytes;
-        const char *src = data ? a.in + t * a.in_stride : a.scales + t * a.scales_stride;
-        char *dst = data ? a.out : a.scales_out;
-        const size_t stride = data ? a.out_stride : a.scales_out_stride;
-        const uint32_t u = data ? i : i - a.units;
+    const uint32_t i = split * kExpertThreads + threadIdx.x % L;
+    const bool data = i < a.units, mine = i < units;
+    const size_t bytes = data ? a.row_bytes : a.scale_bytes;
+    const char *src = data ? a.in + t * a.in_stride : a.scales + t * a.scales_stride;
+    char *dst = data ? a.out : a.scales_out;
+    const size_t stride = data ? a.out_stride : a.scales_out_stride;
+    const uint32_t u = data ? i : i - a.units;
+    const size_t o = bytes >= 16 ? unit_at(u, bytes) : 0;
+    u32x4 v = {0, 0, 0, 0};
+    if (mine && bytes >= 16) v = load_vec<false>(src + o);
+    const auto put = [&](uint32_t p) {
+        if (bytes >= 16) {
+            store_vec<NT>(v, dst + p * stride + o);
+        } else {
+            for (size_t b = 0; b < bytes; ++b) dst[p * stride + b] = src[b];
+        }
+    };
+    if constexpr (L >= kWave) {
+        // a lane holds a pick's place: they are read with the row, and picks
+        // that go nowhere take no turn
+        const int lane = threadIdx.x % kWave;
+        const uint32_t p = lane < a.k ? static_cast<uint32_t>(pos[lane]) : ~0u;
+        for (uint64_t left = __builtin_amdgcn_ballot_w64(p < a.rows); left != 0; left &= left - 1) {
+            const uint32_t to = __builtin_amdgcn_readlane(p, __builtin_ctzll(left));
+            if (mine) put(to);
+        }
+    } else {
         // the places first: they lie in memory that the stores could be thought
         // to change, and would be waited for one by one
         for (int j0 = 0; j0 < a.k; j0 += kPicks) {
             uint32_t p[kPicks];
 #pragma unroll
             for (int j = 0; j < kPicks; ++j) p[j] = j0 + j < a.k ? static_cast<uint32_t>(pos[j0 + j]) : ~0u;
-            if (bytes >= 16) {
-                const size_t o = unit_at(u, bytes);
-                const u32x4 v = load_vec<false>(src + o);
 #pragma unroll
-                for (int j = 0; j < kPicks; ++j)
-                    if (p[j] < a.rows) store_vec<NT>(v, dst + p[j] * stride + o);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPicks; ++j)
-                    if (p[j] < a.rows)
-                        for (size_t o = 0; o < bytes; ++o) dst[p[j] * stride + o] = src[o];
-            }
+            for (int j = 0; j < kPicks; ++j)
+                if (mine && p[j] < a.rows) put(p[j]);
         }
     }
 }
@@ -431,12 +444,16 @@ struct CombineArgs {
 };
 
 // The sum is binary32 and runs in pick order, the addend first; one rounding.
-// Bound by HBM: 8191 tokens x 4096 of 8 picks 98 us, 6.0 TB/s.  A lane has up to
-// 8 loads in flight, which with 8 waves on every SIMD is more than a compute
-// unit needs to keep HBM busy; two units per lane were no faster (117.1 against
-// 116.8 us before the rows passed the caches by).
-template <class E, int L, bool TAIL, bool NT>
-__global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
+// L lanes per token (L = kExpertThreads: its units are also split over
+// workgroups), U units of a lane at once.  Bound by HBM: 8191 tokens x 4096 of 8
+// picks 101 us, 6.0 TB/s; 8192 x 4096 of 8 picks, one in eight of them here, 25
+// (40 with the places read through the scalar cache and looked at one by one).
+// Rows that pass the caches by are read by 6 waves of a SIMD: 8 have so many rows
+// open that 16384 x 4096 of 8 picks all here take 207 us, not 205 (4 waves 200),
+// but the 25 us above are 23 with 8 and 30 with 4.
+template <class E, int L, int U, bool TAIL, bool NT>
+__global__ __launch_bounds__(kExpertThreads)
+__attribute__((amdgpu_waves_per_eu(1, NT && L >= kWave ? 6 : 8))) void combine_rows(CombineArgs a) {
     constexpr uint32_t kTokens = kExpertThreads / L;
     const uint32_t t = L == kExpertThreads ? blockIdx.x / a.splits : blockIdx.x * kTokens + threadIdx.x / L;
     const uint32_t split = L == kExpertThreads ? blockIdx.x % a.splits : 0;
@@ -444,8 +461,66 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
     const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
     const float *weights = a.weights != nullptr ? a.weights + static_cast<size_t>(t) * a.k : nullptr;
     const int units = (a.hidden + 7) / 8;
-    const int step = L == kExpertThreads ? static_cast<int>(kExpertThreads * a.splits) : L;
-    for (int i = static_cast<int>(split * kExpertThreads + threadIdx.x % L); i < units; i += step) {
+    if constexpr (L >= kWave) {
+        // A lane holds a pick's place and weight, so that both are read at
+        // once and picks that go nowhere take no turn.  All lanes of a wave stay
+        // to be asked for them: one without a unit loads the row's last.
+        constexpr int kAtOnce = kPicks / U;
+        const int lane = threadIdx.x % kWave;
+        const uint32_t p = lane < a.k ? static_cast<uint32_t>(pos[lane]) : ~0u;
+        const float w = weights != nullptr && lane < a.k ? weights[lane] : 1.0f;
+        const int i0 = static_cast<int>(split) * kExpertThreads * U + threadIdx.x % L;
+        if (i0 - lane >= units) return;
+        const auto unit = [&](int u) {
+            const int i = i0 + u * L;
+            return Unit<TAIL>(i < units ? i : units - 1, a.hidden);
+        };
+        float sum[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            u32x4 x = {0, 0, 0, 0};
+            if (a.addend != nullptr) x = unit(u).load(a.addend + t * a.addend_stride);
+            Wide<E>::widen(x, sum[u]);
+        }
+        uint64_t left = __builtin_amdgcn_ballot_w64(p < a.rows);
+        // (a full batch apart, whose rows are then added one by one as they come)
+        const auto batch = [&](auto full) {
+            u32x4 z[kAtOnce][U];
+            float weight[kAtOnce];
+            uint64_t next = left;
+#pragma unroll
+            for (int b = 0; b < kAtOnce; ++b) {
+                if (!full && next == 0) break;
+                const int from = __builtin_ctzll(next);
+                next &= next - 1;
+                const uint16_t *row = a.z + static_cast<uint32_t>(__builtin_amdgcn_readlane(p, from)) * a.z_stride;
+                weight[b] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), from));
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u == 0 || i0 + u * L < units) z[b][u] = unit(u).template load<NT>(row);
+            }
+#pragma unroll
+            for (int b = 0; b < kAtOnce; ++b) {
+                if (!full && left == 0) break;
+                left &= left - 1;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[8];
+                    Wide<E>::widen(z[b][u], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[u][e] = fmaf(weight[b], f[e], sum[u][e]);
+                }
+            }
+        };
+        while (__builtin_popcountll(left) >= kAtOnce) batch(std::true_type{});
+        while (left != 0) batch(std::false_type{});
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            // its own values only: out may be the addend, which a neighbour reads
+            if (i0 + u * L < units) unit(u).template store_own<NT>(a.out + t * a.out_stride, Wide<E>::narrow(sum[u]));
+        return;
+    }
+    for (int i = threadIdx.x % L; i < units; i += L) {
         const Unit<TAIL> at(i, a.hidden);
         float sum[8];
         if (a.addend != nullptr) {
@@ -480,7 +555,6 @@ __global__ __launch_bounds__(kExpertThreads) void combine_rows(CombineArgs a) {
                 }
             }
         }
-        // its own values only: out may be the addend, which a neighbour reads
         at.template store_own<NT>(a.out + t * a.out_stride, Wide<E>::narrow(sum));
     }
 }
@@ -500,7 +574,8 @@ struct CombineGradArgs {
 
 // L lanes per token over all of its row, since the weights' gradients are sums
 // over it; kPicks of them at a time in registers.  Bound by HBM: 4096 tokens x
-// 8192 of 4 picks 122 us, 630 MB with the padding, 5.2 TB/s.
+// 8192 of 4 picks 112 us, 630 MB with the padding, 5.6 TB/s; 8192 x 4096 with one
+// pick in eight here 32 us (44 with the places read through the scalar cache).
 template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
     __shared__ float sums[kExpertThreads / kWave][kPicks];
@@ -517,6 +592,14 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
     const bool here = t < a.tokens;
     const int32_t *pos = a.pos + static_cast<size_t>(t) * a.k;
     const int units = here ? (a.hidden + 7) / 8 : 0;
+    // (a lane holds a pick's place and weight, which are read at once)
+    const int pick = threadIdx.x % kWave;
+    uint32_t place = ~0u;
+    float weight = 1.0f;
+    if (L >= kWave && here && pick < a.k) {
+        place = static_cast<uint32_t>(pos[pick]);
+        if (a.weights != nullptr) weight = a.weights[static_cast<size_t>(t) * a.k + pick];
+    }
     for (int j0 = 0; j0 < a.k; j0 += kPicks) {
         uint32_t p[kPicks];
         float w[kPicks], dot[kPicks];
@@ -525,7 +608,10 @@ __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradA
             p[j] = ~0u;
             w[j] = 1.0f;
             dot[j] = 0.0f;
-            if (here && j0 + j < a.k) {
+            if constexpr (L >= kWave) {
+                p[j] = static_cast<uint32_t>(__builtin_amdgcn_readlane(place, j0 + j));
+                w[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), j0 + j));
+            } else if (here && j0 + j < a.k) {
                 p[j] = static_cast<uint32_t>(pos[j0 + j]);
                 if (a.weights != nullptr) w[j] = a.weights[static_cast<size_t>(t) * a.k + j0 + j];
             }
@@ -634,9 +720,9 @@ uint32_t padding_groups(Padding &q, size_t slots, int lanes) {
 }
 
 // The variant of a kernel for a call's `tail` and `nt`.
-#define HR_VARIANT(K, L)                                                      \
-    (tail ? (nt ? K<E, L, true, true> : K<E, L, true, false>)                 \
-          : (nt ? K<E, L, false, true> : K<E, L, false, false>))
+#define HR_VARIANT(K, ...)                                                                  \
+    (tail ? (nt ? K<E, __VA_ARGS__, true, true> : K<E, __VA_ARGS__, true, false>)           \
+          : (nt ? K<E, __VA_ARGS__, false, true> : K<E, __VA_ARGS__, false, false>))
 
 template <class E>
 hr_status combine_impl(const hr_experts_combine_args *q, hr_stream_t stream) {
@@ -674,15 +760,21 @@ hr_status combine_impl(const hr_experts_combine_args *q, hr_stream_t stream) {
     a.hidden = static_cast<int>(q->hidden);
     const size_t units = (q->hidden + 7) / 8;
     const int lanes = lanes_for(units);
-    a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + kExpertThreads - 1) / kExpertThreads) : 1;
+    // two units of a lane where a second workgroup would have less than half of
+    // its lanes busy (8192 tokens x 2304 of 2 picks 28.6 and 23.2 us; with two
+    // full workgroups of such a token's row the second unit only costs waves)
+    const int at_once = units > kExpertThreads && units < kExpertThreads * 3 / 2 ? 2 : 1;
+    const size_t share = static_cast<size_t>(kExpertThreads) * at_once;
+    a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + share - 1) / share) : 1;
     const size_t grid = lanes == kExpertThreads ? q->tokens * a.splits
                                                 : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
     if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool nt = slots * width >= kStreamBytes, tail = q->hidden % 8 != 0;
-    const hipError_t e = lanes == 16   ? launch_k(HR_VARIANT(combine_rows, 16), grid, s, a)
-                         : lanes == 64 ? launch_k(HR_VARIANT(combine_rows, 64), grid, s, a)
-                                       : launch_k(HR_VARIANT(combine_rows, kExpertThreads), grid, s, a);
+    const hipError_t e = lanes == 16    ? launch_k(HR_VARIANT(combine_rows, 16, 1), grid, s, a)
+                         : lanes == 64  ? launch_k(HR_VARIANT(combine_rows, 64, 1), grid, s, a)
+                         : at_once == 1 ? launch_k(HR_VARIANT(combine_rows, kExpertThreads, 1), grid, s, a)
+                                        : launch_k(HR_VARIANT(combine_rows, kExpertThreads, 2), grid, s, a);
     return e == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
