@@ -448,9 +448,9 @@ struct CombineArgs {
 // workgroups), U units of a lane at once.  Bound by HBM: 8191 tokens x 4096 of 8
 // picks 101 us, 6.0 TB/s; 8192 x 4096 of 8 picks, one in eight of them here, 25
 // (40 with the places read through the scalar cache and looked at one by one).
-// Rows that pass the caches by are read by 6 waves of a SIMD: 8 have so many rows
-// open that 16384 x 4096 of 8 picks all here take 207 us, not 205 (4 waves 200),
-// but the 25 us above are 23 with 8 and 30 with 4.
+// Rows that pass the caches by are read by up to 6 waves of a SIMD, between what
+// is best for rows that are all here (16384 x 4096 of 8 picks with 8, 6 and 4
+// waves 207, 205 and 200 us) and for few of them (the 25 us above: 23, 25, 30).
 template <class E, int L, int U, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads)
 __attribute__((amdgpu_waves_per_eu(1, NT && L >= kWave ? 6 : 8))) void combine_rows(CombineArgs a) {
