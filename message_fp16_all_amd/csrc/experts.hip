@@ -173,8 +173,9 @@ __device__ __forceinline__ void fill_padding(const SortArgs &a, const int *offse
             const int x = e + lane * waves;
             const int from = x < a.experts ? offsets[x] + counts[x] : 0, to = x < a.experts ? offsets[x + 1] : 0;
             for (uint64_t m = __builtin_amdgcn_ballot_w64(from < to); m != 0; m &= m - 1) {
-                const int l = __builtin_ctzll(m), end = __builtin_amdgcn_readlane(to, l);
-                for (int p = __builtin_amdgcn_readlane(from, l) + lane; p < end; p += kWave) a.order[p] = -1;
+                const int l = __builtin_ctzll(m);
+                const uint32_t begin = __builtin_amdgcn_readlane(from, l), end = __builtin_amdgcn_readlane(to, l);
+                for (uint32_t p = begin + lane; p < end; p += kWave) a.order[p] = -1;
             }
         }
     }

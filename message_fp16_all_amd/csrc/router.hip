@@ -162,7 +162,6 @@ __device__ __forceinline__ int logit_at(int r, int t) {
 }
 
 struct Logits32 {
-    using Value = float;
     static constexpr size_t kBytes = 4;
     static constexpr int kVec = 4;
     static constexpr bool kPacked = false;
@@ -221,7 +220,6 @@ struct Logits32 {
 
 template <class E>
 struct Logits16 {
-    using Value = uint16_t;
     static constexpr size_t kBytes = 2;
     static constexpr int kVec = 8;
     static constexpr bool kPacked = true;
@@ -490,8 +488,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a)
     }
     order_lds();
     if (id >= 0) {
-        auto *unit = reinterpret_cast<typename T::Value *>(&out[slot][id / (T::kVec * L)][id / T::kVec % L]);
-        unit[id % T::kVec] = T::narrow1(w * (g - c));
+        const auto v = T::narrow1(w * (g - c));
+        char *unit = reinterpret_cast<char *>(&out[slot][id / (T::kVec * L)][id / T::kVec % L]);
+        __builtin_memcpy(unit + id % T::kVec * sizeof(v), &v, sizeof(v));
     }
     order_lds();
     if (!there) return;
