@@ -799,7 +799,8 @@ typedef struct {
     const int32_t *pos;       /* the sort's                                       */
     const int32_t *order;     /* the sort's; NULL: padding rows are left alone    */
     const int32_t *offsets;   /* the sort's; with order                           */
-    size_t tokens, rows;      /* rows: of out, and entries of order               */
+    size_t tokens, rows;      /* rows: of out, and entries of order; the sort's, or
+                                 the first of them (offsets[experts] are used)    */
     size_t row_bytes, in_stride, out_stride;                /* bytes; 0 = row_bytes */
     size_t scales_width, scales_stride, scales_out_stride;  /* scales; 0 = width  */
     int k, experts;

@@ -317,8 +317,8 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_place(SortArgs a) {
 constexpr int kPicks = 8;
 
 // Rows of a sorted buffer that stand for no slot, set to zero: L lanes look at
-// `each` sorted rows, up to kPadRows.  (With a whole workgroup to 8 rows of
-// whatever length and number, 9627 tokens x 64 to 7 rows each took 11.0 us, not
+// `each` sorted rows at a time, up to kPadRows.  (With a whole workgroup to 8 rows
+// of whatever length and number, 9627 tokens x 64 to 7 rows each took 11.0 us, not
 // 4.4, and 64 x 5120 bytes to 6 rows 3.7, not 2.8.)
 constexpr int kPadRows = 8;
 
@@ -336,17 +336,19 @@ __device__ __forceinline__ void zero_row(char *row, size_t bytes) {
 }
 
 template <int L, class F>
-__device__ __forceinline__ void for_padding(const Padding &q, uint32_t group, F f) {
+__device__ __forceinline__ void for_padding(const Padding &q, uint32_t group, uint32_t groups, F f) {
     constexpr uint32_t kStep = kExpertThreads / L;
-    const uint32_t used = static_cast<uint32_t>(q.offsets[q.experts]);
-    const uint32_t end = used < q.rows ? used : q.rows, p = group * q.each * kStep + threadIdx.x / L;
-    if (group * q.each * kStep >= end) return;
-    bool padding[kPadRows];
+    const uint32_t used = static_cast<uint32_t>(q.offsets[q.experts]), share = q.each * kStep;
+    const uint32_t end = used < q.rows ? used : q.rows;
+    for (uint32_t p0 = group * share; p0 < end; p0 += groups * share) {
+        const uint32_t p = p0 + threadIdx.x / L;
+        bool padding[kPadRows];
 #pragma unroll
-    for (int i = 0; i < kPadRows; ++i) padding[i] = i < q.each && p + i * kStep < end && q.order[p + i * kStep] < 0;
+        for (int i = 0; i < kPadRows; ++i) padding[i] = i < q.each && p + i * kStep < end && q.order[p + i * kStep] < 0;
 #pragma unroll
-    for (int i = 0; i < kPadRows; ++i)
-        if (padding[i]) f(p + i * kStep);
+        for (int i = 0; i < kPadRows; ++i)
+            if (padding[i]) f(p + i * kStep);
+    }
 }
 
 struct GatherArgs {
@@ -380,7 +382,7 @@ __device__ __forceinline__ size_t unit_at(uint32_t i, size_t bytes) {
 template <int L, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void gather_rows(GatherArgs a) {
     if (blockIdx.x < a.pad_groups) {
-        for_padding<L>(a.pad, blockIdx.x, [&](uint32_t p) {
+        for_padding<L>(a.pad, blockIdx.x, a.pad_groups, [&](uint32_t p) {
             zero_row<L, NT>(a.out + p * a.out_stride, a.row_bytes);
             if (a.scales_out != nullptr) zero_row<L, NT>(a.scales_out + p * a.scales_out_stride, a.scale_bytes);
         });
@@ -581,7 +583,7 @@ template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {
     __shared__ float sums[kExpertThreads / kWave][kPicks];
     if (blockIdx.x < a.pad_groups) {
-        for_padding<L>(a.pad, blockIdx.x, [&](uint32_t p) {
+        for_padding<L>(a.pad, blockIdx.x, a.pad_groups, [&](uint32_t p) {
             zero_row<L, NT>(reinterpret_cast<char *>(a.dz + p * a.dz_stride), static_cast<size_t>(a.hidden) * 2);
         });
         return;
@@ -679,9 +681,12 @@ constexpr size_t kSortBlocks = 256;
 constexpr size_t kSortChunk = 2048;
 constexpr int kSortBatch = 8;
 
-// Workgroups for the padding that are spread over before a lane takes a second
-// row.  (Gathers with 512, 1024 and 2048: 955 tokens x 512 bytes to 4 rows padded
-// to 64 3.6, 3.1 and 3.5 us; 64 x 4096 to 8 rows of 512 experts 5.7, 5.8 and 6.3.)
+// Workgroups for the padding.  Few rows are spread over them before a lane takes
+// a second one (gathers with 512, 1024 and 2048: 955 tokens x 512 bytes to 4 rows
+// padded to 64 3.6, 3.1 and 3.5 us; 64 x 4096 to 8 rows of 512 experts 5.7, 5.8
+// and 6.3), and many take turns in them (8191 tokens x 4096 to 8 rows, none of them
+// padding, with 1024, 2048 and 2^18: 104.5, 110.8 and 112.9 us, 105.4 unasked;
+// 2000 x 4096 to 8 rows padded to 64, 32 us in all three).
 constexpr size_t kPadGroups = 1024;
 
 uint32_t sort_chunk(size_t slots) {
@@ -711,13 +716,16 @@ hipError_t launch_k(K k, size_t grid, hipStream_t s, const A &a) {
     return hipGetLastError();
 }
 
-// Workgroups of the padding: none where the sorted buffer has no room for any
-// (a sort with padding takes a buffer larger than its slots).
-uint32_t padding_groups(Padding &q, size_t slots, int lanes) {
+// Workgroups of the padding beside `others`, for every row that an order comes
+// with.  (The buffer's size says nothing: the segments of a rank's share of the
+// picks are padded and still fit into fewer rows than there are slots.)
+uint32_t padding_groups(Padding &q, int lanes, size_t others) {
+    if (q.order == nullptr) return 0;
     const size_t at_once = kExpertThreads / lanes, each = q.rows / (at_once * kPadGroups) + 1;
     q.each = each < kPadRows ? static_cast<int>(each) : kPadRows;
-    const size_t rows = at_once * q.each;
-    return q.order != nullptr && q.rows > slots ? static_cast<uint32_t>((q.rows + rows - 1) / rows) : 0;
+    const size_t rows = at_once * q.each, groups = (q.rows + rows - 1) / rows;
+    const size_t room = others + kPadGroups < kMaxGroups ? kPadGroups : kMaxGroups - others;
+    return static_cast<uint32_t>(groups < room ? groups : room);
 }
 
 // The variant of a kernel for a call's `tail` and `nt`.
@@ -824,9 +832,10 @@ hr_status combine_grad_impl(const hr_experts_combine_grad_args *q, hr_stream_t s
     a.k = q->k;
     a.hidden = static_cast<int>(q->hidden);
     const int lanes = lanes_for((q->hidden + 7) / 8);
-    a.pad_groups = padding_groups(a.pad, slots, lanes);
-    const size_t grid = a.pad_groups + (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
-    if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
+    const size_t groups = (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
+    if (groups + (a.pad.order != nullptr) > kMaxGroups) return HR_ERR_TOO_LARGE;
+    a.pad_groups = padding_groups(a.pad, lanes, groups);
+    const size_t grid = a.pad_groups + groups;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool nt = slots * width >= kStreamBytes, tail = q->hidden % 8 != 0;
     const hipError_t e = lanes == 16   ? launch_k(HR_VARIANT(combine_grad_rows, 16), grid, s, a)
@@ -978,12 +987,12 @@ extern "C" HR_API hr_status hr_experts_gather(const hr_experts_gather_args *q, h
     a.k = q->k;
     const size_t units = static_cast<size_t>(a.units) + a.scale_units;
     const int lanes = lanes_for(units);
-    a.pad_groups = padding_groups(a.pad, slots, lanes);
     a.splits = lanes == kExpertThreads ? static_cast<uint32_t>((units + kExpertThreads - 1) / kExpertThreads) : 1;
-    const size_t grid =
-        a.pad_groups + (lanes == kExpertThreads ? q->tokens * a.splits
-                                                : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes));
-    if (grid > kMaxGroups) return HR_ERR_TOO_LARGE;
+    const size_t groups = lanes == kExpertThreads ? q->tokens * a.splits
+                                                  : (q->tokens + kExpertThreads / lanes - 1) / (kExpertThreads / lanes);
+    if (groups + (a.pad.order != nullptr) > kMaxGroups) return HR_ERR_TOO_LARGE;
+    a.pad_groups = padding_groups(a.pad, lanes, groups);
+    const size_t grid = a.pad_groups + groups;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool nt = slots * (q->row_bytes + a.scale_bytes) >= kStreamBytes;
     const hipError_t e = lanes == 16   ? launch_k(nt ? gather_rows<16, true> : gather_rows<16, false>, grid, s, a)

@@ -488,3 +488,38 @@ def test_binding_refusals():
     ids[:, 1] = 3
     hr.experts_sort(ids, offsets, order, pos)
     assert offsets.cpu().tolist() == [0, 8, 8, 8, 16] and order.cpu().tolist() == [*range(0, 16, 2), *range(1, 16, 2)]
+
+
+# a rank's share of the experts in buffers of the rows that it uses: fewer than
+# tokens x k, none to spare, a few, and as many as there are slots
+@pytest.mark.parametrize("tokens,k,experts,first,local,pad", [(11, 3, 12, 5, 2, 4), (64, 6, 64, 16, 16, 16),
+                                                              (500, 8, 64, 56, 8, 16), (3000, 4, 128, 0, 16, 64)])
+@pytest.mark.parametrize("width", [64, 300, 1100])
+def test_padding_is_zero_in_a_trimmed_buffer(tokens, k, experts, first, local, pad, width):
+    offsets, order, pos, o, ph, used = buffers(tokens, tokens, k, experts, pad, first=first, local=local)
+    assert used < tokens * k and (o[:used] < 0).any()
+    m = Maker(width)
+    groups = -(-width // 128)
+    x, codes = m.normal(tokens, width, dtype=torch.float16), torch.randint(0, 256, (tokens, width), generator=m.g,
+                                                                           dtype=torch.uint8)
+    s = torch.rand(tokens, groups, generator=m.g)
+    for n in (used, min(used + 3, tokens * k), tokens * k):
+        print(f"trimmed {tokens}x{width} k={k} pad={pad}: {n} rows, {used} used", flush=True)
+        part, of = order[:n], torch.from_numpy(o[:n])
+        for src, scales in ((x, None), (codes, s)):
+            out = m.place(n, width, src.dtype, width + 2, 1)
+            so = m.place(n, groups, torch.float32, groups + 1, 1) if scales is not None else None
+            hr.experts_gather(src.to(DEV), pos, out, offsets=offsets, order=part,
+                              scales=scales.to(DEV) if scales is not None else None, scales_out=so)
+            torch.cuda.synchronize()
+            for a, got in ((src, out), (scales, so)):
+                if a is None:
+                    continue
+                want = torch.full((n, a.shape[1]), 7).to(a.dtype)
+                want[:used] = 0
+                want[of >= 0] = a[of[of >= 0] // k]
+                assert torch.equal(got.cpu(), want), f"{a.dtype}, {n} rows"
+        for in_place in (False, True):
+            run_grad(m, torch.bfloat16, tokens, width, k, pos, ph, offsets, part, o[:n],
+                     weights=torch.rand(tokens, k, generator=m.g), used=used, in_place=in_place)
+    m.check_frames()
