@@ -638,7 +638,7 @@ typedef struct {
  * is rounded once, to `out`.  The 8-bit output comes from the unrounded y:
  *
  *     scale = max(max |y| over the group / 448, 2^-126)
- *     code  = e4m3(y / scale), to nearest even
+ *     code  = e4m3(y / scale), to nearest even (of the quotient in binary32)
  *
  * so a group of zeros has codes 0 and the smallest scale.  A row that holds a
  * NaN or an infinity gives what the formulas give: NaN where h is one, and a

@@ -458,3 +458,70 @@ def test_binding_refusals():
     hr.reduce_rmsnorm([x + 1], y, eps=0.0)
     torch.cuda.synchronize()
     assert (y == 1).all()
+
+
+# ------------------------------------------------------------------ 8 bits
+
+# one row to a wave's lanes and to a workgroup, whole units and odd lengths, and
+# (the last) rows that pass the caches by
+@pytest.mark.parametrize("rows,hidden,group", [(33, 128, 32), (33, 129, 0), (9, 1000, 64), (9, 1001, 128),
+                                               (7, 5120, 128), (7, 5121, 0), (3, 20000, 0), (3, 20001, 32),
+                                               (8200, 4096, 128)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_codes_at_ties(dt, rows, hidden, group):
+    """Values whose ratio to the largest lies half way between two codes: the
+    codes are e4m3 of the binary32 quotient y / scale, to the bit.  (y is the
+    two binary32 products that the formula names, so it can be had from rstd.)"""
+    g = torch.Generator().manual_seed(hidden)
+
+    def rand(low, high):
+        return torch.randint(low, high, (rows, hidden), generator=g)
+
+    # five significant bits: every odd one is a tie of codes' four
+    x = (rand(16, 32) * 2.0 ** rand(-4, 5)).clamp(max=448.0) * (2 * rand(0, 2) - 1)
+    width = group or hidden
+    x[:, ::width] = 448.0
+    x = x.to(TYPES[dt])
+    w = torch.tensor([0.75, 1.0, 1.3])[torch.arange(-(-hidden // width)) % 3].repeat_interleave(width)[:hidden]
+    codes = torch.empty(rows, hidden, dtype=F8, device="cuda:0")
+    n = -(-hidden // width)
+    scales, rstd = torch.empty(rows, n, device="cuda:0"), torch.empty(rows, device="cuda:0")
+    print(f"ties {dt} {rows}x{hidden} group={group}", flush=True)
+    hr.reduce_rmsnorm([x.cuda()], torch.empty_like(x, device="cuda:0"), weight=w.cuda(), eps=EPS, out8=codes,
+                      scales=scales, group=group, rstd=rstd)
+    torch.cuda.synchronize()
+    y = x.float() * rstd.cpu()[:, None] * w
+    top = torch.stack([part.abs().amax(1) for part in y.split(width, 1)], 1)
+    assert torch.equal(scales.cpu(), top / 448)
+    want = (y / scales.cpu().repeat_interleave(width, 1)[:, :hidden]).to(F8)
+    bad = codes.cpu().view(torch.uint8) != want.view(torch.uint8)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} codes are not the quotient's"
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_codes_over_the_range_of_scales(dt):
+    """The same from the smallest scale to an infinite one, zeros of both signs
+    among the values."""
+    exps = [-148, -140, -130, -126, -118, -110, -100, -95, -92, -91, -90, -89, -60, 0, 60, 100, 115, 119, 121, 124, 126,
+            127]
+    g = torch.Generator().manual_seed(5)
+    rows, group = 64, 32
+    hidden = group * len(exps)
+    x = torch.randint(16, 32, (rows, hidden), generator=g) * 2.0 ** torch.randint(-14, 5, (rows, hidden), generator=g)
+    x = x.clamp(max=448.0) * (2 * torch.randint(0, 2, (rows, hidden), generator=g) - 1)
+    x[:, ::group], x[:, 1::group], x[:, 2::group] = 448.0, 0.0, -0.0
+    x = x.to(TYPES[dt])
+    w = torch.tensor([2.0 ** e for e in exps]).repeat_interleave(group)
+    codes, scales = torch.empty(rows, hidden, dtype=F8, device="cuda:0"), torch.empty(rows, len(exps), device="cuda:0")
+    rstd = torch.empty(rows, device="cuda:0")
+    hr.reduce_rmsnorm([x.cuda()], weight=w.cuda(), eps=EPS, out8=codes, scales=scales, group=group, rstd=rstd)
+    torch.cuda.synchronize()
+    y = x.float() * rstd.cpu()[:, None] * w
+    s = (y.abs().view(rows, -1, group).amax(2) / 448).clamp_min(2.0 ** -126)
+    assert torch.isinf(s).any() and (s == 2.0 ** -126).any()
+    assert torch.equal(scales.cpu(), s)
+    want, got = (y.view(rows, -1, group) / s[:, :, None]).view(rows, hidden).to(F8), codes.cpu()
+    nan = torch.isnan(want.float())
+    assert torch.equal(torch.isnan(got.float()), nan) and nan.any()
+    bad = (got.view(torch.uint8) != want.view(torch.uint8)) & ~nan
+    assert not bad.any(), f"{int(bad.sum())} codes, the first of w = 2^{exps[int(bad.nonzero()[0, 1]) // group]}"
