@@ -303,28 +303,30 @@ struct Logits16 {
 
 // exp(x - top) of R logits and their sum: 0 for -infinity and NaN, and for
 // everything where top is -infinity (nothing to pick); where top is +infinity,
-// 1 for each +infinity.  The exponent (x - top) log2(e) is rounded twice to 24
-// bits: at most 2^-23 of itself, so the terms that weigh, with exponents above
-// -16, are off by less than 2^-19.
+// 1 for each +infinity.  The instruction gives 2^p for p = (x - top) log2(e)
+// rounded to 24 bits, which alone is up to |p| 2^-25 of the result; what the
+// rounding left out, times ln 2, is (x - top) - p ln 2, and corrects it.  So a
+// term is off by the instruction's last place and a rounding, whatever its size.
+// (32768 x 256 bfloat16 logits, k=8, forward and back: 8.4 and 7.6 us uncorrected,
+// 8.7 and 8.0 so.)
+// Infinities and NaN come out as NaN, which the clamp to 0..1, a modifier of the
+// last operation, makes 0.
 template <int R>
 __device__ __forceinline__ float exp_all(float (&x)[R], float top) {
-    constexpr float kLog2e = 1.44269504088896341f;
-    // NaN and infinities show in the sum; a wave without them does not look
-    // at every logit for them
+    constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
     const float from = top == -INFINITY ? 0.0f : top;
     float y[R], total = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        y[r] = __builtin_amdgcn_exp2f((x[r] - from) * kLog2e);
+        const float d = x[r] - from, p = d * kLog2e, e = __builtin_amdgcn_exp2f(p);
+        y[r] = __builtin_amdgcn_fmed3f(fmaf(e, fmaf(-p, kLn2, d), e), 0.0f, 1.0f);
         total += y[r];
     }
-    if (__ballot(!(total < INFINITY)) != 0) {
+    if (__ballot(top == INFINITY) != 0) {
         total = 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float one = x[r] == INFINITY ? 1.0f : 0.0f;
-            const float e = x[r] > -INFINITY ? __builtin_amdgcn_exp2f((x[r] - from) * kLog2e) : 0.0f;
-            y[r] = top == INFINITY ? one : e;
+            y[r] = top != INFINITY ? y[r] : x[r] == INFINITY ? 1.0f : 0.0f;
             total += y[r];
         }
     }
@@ -333,13 +335,12 @@ __device__ __forceinline__ float exp_all(float (&x)[R], float top) {
     return total;
 }
 
-// LIST: up to 8 picks of binary32 logits.  32768 tokens of 256, k=8: bfloat16
-// 9.1 us, 7.9 renormalised, where the logits' way from memory takes 3.  Bound by
-// instructions, about 480 a wave of four tokens: keys 85 (made one by one they
-// were 190, and it took 9.4 and 8.7 us), picks 37 each, exponentials 64 and as
-// much again for their quarter rate.  (The exponent as one fused operation, x
-// log2(e) - top log2(e), needs a case of its own for large logits and was
-// slower, 9.6.)
+// LIST: up to 8 picks of binary32 logits.  32768 tokens of 256, k=8, in a graph:
+// bfloat16 8.7 us, 7.4 renormalised, where the logits' way from memory takes 3;
+// binary32 11.1 and 10.4.  Bound by instructions, about 510 a wave of four
+// bfloat16 tokens: keys 85 (made one by one they were 190, and took 0.3 to 0.8 us
+// more), picks 37 each, exponentials 96 and half as much again for their quarter
+// rate.
 template <class T, int L, int R, bool LIST>
 __global__ __launch_bounds__(kRouterThreads) void router_topk(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L;
@@ -441,8 +442,8 @@ __device__ __forceinline__ void order_lds() {
 
 // p * (0 - c) for every logit, put together in LDS, where the picks' own
 // weights * (dweights - c) take their places; a token's lanes are in one wave.
-// 32768 tokens of 256, k=8: bfloat16 9.1 us, binary32 11.2 (67 MB, 6.0 TB/s from
-// the last-level cache).
+// 32768 tokens of 256, k=8, in a graph: bfloat16 8.0 us, binary32 11.6 (67 MB, 5.8
+// TB/s from the last-level cache), renormalised 5.4 and 7.8.
 template <class T, int L, int R>
 __global__ __launch_bounds__(kRouterThreads) void router_topk_grad(RouterArgs a) {
     constexpr int kTokens = kRouterThreads / L, kUnits = R / T::kVec;

@@ -237,3 +237,42 @@ def test_binding_refusals():
             bad()
     hr.router_topk(x, w, ids)
     assert ids.cpu().tolist() == [[0, 1]] * 4 and (w == 1 / 16).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("experts", [32, 64, 200, 700])
+def test_small_weights_are_exact_too(dt, experts):
+    """Weights and gradients of logits up to 60 below the largest, relative to
+    one another, so that the softmax's sum falls out of them.  The differences
+    of these logits are exact in binary32.  An exponential is off by the unit in
+    the last place of the instruction, 2^-23, one more rounding and 60 x 2^-28
+    for ln 2, and every quotient or product by 2^-24: below 2^-21.  Two of them
+    are compared, hence 2^-20."""
+    g = torch.Generator().manual_seed(experts)
+    x = -torch.randint(0, 60 * 64 + 1, (300, experts), generator=g) / 64.0
+    x[torch.arange(300), torch.randint(0, experts, (300,), generator=g)] = 1.0
+    x = x.to(TYPES[dt])
+    d, k = x.cuda(), 32
+    dw = torch.zeros(300, k)
+    dw[:, 0] = 1.0
+    xs = x.double()
+    for renormalize in (False, True):
+        w, ids = torch.empty(300, k, device="cuda:0"), torch.empty(300, k, dtype=torch.int32, device="cuda:0")
+        print(f"small weights {dt} {experts} renormalize={renormalize}", flush=True)
+        hr.router_topk(d, w, ids, renormalize=renormalize)
+        torch.cuda.synchronize()
+        v = xs.gather(1, ids.cpu().long())
+        ref = torch.exp(v - v[:, :1])
+        got = w.double().cpu()
+        within(got / got[:, :1], ref, ref * 2.0 ** -20, "weights")
+    if experts > k and dt == "f32":
+        dx = torch.empty_like(d)
+        hr.router_topk(d, w, ids)
+        hr.router_topk_grad(dw.cuda(), w, ids, dx, logits=d)
+        torch.cuda.synchronize()
+        rest = torch.ones(300, experts, dtype=torch.bool).scatter_(1, ids.cpu().long(), False)
+        got = dx.double().cpu()[rest].view(300, -1)
+        v = xs[rest].view(300, -1)
+        top, at = v.max(1, keepdim=True)
+        ref = torch.exp(v - top)
+        within(got / got.gather(1, at), ref, ref * 2.0 ** -20, "dlogits")
