@@ -135,7 +135,10 @@ class Layer:
         dlogits = dlogits.to(dt)
         g["router"] = torch.mm(self.y.t(), dlogits)
         dys.append(torch.mm(dlogits, w.router.t()))
-        dy = hr.reduce(dys, torch.empty_like(self.y))
+        # a fold takes so many operands; the one left over follows, in the same order
+        dy = hr.reduce(dys[:hr.HR_MAX_G], torch.empty_like(self.y))
+        if len(dys) > hr.HR_MAX_G:
+            dy = hr.reduce([dy, *dys[hr.HR_MAX_G:]], torch.empty_like(self.y))
         g["x"] = torch.empty_like(self.x)
         hr.rmsnorm_grad(dy, self.x, self.rstd_in, g["x"], weight=w.scale_in, dresidual=dh, dweight=g["scale_in"])
         return g

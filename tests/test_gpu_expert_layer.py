@@ -86,3 +86,9 @@ def test_command(capsys):
     el.main(["--tokens", "8", "--hidden", "256", "--experts", "8", "--k", "2", "--bf16"])
     out = capsys.readouterr().out
     assert "forward:" in out and "backward:" in out
+
+
+def test_as_many_ranks_as_a_fold_takes():
+    """Backward then adds a gradient more than one fold takes: every rank's and
+    the router's."""
+    test_layer(torch.float16, 21, 256, 32, 4, hr.HR_MAX_G)
