@@ -760,9 +760,9 @@ HR_API hr_status hr_router_topk_grad(const float *dweights, const float *weights
 #define HR_EXPERTS_SORT_FEW 8192 /* slots that a sort needs no workspace for */
 
 /* Rows that sorted tokens take at most: tokens * k, and pad - 1 more for every
- * segment that can hold a slot.  0 when an argument is out of range. */
+ * segment that can hold a slot.  0 when hr_experts_sort takes no such sort. */
 HR_API size_t hr_experts_rows(size_t tokens, int k, int experts, int pad);
-/* Bytes of workspace that a sort needs (0: none). */
+/* Bytes of workspace that a sort needs (0: none, or no such sort). */
 HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int experts);
 
 /*

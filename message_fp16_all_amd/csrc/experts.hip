@@ -698,6 +698,15 @@ bool picks_ok(size_t tokens, int k, size_t *slots) {
     return k >= 1 && !__builtin_mul_overflow(tokens, static_cast<size_t>(k), slots);
 }
 
+// Rows that a sort of so many slots takes at most: pad - 1 beside them for every
+// segment that can hold one.  False above what hr_experts_sort takes.
+bool sort_rows(size_t slots, int k, int experts, int pad, size_t *rows) {
+    if (k > HR_EXPERTS_MAX_K || experts > HR_EXPERTS_MAX || slots > kMaxCount) return false;
+    const size_t segments = static_cast<size_t>(experts) < slots ? static_cast<size_t>(experts) : slots;
+    *rows = slots + segments * static_cast<size_t>(pad - 1);     // below 2^42
+    return *rows <= kMaxCount;
+}
+
 // Lanes that a row of `units` 16-byte units keeps busy.
 int lanes_for(size_t units) { return units <= 16 ? 16 : units <= 64 ? 64 : kExpertThreads; }
 
@@ -853,18 +862,16 @@ hr_status combine_grad_impl(const hr_experts_combine_grad_args *q, hr_stream_t s
 using namespace hr;
 
 extern "C" HR_API size_t hr_experts_rows(size_t tokens, int k, int experts, int pad) {
-    size_t slots = 0, extra = 0, rows = 0;
+    size_t slots = 0, rows = 0;
     if (!picks_ok(tokens, k, &slots) || experts < 1 || pad < 1) return 0;
-    const size_t segments = static_cast<size_t>(experts) < slots ? static_cast<size_t>(experts) : slots;
-    if (__builtin_mul_overflow(segments, static_cast<size_t>(pad - 1), &extra) ||
-        __builtin_add_overflow(slots, extra, &rows))
-        return 0;
-    return rows;
+    return sort_rows(slots, k, experts, pad, &rows) ? rows : 0;
 }
 
 extern "C" HR_API size_t hr_experts_sort_workspace(size_t tokens, int k, int experts) {
     size_t slots = 0;
-    if (!picks_ok(tokens, k, &slots) || experts < 1 || experts > HR_EXPERTS_MAX || slots > kMaxCount) return 0;
+    if (!picks_ok(tokens, k, &slots) || k > HR_EXPERTS_MAX_K || experts < 1 || experts > HR_EXPERTS_MAX ||
+        slots > kMaxCount)
+        return 0;
     if (slots <= static_cast<size_t>(HR_EXPERTS_SORT_FEW)) return 0;
     const size_t chunk = sort_chunk(slots);
     return (slots + chunk - 1) / chunk * static_cast<size_t>(experts) * 4;
@@ -875,10 +882,9 @@ extern "C" HR_API hr_status hr_experts_sort(const int32_t *ids, size_t tokens, i
                                             void *workspace, size_t workspace_bytes, hr_stream_t stream) {
     size_t slots = 0;
     if (!picks_ok(tokens, k, &slots) || first < 0 || experts < 1 || pad < 1) return HR_ERR_INVALID_ARG;
-    if (experts > HR_EXPERTS_MAX || k > HR_EXPERTS_MAX_K || slots > kMaxCount || rows > kMaxCount)
-        return HR_ERR_TOO_LARGE;
-    const size_t most = hr_experts_rows(tokens, k, experts, pad);
-    if (rows < most || (most == 0 && slots > 0)) return HR_ERR_INVALID_ARG;
+    size_t most = 0;
+    if (!sort_rows(slots, k, experts, pad, &most) || rows > kMaxCount) return HR_ERR_TOO_LARGE;
+    if (rows < most) return HR_ERR_INVALID_ARG;
     if (offsets == nullptr || (rows > 0 && order == nullptr) || (slots > 0 && (ids == nullptr || pos == nullptr)))
         return HR_ERR_INVALID_ARG;
     const size_t need = hr_experts_sort_workspace(tokens, k, experts);

@@ -142,3 +142,24 @@ def grad(**over):
     (dict(dweights=at(2) + 64), hr.HR_ERR_INVALID_ARG), (dict(dz=at(6) + 64), hr.HR_ERR_INVALID_ARG)])
 def test_grad_refusals(over, status):
     assert grad(**over) == status
+
+
+@pytest.mark.parametrize("tokens,k,experts,pad", [
+    (5, hr.HR_EXPERTS_MAX_K + 1, 8, 1), (5, 1, hr.HR_EXPERTS_MAX + 1, 1), (1 << 31, 1, 8, 1), (1 << 26, 32, 8, 1),
+    (2000, 8, 64, 1 << 30), ((1 << 31) - 1, 1, 8, 2)])
+def test_sizes_of_what_a_sort_refuses(tokens, k, experts, pad):
+    """No size for a call that hr_experts_sort refuses whatever the buffers."""
+    assert sort(tokens=tokens, k=k, experts=experts, pad=pad, offsets=at(100), order=at(200), pos=at(300), ws=at(400),
+                ws_bytes=1 << 60, rows=(1 << 31) - 1) == hr.HR_ERR_TOO_LARGE
+    assert hr.hr_experts_rows(tokens, k, experts, pad) == 0
+    if pad == 1:
+        assert hr.hr_experts_sort_workspace(tokens, k, experts) == 0
+
+
+def test_largest_sizes():
+    assert hr.hr_experts_rows(5, hr.HR_EXPERTS_MAX_K, hr.HR_EXPERTS_MAX, 1) == 5 * hr.HR_EXPERTS_MAX_K
+    assert hr.hr_experts_rows((1 << 31) - 1, 1, 8, 1) == (1 << 31) - 1
+    assert hr.hr_experts_rows((1 << 31) - 1 - 8 * 15, 1, 8, 16) == (1 << 31) - 1
+    assert hr.hr_experts_rows((1 << 31) - 8 * 15, 1, 8, 16) == 0
+    assert hr.hr_experts_sort_workspace((1 << 31) - 1, 1, 8) > 0
+    assert hr.hr_experts_sort_workspace(1 << 20, hr.HR_EXPERTS_MAX_K, hr.HR_EXPERTS_MAX) > 0
