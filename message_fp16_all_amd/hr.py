@@ -880,8 +880,10 @@ def _padding_ptrs(order, offsets, rows: int):
 def experts_gather(x, pos, out, *, offsets=None, order=None, scales=None, scales_out=None, stream=None):
     """Every token's row to its sorted rows, and its scales with it
     (hr_experts_gather): ``x`` and ``out`` of any one type, ``scales``
-    torch.float32.  With ``order`` and ``offsets`` the padding rows inside the
-    segments become zeros; rows past the last segment are not written."""
+    torch.float32 (as reduce_rmsnorm writes them).  With ``order`` and
+    ``offsets`` the padding rows inside the segments become zeros; rows past the
+    last segment are not written.  ``out`` and ``order`` may be the first rows
+    of a sort's, down to those in use."""
     if _torch is None:
         _tm()
     dt = x.dtype
@@ -896,7 +898,12 @@ def experts_gather(x, pos, out, *, offsets=None, order=None, scales=None, scales
         if scales is None or scales_out is None:
             raise ValueError("scales and scales_out go together")
         f32 = _torch.float32
+        # one scale per row may come in one dimension
+        if scales.dim() == 1 and scales.shape[0] == tokens:
+            scales = scales.unsqueeze(1)
         sw = scales.shape[-1]
+        if scales_out.dim() == 1 and sw == 1:
+            scales_out = scales_out.unsqueeze(1)
         sp, _, _, ss = _row_view(scales, "scales", f32, tokens, sw)
         tp, _, _, ts = _row_view(scales_out, "scales_out", f32, rows, sw)
     size = x.element_size()

@@ -523,3 +523,30 @@ def test_padding_is_zero_in_a_trimmed_buffer(tokens, k, experts, first, local, p
             run_grad(m, torch.bfloat16, tokens, width, k, pos, ph, offsets, part, o[:n],
                      weights=torch.rand(tokens, k, generator=m.g), used=used, in_place=in_place)
     m.check_frames()
+
+
+def test_gather_takes_the_scales_of_rows():
+    """A scale per row in one dimension, as reduce_rmsnorm writes it."""
+    tokens, k, hidden = 20, 3, 512
+    offsets, order, pos, o, _, used = buffers(7, tokens, k, 6, 4)
+    h = Maker(7).normal(tokens, hidden, dtype=torch.float16).to(DEV)
+    f8 = torch.float8_e4m3fn
+    codes, scales = torch.empty(tokens, hidden, dtype=f8, device=DEV), torch.empty(tokens, device=DEV)
+    hr.reduce_rmsnorm([h], out8=codes, scales=scales)
+    out, scales_out = torch.empty(len(o), hidden, dtype=f8, device=DEV), torch.full((len(o),), 7.0, device=DEV)
+    hr.experts_gather(codes, pos, out, offsets=offsets, order=order, scales=scales, scales_out=scales_out)
+    torch.cuda.synchronize()
+    want = torch.full((len(o),), 7.0)
+    want[:used] = 0
+    want[torch.from_numpy(o >= 0)] = scales.cpu()[torch.from_numpy(o[o >= 0] // k)]
+    assert torch.equal(scales_out.cpu(), want)
+    here = torch.from_numpy(o >= 0).to(DEV)
+    assert torch.equal(out.view(torch.uint8)[here], codes.view(torch.uint8)[torch.from_numpy(o[o >= 0] // k).to(DEV)])
+    with pytest.raises(ValueError):
+        hr.experts_gather(codes, pos, out, offsets=offsets, order=order, scales=scales[:-1], scales_out=scales_out)
+    with pytest.raises(ValueError):
+        hr.experts_gather(codes, pos, out, offsets=offsets, order=order, scales=scales, scales_out=scales_out[1:])
+    # and one dimension for the scales of a single row stays what it was
+    row, one = torch.rand(4, device=DEV), torch.zeros(4, device=DEV)
+    hr.experts_gather(codes[:1], torch.zeros(1, 1, dtype=torch.int32, device=DEV), out[:1], scales=row, scales_out=one)
+    assert torch.equal(row, one) and torch.equal(out[0].view(torch.uint8), codes[0].view(torch.uint8))
