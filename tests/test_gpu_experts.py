@@ -550,3 +550,50 @@ def test_gather_takes_the_scales_of_rows():
     row, one = torch.rand(4, device=DEV), torch.zeros(4, device=DEV)
     hr.experts_gather(codes[:1], torch.zeros(1, 1, dtype=torch.int32, device=DEV), out[:1], scales=row, scales_out=one)
     assert torch.equal(row, one) and torch.equal(out[0].view(torch.uint8), codes[0].view(torch.uint8))
+
+
+# rows of 64 MiB or more pass the caches by: both sides of every number of lanes,
+# two units of a lane (2304), whole units and odd lengths
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", [100, 128, 129, 500, 512, 1000, 2047, 2303, 2304, 4097])
+def test_streamed_rows(dt, hidden):
+    """Large calls give the bits of calls on parts of the tokens, and leave what
+    lies around their rows alone."""
+    dtype, g, k, experts, pad = TYPES[dt], torch.Generator(device=DEV).manual_seed(hidden), 3, 40, 16
+    tokens = (1 << 26) // (hidden * 2 * k) + 5
+    ids = np.random.default_rng(hidden).integers(-1, experts, (tokens, k))
+    offsets, order, pos = sort(ids, 0, experts, pad)
+    rows = order.numel()
+    print(f"streamed experts {dt} {tokens}x{hidden}, {rows} rows", flush=True)
+
+    def buffer(n, value=None):
+        b = torch.empty(1 + n * (hidden + 3) + 8, dtype=dtype, device=DEV)
+        b = b.normal_(generator=g) if value is None else b.fill_(value)
+        return b, lambda b, a=0, e=n: b.as_strided((e - a, hidden), (hidden + 3, 1), 1 + a * (hidden + 3))
+
+    (x, of_tokens), (add, _) = buffer(tokens), buffer(tokens)
+    z, of_rows = buffer(rows)
+    w = torch.rand(tokens, k, generator=g, device=DEV)
+    whole, cuts = [(0, tokens)], [tokens * i // 4 for i in range(5)]
+    got = []
+    for parts in (whole, list(zip(cuts, cuts[1:]))):
+        s, dz, over = buffer(rows, 7)[0], buffer(rows, 7)[0], z.clone()
+        y, plus, dx = buffer(tokens, 7)[0], add.clone(), buffer(tokens, 7)[0]
+        dw, dw2 = (torch.full((tokens, k), 7.0, device=DEV) for _ in range(2))
+        for a, b in parts:
+            p = pos[a:b]
+            hr.experts_gather(of_tokens(x, a, b), p, of_rows(s), offsets=offsets, order=order)
+            hr.experts_combine(of_rows(z), p, of_tokens(y, a, b), weights=w[a:b])
+            hr.experts_combine(of_rows(z), p, of_tokens(plus, a, b), weights=w[a:b], addend=of_tokens(plus, a, b))
+            hr.experts_combine(of_rows(z), p, of_tokens(dx, a, b))
+            hr.experts_combine_grad(of_tokens(x, a, b), of_rows(z), p, w[a:b], of_rows(dz), dw[a:b], offsets=offsets,
+                                    order=order)
+            hr.experts_combine_grad(of_tokens(x, a, b), of_rows(over), p, w[a:b], of_rows(over), dw2[a:b])
+        torch.cuda.synchronize()
+        assert torch.equal(dw, dw2)
+        got.append((s, y, plus, dx, dz, dw, over))
+    for name, a, b in zip(("gather", "combine", "addend in place", "no weights", "dz", "dweights", "dz in place"), *got):
+        bad = a.view(torch.uint8) != b.view(torch.uint8)
+        assert not bad.any(), f"{name}: {int(bad.sum())} bytes differ"
+    used = int(offsets[-1])
+    assert (of_rows(got[0][0])[:used][order[:used] < 0] == 0).all() and (of_rows(got[0][0])[used:] == 7).all()

@@ -525,3 +525,92 @@ def test_codes_over_the_range_of_scales(dt):
     assert torch.equal(torch.isnan(got.float()), nan) and nan.any()
     bad = (got.view(torch.uint8) != want.view(torch.uint8)) & ~nan
     assert not bad.any(), f"{int(bad.sum())} codes, the first of w = 2^{exps[int(bad.nonzero()[0, 1]) // group]}"
+
+
+# --------------------------------------------------- calls that pass the caches by
+
+STREAMED = 1 << 27               # bytes moved from which they do
+STREAMED_WIDTHS = [121, 128, 250, 256, 505, 512, 4001, 4096, 8190, 8192, 20000, 20001]
+
+
+def rows_buffer(g, rows, hidden, dtype, pad, offset, sigma=1.0):
+    """Random values all over a buffer, and the rows in it: `pad` values between
+    two of them, the first at `offset`."""
+    buf = torch.empty(offset + rows * (hidden + pad) + 8, dtype=dtype, device="cuda:0").normal_(0, sigma, generator=g)
+    return buf, lambda b, a=0, n=rows: b.as_strided((n, hidden), (hidden + pad, 1), offset + a * (hidden + pad))
+
+
+def parts_of(rows):
+    """Four parts, each a call below the limit."""
+    cuts = [rows * i // 4 for i in range(5)]
+    return [(a, b - a) for a, b in zip(cuts, cuts[1:])]
+
+
+def equal(a, b, what):
+    same_bits = a.view(torch.uint8) == b.view(torch.uint8)
+    assert same_bits.all(), f"{what}: {int((~same_bits).sum())} bytes differ"
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", STREAMED_WIDTHS)
+def test_streamed_norm(dt, hidden):
+    """One large call gives the bits of its parts, and leaves what lies around
+    its rows alone: packed and strided, apart and in place."""
+    dtype, g = TYPES[dt], torch.Generator(device="cuda:0").manual_seed(hidden)
+    rows = STREAMED // (hidden * 2 * 5) + 3          # 5 arrays of rows
+    w = torch.empty(hidden, device="cuda:0").normal_(1, 0.2, generator=g)
+    for pad, offset, group in ((0, 0, 128), (5, 1, 0), (8, 8, 64)):
+        print(f"streamed norm {dt} {rows}x{hidden} pad={pad} group={group}", flush=True)
+        (x, view), (r, _) = (rows_buffer(g, rows, hidden, dtype, pad, offset) for _ in range(2))
+        n = -(-hidden // group) if group else 1
+        got = []
+        for parts in ([(0, rows)], parts_of(rows)):
+            h, y = (torch.full_like(x, 7) for _ in range(2))
+            codes = torch.full(x.shape, 7, dtype=torch.uint8, device="cuda:0").view(F8)
+            scales, rstd = torch.full((rows, n), 7.0, device="cuda:0"), torch.full((rows,), 7.0, device="cuda:0")
+            x2, r2 = x.clone(), r.clone()
+            for a, m in parts:
+                hr.reduce_rmsnorm([view(x, a, m)], view(y, a, m), residual=view(r, a, m), residual_out=view(h, a, m),
+                                  weight=w, eps=EPS, out8=view(codes, a, m), scales=scales[a:a + m], group=group,
+                                  rstd=rstd[a:a + m])
+                hr.reduce_rmsnorm([view(x2, a, m)], view(x2, a, m), residual=view(r2, a, m), residual_out=view(r2, a, m),
+                                  weight=w, eps=EPS, out8=view(codes, a, m), scales=scales[a:a + m], group=group)
+            torch.cuda.synchronize()
+            equal(view(y).contiguous(), view(x2).contiguous(), "out in place")
+            equal(view(h).contiguous(), view(r2).contiguous(), "h in place")
+            got.append((h, y, codes, scales, rstd, x2, r2))
+        for name, a, b in zip(("h", "y", "codes", "scales", "rstd", "out in place", "h in place"), *got):
+            equal(a, b, name)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hidden", STREAMED_WIDTHS)
+def test_streamed_grad(dt, hidden):
+    """dx of one large call has the bits of its parts, in place too; dweight
+    against the formula in 64 bits."""
+    dtype, g = TYPES[dt], torch.Generator(device="cuda:0").manual_seed(hidden)
+    rows = STREAMED // (hidden * 2 * 4) + 3          # dy, h, dresidual and dx
+    w = torch.empty(hidden, device="cuda:0").normal_(1, 0.2, generator=g)
+    for pad, offset in ((0, 0), (5, 1)):
+        print(f"streamed norm grad {dt} {rows}x{hidden} pad={pad}", flush=True)
+        made = [rows_buffer(g, rows, hidden, dtype, pad, offset) for _ in range(3)]
+        view = made[0][1]
+        dy, h, r = (b for b, _ in made)
+        rstd = 1.0 / torch.sqrt(view(h).float().square().mean(1) + EPS)
+        first = torch.full_like(dy, 7)
+        for a, m in parts_of(rows):
+            hr.rmsnorm_grad(view(dy, a, m), view(h, a, m), rstd[a:a + m], view(first, a, m), weight=w,
+                            dresidual=view(r, a, m))
+        prod = view(dy).double() * (view(h).double() * rstd.double()[:, None])
+        ref, size = prod.sum(0).cpu(), prod.abs().sum(0).cpu()
+        del prod
+        for into in (None, 0, 1, 2):
+            d = [b.clone() for b in (dy, h, r)]
+            out = torch.full_like(dy, 7) if into is None else d[into]
+            dw = torch.full((hidden,), 7.0, device="cuda:0")
+            hr.rmsnorm_grad(view(d[0]), view(d[1]), rstd, view(out), weight=w, dresidual=view(d[2]), dweight=dw)
+            torch.cuda.synchronize()
+            want = first if into is None else (dy, h, r)[into].clone()
+            view(want).copy_(view(first))
+            equal(out, want, f"dx into {into}")
+            within(dw, ref, size * (rows + 32) * 2.0 ** -24, "dweight")
