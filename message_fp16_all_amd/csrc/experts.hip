@@ -243,10 +243,10 @@ __global__ __launch_bounds__(kMaxSortThreads) void sort_count(SortArgs a) {
     for (int i = threadIdx.x; i < a.experts; i += blockDim.x) a.counts[blockIdx.x * a.experts + i] = lds[i];
 }
 
-// Every workgroup adds the counts of all of them up by itself: both kernels take
-// 9.2 us for 65528 slots of 128 experts, 17.5 for 2^20 of 256.  (With a kernel of
-// one workgroup between the two, 12.9 against 10.4 and 27.7 against 18.5 when
-// these were measured.)
+// Every workgroup adds the counts of all of them up by itself: in a graph both
+// kernels take 9.4 us for 65528 slots of 128 experts, 18.3 for 2^20 of 256.  (With
+// a kernel of one workgroup between the two, 12.9 against 10.4 and 27.7 against
+// 18.5 when these were measured.)
 // Dynamic LDS: [waves][experts] counts, then [experts + 1] offsets, [experts]
 // totals, [experts] firsts, [threads] sums and [waves].
 template <int N>
@@ -577,7 +577,7 @@ struct CombineGradArgs {
 
 // L lanes per token over all of its row, since the weights' gradients are sums
 // over it; kPicks of them at a time in registers.  Bound by HBM: 4096 tokens x
-// 8192 of 4 picks 112 us, 630 MB with the padding, 5.6 TB/s; 8192 x 4096 with one
+// 8192 of 4 picks 118 us, 630 MB with the padding, 5.3 TB/s; 8192 x 4096 with one
 // pick in eight here 32 us (44 with the places read through the scalar cache).
 template <class E, int L, bool TAIL, bool NT>
 __global__ __launch_bounds__(kExpertThreads) void combine_grad_rows(CombineGradArgs a) {

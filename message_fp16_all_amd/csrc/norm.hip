@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
 
 // One row per workgroup (L = 0), or one row per L lanes of a workgroup.  Bound
 // by HBM: 2048 x 8192 of eight contributions and a residual 60 us, 6.1 TB/s;
-// 4999 x 5120 with both outputs 41 us, 5.6 TB/s.
+// 4999 x 5120 with both outputs 41.6 us, 5.5 TB/s.
 // Thread t of a row holds units t, t + threads, .. (U of them) from the fold's
 // loads to the stores, so every input byte is read once.  B operands are loaded
 // at once: few, because registers held for loads keep waves off the compute
@@ -318,7 +318,8 @@ __device__ __forceinline__ void sum_few_rows(const NormGradArgs &a) {
 // workgroups (L = 0) or to groups of L lanes in turn; a thread keeps its
 // columns' sums in registers from its first row to its last.  Bound by HBM:
 // 2048 x 8192 with dres and dweight 31 us, of which 4 are sum_columns.  (Loading
-// a row ahead was no faster: 33.9 against 33.0 us at the time.)
+// a row ahead was no faster: 33.9 against 33.0 us at the time.)  Rows of more than
+// 16384 values (U = 4) are read twice: 8192 x 20000 382 us, 8192 x 16384 181.
 // FEW: further workgroups sum the columns (in kernels of their own, since that
 // takes registers).
 template <class E, int U, int L, bool TAIL, bool NT, bool FEW>
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_grad_rows(NormGradArgs a
             if (!there || i >= units) continue;
             float dy[8], unit[8], w[8], f[8];
             if constexpr (!kKeep) {
-                load(u);   // again, from the caches
+                load(u);   // again (below the streaming limit from the caches)
             }
             Wide<E>::widen(d[u], dy);
             Wide<E>::widen(h[u], unit);
@@ -517,8 +518,9 @@ RowShape row_shape(int hidden, bool spread = false) {
 
 // Few workgroups with many operands wait for their loads: nine operands at
 // once, and of long rows one unit per thread, twice the threads.  (In a graph,
-// 64 x 6144 of eight contributions 5.6 us with two units per thread, 5.0 with
-// one and four operands at once, 4.2 with nine; 2048 x 8192 of eight 61.6 with
+// with binary16 output alone, 64 x 6144 of eight contributions 5.6 us with two
+// units per thread, 5.0 with one and four operands at once, 4.1 with nine, and 5.4
+// from bfloat16 to e4m3 with scales of 128; 2048 x 8192 of eight 61.6 with
 // two units and 67.8 with one; 8192 x 64 of sixteen 8.4 us with four operands at
 // once, 6.5 with nine, 32768 x 64 15.1 either way.)
 constexpr size_t kSpreadGroups = 512;
