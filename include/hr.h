@@ -875,6 +875,154 @@ typedef struct {
 HR_API hr_status hr_experts_combine_grad_f16(const hr_experts_combine_grad_args *args, hr_stream_t stream);
 HR_API hr_status hr_experts_combine_grad_bf16(const hr_experts_combine_grad_args *args, hr_stream_t stream);
 
+/*
+ * The experts' own work, over rows sorted by expert: expert e's rows are
+ * offsets[e] .. offsets[e + 1] - 1, as hr_experts_sort leaves them (with
+ * offsets NULL, experts 1 and all rows).  Offsets are read on the device, and
+ * whatever they hold nothing outside the buffers is touched.  Rows of no segment
+ * are not written.
+ */
+#define HR_EXPERTS_PRODUCT_MAX (1u << 20) /* largest n and k */
+
+typedef struct {
+    const void *x;            /* rows rows of k values                            */
+    const void *w;            /* experts matrices of n rows of k values;
+                                 transposed: of k rows of n                       */
+    void *out;                /* rows rows of n 16-bit values                     */
+    const int32_t *offsets;   /* experts + 1 row numbers, upward; NULL: one expert
+                                 and all rows                                     */
+    const float *x_scales;    /* e4m3: rows rows of ceil(k / 128) scales          */
+    const float *w_scales;    /* e4m3: experts matrices, a scale per 128 x 128
+                                 values of w's, lying as they do                  */
+    size_t rows, n, k;
+    size_t x_stride, out_stride;                  /* values; 0 = k, n             */
+    size_t w_stride;                              /* values; 0 = k (transposed n) */
+    size_t w_expert_stride;                       /* values; 0 = adjacent         */
+    size_t x_scales_stride;                       /* scales; 0 = their number     */
+    size_t w_scales_stride, w_scales_expert_stride;   /* scales; 0 = adjacent     */
+    int experts, transposed;
+} hr_experts_product_args;
+
+/*
+ * hr_experts_product_f16 / _bf16 -- every row times its expert's matrix:
+ *
+ *     out[r][j] = sum over i of x[r][i] * w[e][j][i]      (transposed: w[e][i][j])
+ *
+ * in one kernel, summed in binary32 and rounded once.  A linear layer keeps its
+ * matrix as n x k; the gradient of its rows is the same call with the other
+ * value of `transposed` and n and k exchanged: dx = product of dy.  x_scales and
+ * w_scales are NULL.
+ *
+ * hr_experts_product_e4m3_f16 / _bf16 -- the same of e4m3 values (OCP) with
+ * scales, the output in 16 bits:
+ *
+ *     out[r][j] = sum over the groups g of 128 of i:
+ *                 x_scales[r][g] * w_scales[e][j / 128][g] * sum over g of x[r][i] * w[e][j][i]
+ *
+ * x and x_scales are what hr_reduce_rmsnorm, hr_experts_gather and
+ * hr_experts_act write with groups of 128.  A group's products are added by the
+ * matrix instruction, eight at a time after cutting them at 2^-13 of the largest
+ * one's leading bit; everything beyond that in binary32.  Without offsets it is
+ * a dense layer's product.
+ *
+ * The order of every sum depends on the sizes alone: equal inputs give equal
+ * outputs.  A row's NaN and infinities stay in its row.
+ * Errors: HR_ERR_INVALID_ARG (n, k or experts 0, offsets NULL with several
+ * experts, null pointers, scales missing or not wanted, a stride below the row,
+ * overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (n or k above
+ * HR_EXPERTS_PRODUCT_MAX, experts above HR_EXPERTS_MAX, 2^31 rows or more, rows
+ * more than 4 MiB apart, a launch of 2^32 work-items or more, at the least one
+ * per 4 values of out), HR_ERR_HIP.
+ */
+HR_API hr_status hr_experts_product_f16(const hr_experts_product_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_product_bf16(const hr_experts_product_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_product_e4m3_f16(const hr_experts_product_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_product_e4m3_bf16(const hr_experts_product_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *dy;           /* rows rows of n values                            */
+    const void *x;            /* rows rows of k values                            */
+    void *dw;                 /* experts matrices of n rows of k values           */
+    const int32_t *offsets;   /* as the product's                                 */
+    size_t rows, n, k;
+    size_t dy_stride, x_stride;                   /* values; 0 = n, k             */
+    size_t dw_stride, dw_expert_stride;           /* values; 0 = adjacent         */
+    int experts;
+    int dw_f32;               /* 0: dw has the rows' type; else binary32          */
+} hr_experts_product_grad_args;
+
+/*
+ * hr_experts_product_grad_f16 / _bf16 -- the gradient of the matrices:
+ *
+ *     dw[e][j][i] = sum over e's rows r of dy[r][j] * x[r][i]
+ *
+ * summed in binary32 in the rows' order, rounded once; zeros for an expert
+ * without rows.  Rows of no segment are not used.  (Matrices kept transposed:
+ * dy and x exchanged, and n and k.)
+ * Errors: as hr_experts_product.
+ */
+HR_API hr_status hr_experts_product_grad_f16(const hr_experts_product_grad_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_product_grad_bf16(const hr_experts_product_grad_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *x;            /* rows rows: gated 2 width values (gate, then up),
+                                 else width                                       */
+    void *out;                /* width 16-bit values; NULL = not wanted           */
+    void *codes;              /* y in e4m3 (OCP, largest 448); NULL = not wanted  */
+    float *scales;            /* one per group; with codes                        */
+    const int32_t *offsets;   /* the sort's: rows from offsets[experts] on are left
+                                 alone; NULL = all rows                           */
+    size_t rows, width;
+    size_t x_stride, out_stride;                  /* values; 0 = the row          */
+    size_t codes_stride;                          /* bytes; 0 = width             */
+    size_t scales_stride;                         /* scales; 0 = their number     */
+    int gated;                /* 0: y = x                                         */
+    int group;                /* values that share a scale: 32, 64 or 128 (the
+                                 last group may be shorter); read with codes      */
+    int experts;              /* with offsets                                     */
+} hr_experts_act_args;
+
+/*
+ * hr_experts_act_f16 / _bf16 -- what stands between the experts' products:
+ *
+ *     y = silu(gate) * up,  silu(g) = g / (1 + e^-g)      (not gated: y = x)
+ *
+ * in binary32, rounded once to `out`, and from the unrounded y, as
+ * hr_reduce_rmsnorm does, to e4m3 codes with a scale per group.  Not gated, it is
+ * the quantisation of any 16-bit rows for an 8-bit product.  A gate of -infinity
+ * gives NaN, as the formula does.
+ * Errors: HR_ERR_INVALID_ARG (width 0, group, codes without scales or scales
+ * without codes, nothing to write, offsets with experts below 1, null pointers, a
+ * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (2^31 rows
+ * or more, width above HR_EXPERTS_PRODUCT_MAX), HR_ERR_HIP.
+ */
+HR_API hr_status hr_experts_act_f16(const hr_experts_act_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_act_bf16(const hr_experts_act_args *args, hr_stream_t stream);
+
+typedef struct {
+    const void *dy;           /* rows rows of width values                        */
+    const void *x;            /* the forward call's: gate, then up                */
+    void *dx;                 /* 2 width values, as x                             */
+    void *out;                /* the forward call's out once more; NULL = not wanted */
+    const int32_t *offsets;   /* as the forward call's                            */
+    size_t rows, width;
+    size_t dy_stride, x_stride, dx_stride, out_stride;   /* values; 0 = the row   */
+    int experts;
+} hr_experts_act_grad_args;
+
+/*
+ * hr_experts_act_grad_f16 / _bf16 -- the gradient of hr_experts_act, gated, with
+ * s = 1 / (1 + e^-gate):
+ *
+ *     dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s
+ *
+ * and, where wanted, `out` computed again (a training step need not keep it for
+ * the next matrices' gradient).  dx may be exactly x.
+ * Errors: as hr_experts_act.
+ */
+HR_API hr_status hr_experts_act_grad_f16(const hr_experts_act_grad_args *args, hr_stream_t stream);
+HR_API hr_status hr_experts_act_grad_bf16(const hr_experts_act_grad_args *args, hr_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 HR_API const char *hr_status_str(hr_status s);
 

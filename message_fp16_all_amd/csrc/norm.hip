@@ -19,8 +19,6 @@ namespace hr {
 constexpr int kNormMaxThreads = 1024;
 constexpr int kNormMaxWaves = kNormMaxThreads / kWave;
 constexpr int kOperands = HR_MAX_G + 1;
-constexpr float kE4m3Max = 448.0f;
-constexpr float kMinScale = 0x1p-126f;
 
 struct NormArgs {
     const uint16_t *in[kOperands];   // contributions, then the residual if there is one
@@ -94,12 +92,6 @@ __device__ __forceinline__ uint32_t max_row(uint32_t v, uint32_t *part) {
         const int lane = threadIdx.x % kNormMaxWaves;
         return max_lanes<kNormMaxWaves>(lane < waves ? part[lane] : 0u);
     }
-}
-
-__device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
-    if (lanes == 16) return max_lanes<16>(v);
-    if (lanes == 8) return max_lanes<8>(v);
-    return max_lanes<4>(v);
 }
 
 // One row per workgroup (L = 0), or one row per L lanes of a workgroup.  Bound
@@ -209,39 +201,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows(NormArgs a) {
         const int i = t + u * threads;
         if (!there || i >= units) continue;
         const float m = __builtin_bit_cast(float, top[u]);
-        const float scale = m < kE4m3Max * kMinScale ? kMinScale : m / kE4m3Max;   // NaN stays NaN
+        const float scale = e4m3_scale(m);
         if (a.group_lanes == 0 ? i == 0 : i % a.group_lanes == 0)
             a.scales[row * a.scales_stride + (a.group_lanes == 0 ? 0 : i / a.group_lanes)] = scale;
-        // y / scale, rounded once, with one reciprocal for the group.  The product
-        // with it is up to 1.5 units in the last place off, which moves quotients
-        // half way between two codes.  A step by the remainder brings it within
-        // one unit, and from there the next gives the division's own result
-        // (Markstein 1990: a quotient within a unit, the reciprocal to nearest, an
-        // exact remainder; the negated one keeps the sign of a zero).  Remainders
-        // are exact for scales from 2^-90 on where a quotient is 2^-11 or more,
-        // and smaller ones have the code 0; smaller scales are lifted.  What is
-        // finite over an infinite scale is 0.  (16384 x 4096 of one contribution and
-        // a residual 78.8 us, 84.0 with divisions, 77.6 with the bare product.)
-        float divisor = scale;
-        if (scale < 0x1p-90f) {
-            divisor *= 0x1p60f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[u][e] *= 0x1p60f;
-        }
-        const float inv = 1.0f / divisor;
-        divisor = divisor == INFINITY ? 0.0f : divisor;
-        const auto over = [&](float v) {
-            float r = v * inv;
-            r = fmaf(-fmaf(r, divisor, -v), inv, r);
-            return fmaf(-fmaf(r, divisor, -v), inv, r);
-        };
-        u32x2 c;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            int v = __builtin_amdgcn_cvt_pk_fp8_f32(over(y[u][4 * q]), over(y[u][4 * q + 1]), 0, false);
-            v = __builtin_amdgcn_cvt_pk_fp8_f32(over(y[u][4 * q + 2]), over(y[u][4 * q + 3]), v, true);
-            c[q] = static_cast<uint32_t>(v);
-        }
+        const E4m3Codes at_scale(scale, y[u]);
+        const u32x2 c = at_scale.codes(y[u]);
         // a last unit's shared values may have another group's scale: its own only
         const Unit<TAIL> at(i, hidden);
         uint8_t *p = a.codes + row * a.codes_stride + at.start;

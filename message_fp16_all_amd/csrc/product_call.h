@@ -1,0 +1,191 @@
+// product_call.h -- checks of the experts' products' arguments and the choice
+// of a kernel; not exported.
+#pragma once
+
+#include "product.h"
+
+namespace hr {
+
+// Rows of at most 4 MiB apart: a tile's 256 stay inside a buffer's 2 GiB.
+constexpr size_t kMaxProductStride = size_t(1) << 22;
+
+inline bool units16(const void *p) { return aligned(p, 16); }
+
+// Matrices of `rows` rows of `width` values, as a caller passes them.
+struct Matrices {
+    size_t stride, expert_stride;       // values
+    Region region;
+};
+inline bool matrices(const void *p, int experts, size_t rows, size_t width, size_t stride, size_t expert_stride,
+                     size_t bytes, Matrices *m) {
+    m->stride = stride;
+    if (!row_stride(rows, width, &m->stride, bytes)) return false;
+    m->expert_stride = expert_stride;
+    const size_t span = rows * m->stride;               // below 2^63: checked
+    if (m->expert_stride == 0) m->expert_stride = span;
+    if (experts > 1 && m->expert_stride < (rows - 1) * m->stride + width) return false;
+    size_t all = 0;
+    if (__builtin_mul_overflow(static_cast<size_t>(experts), m->expert_stride, &all) ||
+        __builtin_mul_overflow(all, bytes, &all) || all > SIZE_MAX / 2)
+        return false;
+    if (experts == 1 || m->expert_stride == span)
+        m->region = {p, static_cast<size_t>(experts) * rows, width * bytes, m->stride * bytes};
+    else
+        m->region = {p, static_cast<size_t>(experts), ((rows - 1) * m->stride + width) * bytes,
+                     m->expert_stride * bytes};
+    return true;
+}
+
+template <int SIZE>
+hr_status product_check(const hr_experts_product_args *q, ProductArgs &a, bool &any) {
+    if (q == nullptr || q->n == 0 || q->k == 0 || q->experts < 1 || (q->offsets == nullptr && q->experts != 1))
+        return HR_ERR_INVALID_ARG;
+    if (q->n > HR_EXPERTS_PRODUCT_MAX || q->k > HR_EXPERTS_PRODUCT_MAX || q->experts > HR_EXPERTS_MAX ||
+        q->rows > 0x7FFFFFFFu)
+        return HR_ERR_TOO_LARGE;
+    const bool across = q->transposed != 0;
+    const size_t wr = across ? q->k : q->n, wc = across ? q->n : q->k;
+    size_t xs = q->x_stride, os = q->out_stride, ss = q->x_scales_stride;
+    Matrices w, ws{};
+    const size_t kb = (q->k + 127) / 128, rb = (wr + 127) / 128, cb = (wc + 127) / 128;
+    if (!row_stride(q->rows, q->k, &xs, SIZE) || !row_stride(q->rows, q->n, &os, 2) ||
+        !matrices(q->w, q->experts, wr, wc, q->w_stride, q->w_expert_stride, SIZE, &w))
+        return HR_ERR_INVALID_ARG;
+    if (SIZE == 1 && (!row_stride(q->rows, kb, &ss, 4) ||
+                      !matrices(q->w_scales, q->experts, rb, cb, q->w_scales_stride, q->w_scales_expert_stride, 4, &ws)))
+        return HR_ERR_INVALID_ARG;
+    if (xs * SIZE > kMaxProductStride || w.stride * SIZE > kMaxProductStride || os * 2 > kMaxProductStride ||
+        ss * 4 > kMaxProductStride)
+        return HR_ERR_TOO_LARGE;
+    if (q->rows == 0) return HR_OK;
+    if (q->x == nullptr || q->w == nullptr || q->out == nullptr) return HR_ERR_INVALID_ARG;
+    if (SIZE == 1 && (q->x_scales == nullptr || q->w_scales == nullptr)) return HR_ERR_INVALID_ARG;
+    if (!aligned(q->x, SIZE) || !aligned(q->w, SIZE) || !aligned(q->out, 2) || !aligned(q->offsets, 4) ||
+        !aligned(q->x_scales, 4) || !aligned(q->w_scales, 4))
+        return HR_ERR_ALIGNMENT;
+    const Region out = {q->out, q->rows, q->n * 2, os * 2};
+    if (regions_overlap(out, {q->x, q->rows, q->k * SIZE, xs * SIZE}) || regions_overlap(out, w.region) ||
+        regions_overlap(out, {q->offsets, 1, (static_cast<size_t>(q->experts) + 1) * 4, 0}))
+        return HR_ERR_INVALID_ARG;
+    if (SIZE == 1 && (regions_overlap(out, {q->x_scales, q->rows, kb * 4, ss * 4}) || regions_overlap(out, ws.region)))
+        return HR_ERR_INVALID_ARG;
+    a.q = static_cast<const char *>(q->x);
+    a.p = static_cast<const char *>(q->w);
+    a.out = static_cast<char *>(q->out);
+    a.offsets = q->offsets;
+    a.q_scales = q->x_scales;
+    a.p_scales = q->w_scales;
+    a.q_stride = xs * SIZE;
+    a.p_stride = w.stride * SIZE;
+    a.out_stride = os * 2;
+    a.p_expert_stride = w.expert_stride * SIZE;
+    a.q_scales_stride = ss;
+    a.scales_expert = ws.expert_stride;
+    a.scales_p = across ? 1 : ws.stride;
+    a.scales_c = across ? ws.stride : 1;
+    a.rows = static_cast<uint32_t>(q->rows);
+    a.experts = q->experts;
+    a.np = static_cast<int>(q->n);
+    a.nc = static_cast<int>(q->k);
+    // DMA brings whole 16-byte units from 16-byte addresses
+    any = !(units16(q->x) && units16(q->w) && a.q_stride % 16 == 0 && a.p_stride % 16 == 0 &&
+            a.p_expert_stride % 16 == 0 && q->k * SIZE % 16 == 0 && (!across || q->n * SIZE % 16 == 0));
+    return HR_OK;
+}
+
+inline hr_status product_grad_check(const hr_experts_product_grad_args *q, ProductArgs &a, bool &any) {
+    if (q == nullptr || q->n == 0 || q->k == 0 || q->experts < 1 || (q->offsets == nullptr && q->experts != 1))
+        return HR_ERR_INVALID_ARG;
+    if (q->n > HR_EXPERTS_PRODUCT_MAX || q->k > HR_EXPERTS_PRODUCT_MAX || q->experts > HR_EXPERTS_MAX ||
+        q->rows > 0x7FFFFFFFu)
+        return HR_ERR_TOO_LARGE;
+    size_t ys = q->dy_stride, xs = q->x_stride;
+    const size_t ob = q->dw_f32 ? 4 : 2;
+    Matrices w;
+    if (!row_stride(q->rows, q->n, &ys, 2) || !row_stride(q->rows, q->k, &xs, 2) ||
+        !matrices(q->dw, q->experts, q->n, q->k, q->dw_stride, q->dw_expert_stride, ob, &w))
+        return HR_ERR_INVALID_ARG;
+    if (ys * 2 > kMaxProductStride || xs * 2 > kMaxProductStride || w.stride * ob > kMaxProductStride)
+        return HR_ERR_TOO_LARGE;
+    if (q->dw == nullptr || (q->rows > 0 && (q->dy == nullptr || q->x == nullptr))) return HR_ERR_INVALID_ARG;
+    if (!aligned(q->dy, 2) || !aligned(q->x, 2) || !aligned(q->dw, ob) || !aligned(q->offsets, 4))
+        return HR_ERR_ALIGNMENT;
+    if (regions_overlap(w.region, {q->dy, q->rows, q->n * 2, ys * 2}) ||
+        regions_overlap(w.region, {q->x, q->rows, q->k * 2, xs * 2}) ||
+        regions_overlap(w.region, {q->offsets, 1, (static_cast<size_t>(q->experts) + 1) * 4, 0}))
+        return HR_ERR_INVALID_ARG;
+    a.q = static_cast<const char *>(q->dy);
+    a.p = static_cast<const char *>(q->x);
+    a.out = static_cast<char *>(q->dw);
+    a.offsets = q->offsets;
+    a.q_stride = ys * 2;
+    a.p_stride = xs * 2;
+    a.out_stride = w.stride * ob;
+    a.out_expert_stride = w.expert_stride * ob;
+    a.rows = static_cast<uint32_t>(q->rows);
+    a.experts = q->experts;
+    a.nq = static_cast<int>(q->n);
+    a.np = static_cast<int>(q->k);
+    any = !(units16(q->dy) && units16(q->x) && a.q_stride % 16 == 0 && a.p_stride % 16 == 0 && q->n % 8 == 0 &&
+            q->k % 8 == 0);
+    return HR_OK;
+}
+
+template <class K>
+hr_status launch_tiles(K kernel, size_t tiles, int threads, hr_stream_t stream, const ProductArgs &a) {
+    // (the dies' shares of the tiles are rounded up; a launch has fewer than 2^32 work-items)
+    const size_t grid = (tiles + 7) / 8 * 8;
+    if (grid >= (size_t(1) << 32) / threads) return HR_ERR_TOO_LARGE;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, reinterpret_cast<hipStream_t>(stream),
+                       a);
+    return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
+}
+
+// Tiles that segments of so many rows in all take at most.
+inline size_t tiles_of(size_t rows, int experts, size_t high) {
+    const size_t used = static_cast<size_t>(experts) < rows ? experts : rows;
+    const size_t most = rows / high + used;
+    return most < rows ? most : rows;
+}
+
+template <class E, class O, class SH, bool PA, bool ANY>
+hr_status run_product(ProductArgs &a, hr_stream_t stream) {
+    a.tiles_p = (a.np + SH::BP - 1) / SH::BP;
+    return launch_tiles(product_tiles<E, O, SH, false, PA, false, ANY>, tiles_of(a.rows, a.experts, SH::BQ) * a.tiles_p,
+                        SH::kThreads, stream, a);
+}
+
+typedef Shape<256, 256, 2, 4, 1, 2> Large;
+typedef Shape<128, 128, 2, 2, 1, 2> Middle;
+typedef Shape<16, 64, 1, 1, 4, 2> Few;
+
+template <class E, class O>
+hr_status launch_product(ProductArgs &a, bool across, bool any, hr_stream_t stream) {
+    if (any)
+        return across ? run_product<E, O, Middle, true, true>(a, stream) : run_product<E, O, Middle, false, true>(a, stream);
+    const size_t each = a.rows / a.experts;
+    if (each >= 256)
+        return across ? run_product<E, O, Large, true, false>(a, stream) : run_product<E, O, Large, false, false>(a, stream);
+    if (each >= 32)
+        return across ? run_product<E, O, Middle, true, false>(a, stream)
+                      : run_product<E, O, Middle, false, false>(a, stream);
+    return across ? run_product<E, O, Few, true, false>(a, stream) : run_product<E, O, Few, false, false>(a, stream);
+}
+
+template <class E, class O, class SH, bool ANY>
+hr_status run_product_grad(ProductArgs &a, hr_stream_t stream) {
+    a.tiles_q = (a.nq + SH::BQ - 1) / SH::BQ;
+    a.tiles_p = (a.np + SH::BP - 1) / SH::BP;
+    const size_t each = static_cast<size_t>(a.tiles_q) * a.tiles_p;
+    if (each >= (size_t(1) << 32) / HR_EXPERTS_MAX) return HR_ERR_TOO_LARGE;
+    return launch_tiles(product_tiles<E, O, SH, true, true, true, ANY>, each * a.experts, SH::kThreads, stream, a);
+}
+
+template <class E, class O>
+hr_status launch_product_grad(ProductArgs &a, bool any, hr_stream_t stream) {
+    if (any) return run_product_grad<E, O, Middle, true>(a, stream);
+    return a.nq >= 256 && a.np >= 256 ? run_product_grad<E, O, Large, false>(a, stream)
+                                      : run_product_grad<E, O, Middle, false>(a, stream);
+}
+
+}  // namespace hr

@@ -174,6 +174,51 @@ struct Unit {
     }
 };
 
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinScale = 0x1p-126f;
+
+// The scale of values whose largest magnitude is m (NaN stays NaN).
+__device__ __forceinline__ float e4m3_scale(float m) { return m < kE4m3Max * kMinScale ? kMinScale : m / kE4m3Max; }
+
+// y / scale, rounded once, with one reciprocal for the group.  The product
+// with it is up to 1.5 units in the last place off, which moves quotients
+// half way between two codes.  A step by the remainder brings it within
+// one unit, and from there the next gives the division's own result
+// (Markstein 1990: a quotient within a unit, the reciprocal to nearest, an
+// exact remainder; the negated one keeps the sign of a zero).  Remainders
+// are exact for scales from 2^-90 on where a quotient is 2^-11 or more,
+// and smaller ones have the code 0; smaller scales are lifted.  What is
+// finite over an infinite scale is 0.  (A norm of 16384 x 4096, one contribution
+// and a residual, 78.8 us, 84.0 with divisions, 77.6 with the bare product.)
+struct E4m3Codes {
+    float divisor, inv;
+    __device__ __forceinline__ E4m3Codes(float scale, float (&y)[8]) : divisor(scale) {
+        if (scale < 0x1p-90f) {
+            divisor *= 0x1p60f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= 0x1p60f;
+        }
+        inv = 1.0f / divisor;
+        divisor = divisor == INFINITY ? 0.0f : divisor;
+    }
+    __device__ __forceinline__ float over(float v) const {
+        float r = v * inv;
+        r = fmaf(-fmaf(r, divisor, -v), inv, r);
+        return fmaf(-fmaf(r, divisor, -v), inv, r);
+    }
+    // The codes of the 8 values that the constructor was given.
+    __device__ __forceinline__ u32x2 codes(const float (&y)[8]) const {
+        u32x2 c;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            int v = __builtin_amdgcn_cvt_pk_fp8_f32(over(y[4 * q]), over(y[4 * q + 1]), 0, false);
+            v = __builtin_amdgcn_cvt_pk_fp8_f32(over(y[4 * q + 2]), over(y[4 * q + 3]), v, true);
+            c[q] = static_cast<uint32_t>(v);
+        }
+        return c;
+    }
+};
+
 // Reductions over groups of L consecutive lanes (L a power of two up to 64),
 // every lane receiving the result: data-parallel primitives inside a row of
 // 16 lanes, lane-row swaps beyond.  The tree is fixed, so sums are the same
@@ -214,6 +259,12 @@ __device__ __forceinline__ float sum_lanes(float v) {
 template <int L>
 __device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
     return reduce_lanes<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+__device__ __forceinline__ uint32_t max_of_group(uint32_t v, int lanes) {
+    if (lanes == 16) return max_lanes<16>(v);
+    if (lanes == 8) return max_lanes<8>(v);
+    return max_lanes<4>(v);
 }
 
 // A 2-D buffer as a caller passes it: `rows` rows of `width` bytes, `stride`

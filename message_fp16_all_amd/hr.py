@@ -53,7 +53,10 @@ EXPORTS = ("hr_create_channel", "hr_allreduce_f16", "hr_reduce_f16", "hr_channel
            "hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
            "hr_rmsnorm_grad_workspace", "hr_router_topk", "hr_router_topk_grad", "hr_experts_rows",
            "hr_experts_sort_workspace", "hr_experts_sort", "hr_experts_gather", "hr_experts_combine_f16",
-           "hr_experts_combine_bf16", "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16")
+           "hr_experts_combine_bf16", "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16",
+           "hr_experts_product_f16", "hr_experts_product_bf16", "hr_experts_product_e4m3_f16",
+           "hr_experts_product_e4m3_bf16", "hr_experts_product_grad_f16", "hr_experts_product_grad_bf16",
+           "hr_experts_act_f16", "hr_experts_act_bf16", "hr_experts_act_grad_f16", "hr_experts_act_grad_bf16")
 
 HR_ROUTE_HOST = 0
 HR_DECLINE_DISABLED = 1
@@ -73,6 +76,7 @@ HR_ROUTER_MAX_K = 32
 HR_ROUTER_MAX_TOKENS = (1 << 26) - 4
 HR_EXPERTS_MAX = 1024
 HR_EXPERTS_MAX_K = 32
+HR_EXPERTS_PRODUCT_MAX = 1 << 20
 HR_EXPERTS_SORT_FEW = 8192
 
 
@@ -159,6 +163,39 @@ class hr_experts_combine_grad_args(ctypes.Structure):
                 ("experts", ctypes.c_int)]
 
 
+class hr_experts_product_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("x", "w", "out", "offsets", "x_scales", "w_scales")),
+                *((n, ctypes.c_size_t) for n in ("rows", "n", "k", "x_stride", "out_stride", "w_stride",
+                                                 "w_expert_stride", "x_scales_stride", "w_scales_stride",
+                                                 "w_scales_expert_stride")),
+                ("experts", ctypes.c_int),
+                ("transposed", ctypes.c_int)]
+
+
+class hr_experts_product_grad_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("dy", "x", "dw", "offsets")),
+                *((n, ctypes.c_size_t) for n in ("rows", "n", "k", "dy_stride", "x_stride", "dw_stride",
+                                                 "dw_expert_stride")),
+                ("experts", ctypes.c_int),
+                ("dw_f32", ctypes.c_int)]
+
+
+class hr_experts_act_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("x", "out", "codes", "scales", "offsets")),
+                *((n, ctypes.c_size_t) for n in ("rows", "width", "x_stride", "out_stride", "codes_stride",
+                                                 "scales_stride")),
+                ("gated", ctypes.c_int),
+                ("group", ctypes.c_int),
+                ("experts", ctypes.c_int)]
+
+
+class hr_experts_act_grad_args(ctypes.Structure):
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("dy", "x", "dx", "out", "offsets")),
+                *((n, ctypes.c_size_t) for n in ("rows", "width", "dy_stride", "x_stride", "dx_stride",
+                                                 "out_stride")),
+                ("experts", ctypes.c_int)]
+
+
 class HrError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -213,7 +250,10 @@ def load() -> ctypes.CDLL:
     # argument structs: byref of the ctypes struct, or its bytes
     for name in ("hr_reduce_rmsnorm_f16", "hr_reduce_rmsnorm_bf16", "hr_rmsnorm_grad_f16", "hr_rmsnorm_grad_bf16",
                  "hr_experts_gather", "hr_experts_combine_f16", "hr_experts_combine_bf16",
-                 "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16"):
+                 "hr_experts_combine_grad_f16", "hr_experts_combine_grad_bf16", "hr_experts_product_f16",
+                 "hr_experts_product_bf16", "hr_experts_product_e4m3_f16", "hr_experts_product_e4m3_bf16",
+                 "hr_experts_product_grad_f16", "hr_experts_product_grad_bf16", "hr_experts_act_f16",
+                 "hr_experts_act_bf16", "hr_experts_act_grad_f16", "hr_experts_act_grad_bf16"):
         getattr(lib, name).argtypes = [vp, vp]
     lib.hr_rmsnorm_grad_workspace.argtypes = [ctypes.c_size_t, ctypes.c_size_t]
     lib.hr_router_topk.argtypes = [vp, ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
@@ -454,6 +494,56 @@ def hr_experts_combine_grad_bf16(args, stream: int) -> int:
     return load().hr_experts_combine_grad_bf16(ctypes.byref(args), stream)
 
 
+def hr_experts_product_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_product_args.  Returns the hr_status code."""
+    return load().hr_experts_product_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_product_bf16(args, stream: int) -> int:
+    """As hr_experts_product_f16 for bfloat16 buffers."""
+    return load().hr_experts_product_bf16(ctypes.byref(args), stream)
+
+
+def hr_experts_product_e4m3_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_product_args.  Returns the hr_status code."""
+    return load().hr_experts_product_e4m3_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_product_e4m3_bf16(args, stream: int) -> int:
+    """As hr_experts_product_e4m3_f16 for bfloat16 buffers."""
+    return load().hr_experts_product_e4m3_bf16(ctypes.byref(args), stream)
+
+
+def hr_experts_product_grad_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_product_grad_args.  Returns the hr_status code."""
+    return load().hr_experts_product_grad_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_product_grad_bf16(args, stream: int) -> int:
+    """As hr_experts_product_grad_f16 for bfloat16 buffers."""
+    return load().hr_experts_product_grad_bf16(ctypes.byref(args), stream)
+
+
+def hr_experts_act_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_act_args.  Returns the hr_status code."""
+    return load().hr_experts_act_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_act_bf16(args, stream: int) -> int:
+    """As hr_experts_act_f16 for bfloat16 buffers."""
+    return load().hr_experts_act_bf16(ctypes.byref(args), stream)
+
+
+def hr_experts_act_grad_f16(args, stream: int) -> int:
+    """Raw call; ``args`` is an hr_experts_act_grad_args.  Returns the hr_status code."""
+    return load().hr_experts_act_grad_f16(ctypes.byref(args), stream)
+
+
+def hr_experts_act_grad_bf16(args, stream: int) -> int:
+    """As hr_experts_act_grad_f16 for bfloat16 buffers."""
+    return load().hr_experts_act_grad_bf16(ctypes.byref(args), stream)
+
+
 def workspace(G: int, numel: int, dtype=None, device=0):
     """A device buffer holding G contributions in the hr_workspace_stride
     layout; returns (buffer, [view of contribution g])."""
@@ -576,6 +666,10 @@ _NORM_GRAD = struct.Struct("@8P7Ni4x")
 _GATHER = struct.Struct("@7P8N2i")
 _COMBINE = struct.Struct("@5P6Ni4x")
 _COMBINE_GRAD = struct.Struct("@8P6N2i")
+_PRODUCT = struct.Struct("@6P10N2i")
+_PRODUCT_GRAD = struct.Struct("@4P7N2i")
+_ACT = struct.Struct("@5P6N3i4x")
+_ACT_GRAD = struct.Struct("@5P6Ni4x")
 _NULLS = [0] * HR_MAX_G
 _entries = {}
 
@@ -963,6 +1057,172 @@ def experts_combine_grad(dy, z, pos, weights=None, dz=None, dweights=None, *, of
     if st != HR_OK:
         raise HrError(st, name)
     return dz, dweights
+
+
+def _matrices_view(t, name: str, dtype):
+    """(address, experts, rows, columns, row stride, expert stride) of one
+    matrix or of one per expert; a stride that no second row or expert needs is 0."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a device tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        shape, stride = (1, *shape), (0, *stride)
+    elif len(shape) != 3:
+        raise ValueError(f"{name}: expected experts x rows x columns, or one matrix")
+    e, r, c = shape
+    se, sr, sc = stride
+    if sc != 1 and c > 1:
+        raise ValueError(f"{name}: expected rows of adjacent values")
+    sr = sr if r > 1 else 0
+    if (r > 1 and sr < c) or (e > 1 and se < (r - 1) * sr + c):
+        raise ValueError(f"{name}: rows or matrices overlap")
+    return t.data_ptr(), e, r, c, sr, se if e > 1 else 0
+
+
+def _segments_ptr(offsets, experts: int, rows: int) -> int:
+    """Address of a sort's offsets, or of none (one expert, every row)."""
+    if offsets is None:
+        if experts != 1:
+            raise ValueError(f"{experts} matrices without offsets")
+        return 0
+    return _flat_ptr(offsets, "offsets", _torch.int32, experts + 1)
+
+
+def _call_on(fn, name: str, args, stream, first, *others):
+    """The call on ``first``'s device, which every tensor has to be on."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on several devices")
+    if dev >= 0 and _torch.cuda.current_device() != dev:
+        with _torch.cuda.device(dev):
+            st = fn(args, _stream_of(stream, first))
+    else:
+        st = fn(args, _stream_of(stream, first))
+    if st != HR_OK:
+        raise HrError(st, name)
+
+
+def experts_product(x, w, out, *, offsets=None, transposed: bool = False, x_scales=None, w_scales=None, stream=None):
+    """Every row times its expert's matrix, in one kernel (hr_experts_product):
+    out[r] = x[r] @ w[e].T, or with ``transposed`` x[r] @ w[e], for the rows
+    offsets[e] .. offsets[e + 1] - 1 of each expert (a sort's ``offsets``; None:
+    one matrix, every row).  Rows of no segment are not written.
+
+    ``x`` and ``w`` (experts x n x k, as linear layers keep it; transposed,
+    experts x k x n) are torch.float16 or torch.bfloat16 like ``out``; or
+    torch.float8_e4m3fn with ``x_scales``, one per 128 values of a row, and
+    ``w_scales``, one per 128 x 128 values of a matrix (torch.float32).  The
+    gradient of the rows is the same call of dy with the other ``transposed``."""
+    dt = out.dtype
+    if _torch is None:
+        _tm()
+    eight = x_scales is not None or w_scales is not None
+    fn, name = _entry("hr_experts_product_e4m3" if eight else "hr_experts_product", dt)
+    if eight:
+        if x_scales is None or w_scales is None:
+            raise ValueError("x_scales and w_scales go together")
+        dt = _torch.float8_e4m3fn
+    xp, rows, k, xs = _row_view(x, "x", dt)
+    wp, experts, wr, wc, ws, we = _matrices_view(w, "w", dt)
+    n = wc if transposed else wr
+    if k != (wr if transposed else wc):
+        raise ValueError(f"w: matrices of {wr} x {wc} for rows of {k} values")
+    op, _, _, os_ = _row_view(out, "out", out.dtype, rows, n)
+    fp = _segments_ptr(offsets, experts, rows)
+    sp = ss = tp = ts = te = 0
+    if eight:
+        f32 = _torch.float32
+        groups = -(-k // 128)
+        if x_scales.dim() == 1 and groups == 1:
+            x_scales = x_scales.unsqueeze(1)
+        sp, _, _, ss = _row_view(x_scales, "x_scales", f32, rows, groups)
+        tp, e, r, c, ts, te = _matrices_view(w_scales, "w_scales", f32)
+        if e != experts or r != -(-wr // 128) or c != -(-wc // 128):
+            raise ValueError(f"w_scales: {e} x {r} x {c}, expected {experts} x {-(-wr // 128)} x {-(-wc // 128)}")
+    args = _PRODUCT.pack(xp, wp, op, fp, sp, tp, rows, n, k, xs, os_, ws, we, ss, ts, te, experts,
+                         1 if transposed else 0)
+    _call_on(fn, name, args, stream, x, w, out, offsets, x_scales, w_scales)
+    return out
+
+
+def experts_product_grad(dy, x, dw, *, offsets=None, stream=None):
+    """The gradient of experts_product's matrices (hr_experts_product_grad):
+    dw[e] = dy[rows of e].T @ x[rows of e] (experts x n x k), in the rows' type
+    or torch.float32; zeros for an expert without rows.  For matrices kept
+    transposed, ``x`` and ``dy`` change places."""
+    dt = dy.dtype
+    fn, name = _entry("hr_experts_product_grad", dt)
+    yp, rows, n, ys = _row_view(dy, "dy", dt)
+    xp, xrows, k, xs = _row_view(x, "x", dt)
+    if xrows != rows:
+        raise ValueError(f"x: {xrows} rows, dy has {rows}")
+    f32 = dw.dtype is _torch.float32
+    wp, experts, wr, wc, ws, we = _matrices_view(dw, "dw", _torch.float32 if f32 else dt)
+    if wr != n or wc != k:
+        raise ValueError(f"dw: matrices of {wr} x {wc}, expected {n} x {k}")
+    fp = _segments_ptr(offsets, experts, rows)
+    args = _PRODUCT_GRAD.pack(yp, xp, wp, fp, rows, n, k, ys, xs, ws, we, experts, int(f32))
+    _call_on(fn, name, args, stream, dy, x, dw, offsets)
+    return dw
+
+
+def _used_ptr(offsets):
+    """(address, experts) of a sort's offsets, whose last entry bounds the rows."""
+    if offsets is None:
+        return 0, 0
+    return _flat_ptr(offsets, "offsets", _torch.int32, offsets.numel()), offsets.numel() - 1
+
+
+def experts_act(x, out=None, *, gated: bool = True, offsets=None, out8=None, scales=None, group: int = 128,
+                stream=None):
+    """silu(gate) * up of rows that hold gate, then up (not ``gated``: the rows
+    as they are), into ``out`` in their type and into ``out8``
+    (torch.float8_e4m3fn) with ``scales`` (torch.float32, one per ``group`` of 32,
+    64 or 128 values), in one kernel (hr_experts_act).  With a sort's ``offsets``
+    the rows past its last segment are left alone."""
+    dt = x.dtype
+    fn, name = _entry("hr_experts_act", dt)
+    xp, rows, width, xs = _row_view(x, "x", dt)
+    if gated:
+        if width % 2:
+            raise ValueError(f"x: rows of {width} values hold no two halves")
+        width //= 2
+    op = os_ = cp = cs = sp = ss = 0
+    if out is not None:
+        op, _, _, os_ = _row_view(out, "out", dt, rows, width)
+    if out8 is not None:
+        cp, _, _, cs = _row_view(out8, "out8", _torch.float8_e4m3fn, rows, width)
+    if scales is not None:
+        if group < 1:
+            raise ValueError(f"groups of {group}")
+        groups = -(-width // group)
+        if scales.dim() == 1 and groups == 1:
+            scales = scales.unsqueeze(1)
+        sp, _, _, ss = _row_view(scales, "scales", _torch.float32, rows, groups)
+    fp, experts = _used_ptr(offsets)
+    args = _ACT.pack(xp, op, cp, sp, fp, rows, width, xs, os_, cs, ss, 1 if gated else 0, group, experts)
+    _call_on(fn, name, args, stream, x, out, out8, scales, offsets)
+    return out
+
+
+def experts_act_grad(dy, x, dx, *, out=None, offsets=None, stream=None):
+    """The gradient of experts_act, gated, into ``dx`` (which may be ``x``), and
+    the forward call's ``out`` once more if given (hr_experts_act_grad)."""
+    dt = x.dtype
+    fn, name = _entry("hr_experts_act_grad", dt)
+    yp, rows, width, ys = _row_view(dy, "dy", dt)
+    xp, _, _, xs = _row_view(x, "x", dt, rows, 2 * width)
+    dp, _, _, ds = _row_view(dx, "dx", dt, rows, 2 * width)
+    op = os_ = 0
+    if out is not None:
+        op, _, _, os_ = _row_view(out, "out", dt, rows, width)
+    fp, experts = _used_ptr(offsets)
+    args = _ACT_GRAD.pack(yp, xp, dp, op, fp, rows, width, ys, xs, ds, os_, experts)
+    _call_on(fn, name, args, stream, x, dy, dx, out, offsets)
+    return dx
 
 
 class Channel:
