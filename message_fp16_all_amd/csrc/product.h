@@ -37,6 +37,8 @@
 // values have 8 bits.  The 16-bit instructions keep all of binary32.)
 #pragma once
 
+#include <type_traits>
+
 #include "rows.h"
 
 namespace hr {
@@ -77,9 +79,9 @@ struct ProductArgs {
 // (the buffer's bounds check).
 constexpr uint32_t kNowhere = 0x80000000u;
 
-__device__ __forceinline__ i32x4 buffer_of(const char *base) {
+__device__ __forceinline__ i32x4 buffer_of(const char *base, bool here = true) {
     const uint64_t a = reinterpret_cast<uint64_t>(base);
-    return i32x4{static_cast<int>(a), static_cast<int>((a >> 32) & 0xFFFFu), 0x7FFFFFFF, 0x00020000};
+    return i32x4{static_cast<int>(a), static_cast<int>((a >> 32) & 0xFFFFu), here ? 0x7FFFFFFF : 0, 0x00020000};
 }
 
 // 16 (or 4) bytes a lane from HBM to LDS at `to` + 16 (4) * lane.  Written out
@@ -104,6 +106,23 @@ __device__ __forceinline__ void landed() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
 }
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" : : : "memory"); }
+
+// The LDS reads above are done, and nothing moves over this line.
+__device__ __forceinline__ void read_done() {
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void change() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A value that no kernel running now writes, at an address that a wave shares:
+// read through the scalar cache, so that it is not waited for with the loads.
+__device__ __forceinline__ float constant_at(const float *p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) float *>(reinterpret_cast<uint64_t>(p));
+}
 
 template <class V>
 __device__ __forceinline__ V lds_read(uint32_t at) {
@@ -312,7 +331,7 @@ __device__ __forceinline__ Tile product_tile(const ProductArgs &a, uint32_t grou
         const uint64_t past = __ballot(tile < upto);
         if (past != 0) {
             const int at = __builtin_ctzll(past);
-            t.expert = e0 + at;
+            t.expert = __builtin_amdgcn_readfirstlane(e0 + at);
             t.first = __builtin_amdgcn_readlane(lo, at);
             t.last = __builtin_amdgcn_readlane(hi, at);
             const uint32_t all = __builtin_amdgcn_readlane(n, at), end = __builtin_amdgcn_readlane(upto, at);
@@ -338,6 +357,62 @@ __device__ __forceinline__ Tile gradient_tile(const ProductArgs &a, uint32_t gro
     t.first = __builtin_amdgcn_readfirstlane(lo);
     t.last = __builtin_amdgcn_readfirstlane(hi);
     return t;
+}
+
+template <class O>
+constexpr int kOut = __is_same(O, float) ? 4 : 2;       // bytes
+
+// A wave's sums to the tile's rows at `out`: operand j of Q is its rows q(j) ..
+// q(j) + 15, the wave's first value of P is p0; nq rows and np values are there.
+// A lane holds row q(j) + lane % 16, and per operand of P four adjacent values
+// (laced: 16 of four operands).
+template <class O, bool LACED, int FP, int FQ, class Q>
+__device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out, size_t stride, Q q_of, int p0, int nq,
+                                           int np, uint32_t lane) {
+    constexpr int OB = kOut<O>, RUN = LACED ? 4 : 1;            // RUN: operands whose values are adjacent
+    const int g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+        const int q = q_of(j) + (lane & 15);
+        if (q >= nq) continue;
+        char *row = out + q * stride;
+#pragma unroll
+        for (int i = 0; i < FP; i += RUN) {
+            const int p = p0 + (LACED ? 16 * i + 16 * g : 16 * i + 4 * g);
+            if (p >= np) continue;
+            if constexpr (OB == 4) {
+#pragma unroll
+                for (int r = 0; r < RUN; ++r) {
+                    if (p + 4 * r + 4 <= np) {
+                        *reinterpret_cast<f32x4_row *>(row + (p + 4 * r) * 4) = sum[i + r][j];
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (p + 4 * r + v < np)
+                                *reinterpret_cast<float *>(row + (p + 4 * r + v) * 4) = sum[i + r][j][v];
+                    }
+                }
+            } else if (p + 4 * RUN <= np) {
+                u32x2 v[RUN];
+#pragma unroll
+                for (int r = 0; r < RUN; ++r) v[r] = narrow4<O>(sum[i + r][j]);
+                if constexpr (RUN == 4) {
+                    store_vec<false>(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, row + p * 2);
+                    store_vec<false>(u32x4{v[2].x, v[2].y, v[3].x, v[3].y}, row + p * 2 + 16);
+                } else {
+                    *reinterpret_cast<u32x2_row *>(row + p * 2) = v[0];
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < RUN; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (p + 4 * r + v < np)
+                            *reinterpret_cast<uint16_t *>(row + (p + 4 * r + v) * 2) =
+                                Wide<O>::narrow1(sum[i + r][j][v]);
+            }
+        }
+    }
 }
 
 // A kernel's shape: tiles of BQ x BP; WQ x WP waves over them, WK times over
@@ -488,7 +563,7 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
             }
         } else {
             const int panel = s * SH::WK + wk;
-            const float block = panel < panels ? ws[panel * a.scales_c] : 0.0f;
+            const float block = panel < panels ? constant_at(ws + panel * a.scales_c) : 0.0f;
             i32x8 x[FQ];
             float scale[FQ];
 #pragma unroll
@@ -596,53 +671,278 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
                                                  (i * FQ + j) * 1024);
     }
 
-    // a lane's values: row 16 j + lane % 16 of out, and per operand of P four
-    // adjacent ones (interleaved: 16 of four operands)
-    constexpr int OB = __is_same(O, float) ? 4 : 2;
     char *out = a.out + (GRAD ? tile.expert * a.out_expert_stride + static_cast<size_t>(q0) * a.out_stride
                               : (static_cast<size_t>(tile.first) + q0) * a.out_stride);
-    const int g = lane >> 4;
-    constexpr int RUN = LACED ? 4 : 1;                          // operands whose values are adjacent
+    store_sums<O, LACED, FP, FQ>(sum, out + static_cast<size_t>(p0) * kOut<O>, a.out_stride,
+                                 [&](int j) { return wq * PQ + 16 * j; }, wp * PP, nq, np, lane);
+}
+
+// The large tile: 256 x 256 by eight waves of 128 x 64, which read 24 KB of LDS
+// for 64 matrix instructions and 64 KB of memory for 512.
+//
+// Two sets of four waves, one wave of each set on every SIMD, take turns: while
+// one set's matrix instructions run, the other reads its operands, and a barrier
+// changes them over.  A stage is one panel of P and two of Q (rows 0..127 and
+// 128..255 of the tile; a wave has 64 of each), and is worked on in two turns,
+// one for each panel of Q:
+//
+//     turn          4 s    4 s + 1   4 s + 2   4 s + 3   4 s + 4
+//     first set     read   multiply  read      multiply  read
+//     second set           read      multiply  read      multiply
+//
+// Loads go out between matrix instructions.  P and the first panel of Q were
+// last read in turn 4 s + 1, and the loads of stage s + 2 into their place go out
+// while a set multiplies for the second time; those of the second panel of
+// stage s + 1 while it does so for the first.  A set waits for its own loads
+// before the barrier after which either set reads them, three to four turns
+// later.  Every turn of a wave issues the same number of loads, the last stages'
+// from nowhere, so that the turns are straight code and the waits' counts fixed.
+// (A tile of at most 128 rows takes one turn per stage, and has three buffers.)
+template <class E, class O, bool QA, bool PA, bool GRAD>
+__global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
+    constexpr int SIZE = kBytes<E>, BQ = 256, BP = 256, H = 128, FP = 4, FH = 4;
+    constexpr bool LACED = !PA, SCALED = SIZE == 1;
+    using PanelQ = Panel<SIZE, H, QA, false>;
+    using PanelP = Panel<SIZE, BP, PA, LACED>;
+    constexpr int CK = PanelP::kC;
+    constexpr uint32_t QB = PanelQ::kBytesAll, PB = PanelP::kBytesAll;      // 16 and 32 KB
+    constexpr uint32_t kScales = 3 * (PB + QB);
+    constexpr int D0 = 6 + SCALED, D1 = 2;                                  // a wave's loads for the turns
+    __shared__ __align__(1024) char lds[kScales + (SCALED ? 4 * BQ * 4 : 0)];
+
+    const Tile tile = GRAD ? gradient_tile(a, blockIdx.x) : product_tile<BQ>(a, blockIdx.x);
+    if (!tile.there) return;
+    const uint32_t lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const bool second = wave >= 4;
+    const int wq = wave & 1, wp = wave >> 1;
+
+    const int q0 = tile.q * BQ, p0 = tile.p * BP;
+    const int nq = GRAD ? a.nq - q0 : static_cast<int>(tile.last - tile.first) - q0;
+    const int np = a.np - p0;
+    const int nc = GRAD ? static_cast<int>(tile.last - tile.first) : a.nc;
+    const int stages = (nc + CK - 1) / CK;
+    const char *qs = a.q, *ps = a.p;
+    if constexpr (GRAD) {
+        qs += tile.first * a.q_stride + static_cast<size_t>(q0) * SIZE;
+        ps += tile.first * a.p_stride + static_cast<size_t>(p0) * SIZE;
+    } else {
+        qs += (static_cast<size_t>(tile.first) + q0) * a.q_stride;
+        ps += tile.expert * a.p_expert_stride + (PA ? static_cast<size_t>(p0) * SIZE : p0 * a.p_stride);
+    }
+    const size_t q_step = QA ? CK * a.q_stride : 128, p_step = PA ? CK * a.p_stride : 128;
+    const float *xs = nullptr, *ws = nullptr;
+    if constexpr (SCALED) {
+        xs = a.q_scales + (static_cast<size_t>(tile.first) + q0) * a.q_scales_stride;
+        const int block = (p0 + wp * 64) / 128, last = (a.np - 1) / 128;
+        ws = a.p_scales + tile.expert * a.scales_expert + (block < last ? block : last) * a.scales_p;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(HR_LDS char *)lds;
+
+    // offsets of a wave's loads: P, and the two panels of Q (c values of the stage
+    // left; the last stage's are trimmed before its loads go out)
+    uint32_t off_p[4], off_q[4], off_s = kNowhere;
+    const auto offsets = [&](int c) {
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-        const int q = wq * PQ + 16 * j + (lane & 15);
-        if (q >= nq) continue;
-        char *row = out + q * a.out_stride + static_cast<size_t>(p0) * OB;
+        for (int d = 0; d < 4; ++d) {
+            uint32_t row, unit;
+            PanelP::source(wave * 4 + d, lane, row, unit);
+            off_p[d] = PanelP::there(row, unit, np, c) ? static_cast<uint32_t>(row * a.p_stride) + unit * 16 : kNowhere;
+            PanelQ::source(wave * 2 + (d & 1), lane, row, unit);
+            if constexpr (QA)
+                unit += (d >> 1) * H / PanelQ::kUnit;
+            else
+                row += (d >> 1) * H;
+            off_q[d] = PanelQ::there(row, unit, nq, c) ? static_cast<uint32_t>(row * a.q_stride) + unit * 16 : kNowhere;
+        }
+    };
+    offsets(nc < CK ? nc : CK);
+    if constexpr (SCALED) {
+        const int row = wave % 4 * 64 + lane;                   // (either set brings them all)
+        if (row < nq) off_s = static_cast<uint32_t>(row * a.q_scales_stride * 4);
+    }
+    const auto trim = [&](int s) {
+        if (s == stages - 1 && s > 0 && nc % CK != 0) offsets(nc % CK);
+    };
+    // load d of a wave for the first turn of stage s, into buffer b, and for the
+    // second
+    const auto bring0 = [&](int s, int b, int d) {
+        const bool here = s < stages;
+        if (d < 4)
+            dma16(buffer_of(ps + s * p_step, here), off_p[d], lds0 + b * PB + (wave * 4 + d) * 1024);
+        else if (d < 6)
+            dma16(buffer_of(qs + s * q_step, here), off_q[d - 4], lds0 + 3 * PB + b * QB + (wave * 2 + d - 4) * 1024);
+        else
+            dma4(buffer_of(reinterpret_cast<const char *>(xs + s), here), off_s,
+                 lds0 + kScales + (s & 3) * BQ * 4 + wave % 4 * 256);
+    };
+    const auto bring1 = [&](int s, int b, int d) {
+        dma16(buffer_of(qs + s * q_step, s < stages), off_q[2 + d], lds0 + 2 * PB + b * QB + (wave * 2 + d) * 1024);
+    };
+
+    Reader<SIZE, H, QA, false, FH> from_q;
+    Reader<SIZE, BP, PA, LACED, FP> from_p;
+    from_q.init(wq * 64, lane);
+    from_p.init(wp * 64, lane);
+
+    u32x4 w[2][FP], x[2][FH];
+    i32x8 w8[FP], x8[FH];                                       // (e4m3: both halves as one operand)
+    float block = 0.0f, scale[FH];
+    const auto block_of = [&](int s) { block = constant_at(ws + (s < stages ? s : 0) * a.scales_c); };
+    const auto read_p = [&](uint32_t at) {
 #pragma unroll
-        for (int i = 0; i < FP; i += RUN) {
-            const int p = wp * PP + (LACED ? 16 * i + 16 * g : 16 * i + 4 * g);
-            if (p >= np) continue;
-            if constexpr (OB == 4) {
-#pragma unroll
-                for (int r = 0; r < RUN; ++r) {
-                    if (p + 4 * r + 4 <= np) {
-                        *reinterpret_cast<f32x4_row *>(row + (p + 4 * r) * 4) = sum[i + r][j];
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (p + 4 * r + v < np) *reinterpret_cast<float *>(row + (p + 4 * r + v) * 4) = sum[i + r][j][v];
-                    }
-                }
-            } else if (p + 4 * RUN <= np) {
-                u32x2 v[RUN];
-#pragma unroll
-                for (int r = 0; r < RUN; ++r) v[r] = narrow4<O>(sum[i + r][j]);
-                if constexpr (RUN == 4) {
-                    store_vec<false>(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, row + p * 2);
-                    store_vec<false>(u32x4{v[2].x, v[2].y, v[3].x, v[3].y}, row + p * 2 + 16);
-                } else {
-                    *reinterpret_cast<u32x2_row *>(row + p * 2) = v[0];
-                }
+        for (int i = 0; i < FP; ++i) {
+            if constexpr (SCALED) {
+                w8[i] = join(from_p.read(at, i, 0), from_p.read(at, i, 1));
             } else {
-#pragma unroll
-                for (int r = 0; r < RUN; ++r)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (p + 4 * r + v < np)
-                            *reinterpret_cast<uint16_t *>(row + (p + 4 * r + v) * 2) = Wide<O>::narrow1(sum[i + r][j][v]);
+                w[0][i] = from_p.read(at, i, 0);
+                w[1][i] = from_p.read(at, i, 1);
             }
         }
+    };
+    const auto read_q = [&](int s, int turn, uint32_t at) {
+#pragma unroll
+        for (int j = 0; j < FH; ++j) {
+            if constexpr (SCALED) {
+                x8[j] = join(from_q.read(at, j, 0), from_q.read(at, j, 1));
+                scale[j] = lds_read<float>(lds0 + kScales + (s & 3) * BQ * 4 +
+                                           (turn * H + wq * 64 + 16 * j + (lane & 15)) * 4) * block;
+            } else {
+                x[0][j] = from_q.read(at, j, 0);
+                x[1][j] = from_q.read(at, j, 1);
+            }
+        }
+    };
+    // a turn's instructions for one panel of Q, with the turn's loads between them
+    const auto multiply = [&](f32x4 (&sum)[FP][FH], auto loads_, auto load) {
+        constexpr int loads = decltype(loads_)::value;
+        __builtin_amdgcn_s_setprio(1);
+        if constexpr (!SCALED) {
+            constexpr int N = 2 * FP * FH, EACH = N / (loads + 1);
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                const int half = t / (FP * FH), j = t / FP % FH, i = t % FP;
+                sum[i][j] = mfma16<E>(w[half][i], x[half][j], sum[i][j]);
+                if (t % EACH == EACH - 1 && t / EACH < loads) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    load(t / EACH);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        } else {
+            // (a part is scaled two instructions later, when it is there)
+            constexpr int N = FP * FH, EACH = N / (loads + 1);
+            f32x4 part[3];
+#pragma unroll
+            for (int t = 0; t < N + 2; ++t) {
+                if (t < N) part[t % 3] = mfma8(w8[t % FP], x8[t / FP]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (t >= 2) {
+                    const int u = t - 2;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        sum[u % FP][u / FP][v] = fmaf(part[u % 3][v], scale[u / FP], sum[u % FP][u / FP][v]);
+                }
+                if (t % EACH == EACH - 1 && t / EACH < loads) load(t / EACH);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // (the sums are made here: the compiler would move them past the barriers)
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FH; ++j) asm volatile("" : "+v"(sum[i][j]));
+        __builtin_amdgcn_s_setprio(0);
+    };
+    char *out = a.out + (GRAD ? tile.expert * a.out_expert_stride + static_cast<size_t>(q0) * a.out_stride
+                              : (static_cast<size_t>(tile.first) + q0) * a.out_stride);
+    out += static_cast<size_t>(p0) * kOut<O>;
+    const auto clear = [](f32x4 (&sum)[FP][FH]) {
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FH; ++j) sum[i][j] = f32x4{0, 0, 0, 0};
+    };
+    const auto store = [&](const f32x4 (&sum)[FP][FH], int turn) {
+        store_sums<O, LACED, FP, FH>(sum, out, a.out_stride, [&](int j) { return turn * H + wq * 64 + 16 * j; }, wp * 64,
+                                     nq, np, lane);
+    };
+
+    const std::integral_constant<int, D0> d0;
+    const std::integral_constant<int, D1> d1;
+    f32x4 sum0[FP][FH];
+    clear(sum0);
+    if constexpr (SCALED) block_of(0);
+    if (nq <= H) {
+        //     turn          2 s    2 s + 1   2 s + 2   2 s + 3
+        //     first set     read   multiply  read      multiply
+        //     second set           read      multiply  read
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            trim(s);
+#pragma unroll
+            for (int d = 0; d < D0; ++d) bring0(s, s, d);
+        }
+        landed<D0>();
+        change();
+        if (second) change();
+        int b = 0;
+        for (int s = 0; s < stages; ++s) {
+            read_p(lds0 + b * PB);
+            read_q(s, 0, lds0 + 3 * PB + b * QB);
+            if (second) landed<0>();                            // stage s + 1
+            read_done();
+            change();
+            trim(s + 2);
+            if constexpr (SCALED) block_of(s + 1);
+            const int to = b == 0 ? 2 : b - 1;
+            multiply(sum0, d0, [&](int d) { bring0(s + 2, to, d); });
+            if (!second) landed<D0>();                          // stage s + 1
+            change();
+            b = b == 2 ? 0 : b + 1;
+        }
+        if (!second) change();
+        landed<0>();            // (nothing may reach this LDS when it is another's)
+        store(sum0, 0);
+        return;
     }
+
+#pragma unroll
+    for (int d = 0; d < D0; ++d) bring0(0, 0, d);
+#pragma unroll
+    for (int d = 0; d < D1; ++d) bring1(0, 0, d);
+    trim(1);
+#pragma unroll
+    for (int d = 0; d < D0; ++d) bring0(1, 1, d);
+    landed<D0 + D1>();          // stage 0, for its first turn
+    change();
+    if (second) change();
+    f32x4 sum1[FP][FH];
+    clear(sum1);
+    for (int s = 0; s < stages; ++s) {
+        const int b = s & 1;
+        read_p(lds0 + b * PB);
+        read_q(s, 0, lds0 + 3 * PB + b * QB);
+        if (second) landed<D0>();                               // stage s, second turn
+        read_done();
+        change();
+        multiply(sum0, d1, [&](int d) { bring1(s + 1, b ^ 1, d); });
+        if (!second) landed<D0 + D1>();                         // the same
+        change();
+        read_q(s, 1, lds0 + 2 * PB + b * QB);
+        if (second) landed<D1>();                               // stage s + 1, first turn
+        read_done();
+        change();
+        trim(s + 2);
+        if constexpr (SCALED) block_of(s + 1);
+        multiply(sum1, d0, [&](int d) { bring0(s + 2, b, d); });
+        if (!second) landed<D0 + D1>();                         // the same
+        change();
+    }
+    if (!second) change();
+    landed<0>();
+    store(sum0, 0);
+    store(sum1, 1);
 }
 
 }  // namespace hr

@@ -155,7 +155,6 @@ hr_status run_product(ProductArgs &a, hr_stream_t stream) {
                         SH::kThreads, stream, a);
 }
 
-typedef Shape<256, 256, 2, 4, 1, 2> Large;
 typedef Shape<128, 128, 2, 2, 1, 2> Middle;
 typedef Shape<16, 64, 1, 1, 4, 2> Few;
 
@@ -164,8 +163,12 @@ hr_status launch_product(ProductArgs &a, bool across, bool any, hr_stream_t stre
     if (any)
         return across ? run_product<E, O, Middle, true, true>(a, stream) : run_product<E, O, Middle, false, true>(a, stream);
     const size_t each = a.rows / a.experts;
-    if (each >= 256)
-        return across ? run_product<E, O, Large, true, false>(a, stream) : run_product<E, O, Large, false, false>(a, stream);
+    if (each >= 256) {
+        a.tiles_p = (a.np + 255) / 256;
+        const size_t tiles = tiles_of(a.rows, a.experts, 256) * a.tiles_p;
+        return across ? launch_tiles(product_large<E, O, false, true, false>, tiles, 512, stream, a)
+                      : launch_tiles(product_large<E, O, false, false, false>, tiles, 512, stream, a);
+    }
     if (each >= 32)
         return across ? run_product<E, O, Middle, true, false>(a, stream)
                       : run_product<E, O, Middle, false, false>(a, stream);
@@ -184,8 +187,13 @@ hr_status run_product_grad(ProductArgs &a, hr_stream_t stream) {
 template <class E, class O>
 hr_status launch_product_grad(ProductArgs &a, bool any, hr_stream_t stream) {
     if (any) return run_product_grad<E, O, Middle, true>(a, stream);
-    return a.nq >= 256 && a.np >= 256 ? run_product_grad<E, O, Large, false>(a, stream)
-                                      : run_product_grad<E, O, Middle, false>(a, stream);
+    if (a.nq >= 256 && a.np >= 256) {
+        a.tiles_q = (a.nq + 255) / 256;
+        a.tiles_p = (a.np + 255) / 256;
+        const size_t each = static_cast<size_t>(a.tiles_q) * a.tiles_p;
+        return launch_tiles(product_large<E, O, true, true, true>, each * a.experts, 512, stream, a);
+    }
+    return run_product_grad<E, O, Middle, false>(a, stream);
 }
 
 }  // namespace hr
