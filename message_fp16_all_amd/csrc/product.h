@@ -269,13 +269,13 @@ __device__ __forceinline__ u32x4 any_unit(const char *p, int left) {
 }
 
 // Expert e's rows, whatever the offsets hold: inside 0 .. rows, first <= last.
-__device__ __forceinline__ void segment(const ProductArgs &a, int e, uint32_t &first, uint32_t &last) {
-    if (a.offsets == nullptr) {
+__device__ __forceinline__ void segment(const int32_t *offsets, uint32_t all, int e, uint32_t &first, uint32_t &last) {
+    if (offsets == nullptr) {
         first = 0;
-        last = a.rows;
+        last = all;
         return;
     }
-    const int lo = a.offsets[e], hi = a.offsets[e + 1], rows = static_cast<int>(a.rows);
+    const int lo = offsets[e], hi = offsets[e + 1], rows = static_cast<int>(all);
     first = lo < 0 ? 0 : lo > rows ? rows : lo;
     last = hi < static_cast<int>(first) ? first : hi > rows ? rows : hi;
 }
@@ -311,7 +311,7 @@ __device__ __forceinline__ Tile product_tile(const ProductArgs &a, uint32_t grou
     uint32_t mine = 0;
     for (int e = lane; e < a.experts; e += kWave) {
         uint32_t lo, hi;
-        segment(a, e, lo, hi);
+        segment(a.offsets, a.rows, e, lo, hi);
         mine += (hi - lo + BQ - 1) / BQ;
     }
     const uint32_t tiles = reduce_lanes<64>(mine, [](uint32_t x, uint32_t y) { return x + y; }) * a.tiles_p;
@@ -320,7 +320,7 @@ __device__ __forceinline__ Tile product_tile(const ProductArgs &a, uint32_t grou
     if (!t.there) return t;
     for (int e0 = 0; e0 < a.experts; e0 += kWave) {
         uint32_t lo = 0, hi = 0;
-        if (e0 + lane < a.experts) segment(a, e0 + lane, lo, hi);
+        if (e0 + lane < a.experts) segment(a.offsets, a.rows, e0 + lane, lo, hi);
         const uint32_t n = (hi - lo + BQ - 1) / BQ * a.tiles_p;
         uint32_t upto = n;
 #pragma unroll
@@ -353,7 +353,7 @@ __device__ __forceinline__ Tile gradient_tile(const ProductArgs &a, uint32_t gro
     t.expert = static_cast<int>(tile / each);
     in_bands(tile % each, a.tiles_q, a.tiles_p, t.q, t.p);
     uint32_t lo, hi;
-    segment(a, t.expert, lo, hi);
+    segment(a.offsets, a.rows, t.expert, lo, hi);
     t.first = __builtin_amdgcn_readfirstlane(lo);
     t.last = __builtin_amdgcn_readfirstlane(hi);
     return t;
@@ -362,25 +362,44 @@ __device__ __forceinline__ Tile gradient_tile(const ProductArgs &a, uint32_t gro
 template <class O>
 constexpr int kOut = __is_same(O, float) ? 4 : 2;       // bytes
 
-// A wave's sums to the tile's rows at `out`: operand j of Q is its rows q(j) ..
-// q(j) + 15, the wave's first value of P is p0; nq rows and np values are there.
-// A lane holds row q(j) + lane % 16, and per operand of P four adjacent values
-// (laced: 16 of four operands).
+// The same value, of which the compiler knows nothing: what is computed from it
+// is computed where it stands, and held in no register before.
+__device__ __forceinline__ uint32_t here_only(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Registers f0 .. f3 of the lanes 16 g .. 16 g + 15 become registers g0 .. g3 of
+// the lanes 16 f ..: a transposition of four registers and four groups of lanes.
+__device__ __forceinline__ void exchange4(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+    const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+    const auto ab = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
+    const auto cd = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
+    a = ab[0], b = ab[1], c = cd[0], d = cd[1];
+}
+
+// A wave's sums to the tile's rows at `out`: operand j of Q is its rows q_of(j) ..
+// q_of(j) + 15, the wave's first value of P is p0; nq rows and np values are there.
+// A lane holds row q_of(j) + lane % 16, and per operand of P four adjacent values:
+// laced, 16 of four operands; in 16 bits made so (stores of 8 bytes to rows 32
+// bytes long each took the gradient of 16384 x 4096 x 4096 from 282 us of
+// storing to ...).
 template <class O, bool LACED, int FP, int FQ, class Q>
 __device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out, size_t stride, Q q_of, int p0, int nq,
-                                           int np, uint32_t lane) {
-    constexpr int OB = kOut<O>, RUN = LACED ? 4 : 1;            // RUN: operands whose values are adjacent
+                                           int np, uint32_t lane_) {
+    const uint32_t lane = here_only(lane_);
+    constexpr int OB = kOut<O>, RUN = LACED || (OB == 2 && FP % 4 == 0) ? 4 : 1;    // operands side by side
     const int g = lane >> 4;
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
         const int q = q_of(j) + (lane & 15);
-        if (q >= nq) continue;
         char *row = out + q * stride;
 #pragma unroll
         for (int i = 0; i < FP; i += RUN) {
-            const int p = p0 + (LACED ? 16 * i + 16 * g : 16 * i + 4 * g);
-            if (p >= np) continue;
+            const int p = p0 + 16 * i + (RUN == 4 ? 16 * g : 4 * g);
             if constexpr (OB == 4) {
+                if (q >= nq) continue;
 #pragma unroll
                 for (int r = 0; r < RUN; ++r) {
                     if (p + 4 * r + 4 <= np) {
@@ -392,24 +411,36 @@ __device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out
                                 *reinterpret_cast<float *>(row + (p + 4 * r + v) * 4) = sum[i + r][j][v];
                     }
                 }
-            } else if (p + 4 * RUN <= np) {
+            } else {
                 u32x2 v[RUN];
 #pragma unroll
                 for (int r = 0; r < RUN; ++r) v[r] = narrow4<O>(sum[i + r][j]);
-                if constexpr (RUN == 4) {
-                    store_vec<false>(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, row + p * 2);
-                    store_vec<false>(u32x4{v[2].x, v[2].y, v[3].x, v[3].y}, row + p * 2 + 16);
-                } else {
-                    *reinterpret_cast<u32x2_row *>(row + p * 2) = v[0];
+                if constexpr (RUN == 4 && !LACED) {
+                    uint32_t lo[4], hi[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) lo[r] = v[r].x, hi[r] = v[r].y;
+                    exchange4(lo[0], lo[1], lo[2], lo[3]);
+                    exchange4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = u32x2{lo[r], hi[r]};
                 }
-            } else {
+                if (q >= nq) continue;
+                if (p + 4 * RUN <= np) {
+                    if constexpr (RUN == 4) {
+                        store_vec<false>(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, row + p * 2);
+                        store_vec<false>(u32x4{v[2].x, v[2].y, v[3].x, v[3].y}, row + p * 2 + 16);
+                    } else {
+                        *reinterpret_cast<u32x2_row *>(row + p * 2) = v[0];
+                    }
+                } else {
 #pragma unroll
-                for (int r = 0; r < RUN; ++r)
+                    for (int r = 0; r < RUN; ++r)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (p + 4 * r + v < np)
-                            *reinterpret_cast<uint16_t *>(row + (p + 4 * r + v) * 2) =
-                                Wide<O>::narrow1(sum[i + r][j][v]);
+                        for (int e = 0; e < 4; ++e)
+                            if (p + 4 * r + e < np)
+                                *reinterpret_cast<uint16_t *>(row + (p + 4 * r + e) * 2) =
+                                    static_cast<uint16_t>(v[r][e / 2] >> (16 * (e & 1)));
+                }
             }
         }
     }
@@ -698,6 +729,9 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
 // later.  Every turn of a wave issues the same number of loads, the last stages'
 // from nowhere, so that the turns are straight code and the waits' counts fixed.
 // (A tile of at most 128 rows takes one turn per stage, and has three buffers.)
+// (Tiles one after the other: a workgroup has a compute unit to itself.  The next
+// tile's first loads go out before this one's sums are stored, and the stores
+// are waited for a stage later.)
 template <class E, class O, bool QA, bool PA, bool GRAD>
 __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     constexpr int SIZE = kBytes<E>, BQ = 256, BP = 256, H = 128, FP = 4, FH = 4;
@@ -706,49 +740,82 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     using PanelP = Panel<SIZE, BP, PA, LACED>;
     constexpr int CK = PanelP::kC;
     constexpr uint32_t QB = PanelQ::kBytesAll, PB = PanelP::kBytesAll;      // 16 and 32 KB
-    constexpr uint32_t kScales = 3 * (PB + QB);
+    constexpr uint32_t kScales = 3 * (PB + QB), kTable = kScales + (SCALED ? 4 * BQ * 4 : 0);
     constexpr int D0 = 6 + SCALED, D1 = 2;                                  // a wave's loads for the turns
-    __shared__ __align__(1024) char lds[kScales + (SCALED ? 4 * BQ * 4 : 0)];
+    constexpr int STORES = kOut<O> == 4 ? FP * FH : FH * 2;                 // of a wave and turn, full tile
+    // (and the segments' first rows, and their tiles counted up)
+    __shared__ __align__(1024) char lds[kTable + (GRAD ? 0 : (2 * HR_EXPERTS_MAX + 1) * 4)];
 
-    const Tile tile = GRAD ? gradient_tile(a, blockIdx.x) : product_tile<BQ>(a, blockIdx.x);
-    if (!tile.there) return;
     const uint32_t lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const bool second = wave >= 4;
     const int wq = wave & 1, wp = wave >> 1;
-
-    const int q0 = tile.q * BQ, p0 = tile.p * BP;
-    const int nq = GRAD ? a.nq - q0 : static_cast<int>(tile.last - tile.first) - q0;
-    const int np = a.np - p0;
-    const int nc = GRAD ? static_cast<int>(tile.last - tile.first) : a.nc;
-    const int stages = (nc + CK - 1) / CK;
-    const char *qs = a.q, *ps = a.p;
-    if constexpr (GRAD) {
-        qs += tile.first * a.q_stride + static_cast<size_t>(q0) * SIZE;
-        ps += tile.first * a.p_stride + static_cast<size_t>(p0) * SIZE;
-    } else {
-        qs += (static_cast<size_t>(tile.first) + q0) * a.q_stride;
-        ps += tile.expert * a.p_expert_stride + (PA ? static_cast<size_t>(p0) * SIZE : p0 * a.p_stride);
-    }
-    const size_t q_step = QA ? CK * a.q_stride : 128, p_step = PA ? CK * a.p_stride : 128;
-    const float *xs = nullptr, *ws = nullptr;
-    if constexpr (SCALED) {
-        xs = a.q_scales + (static_cast<size_t>(tile.first) + q0) * a.q_scales_stride;
-        const int block = (p0 + wp * 64) / 128, last = (a.np - 1) / 128;
-        ws = a.p_scales + tile.expert * a.scales_expert + (block < last ? block : last) * a.scales_p;
-    }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(HR_LDS char *)lds;
+    const uint32_t firsts = lds0 + kTable, counts = firsts + (HR_EXPERTS_MAX + 1) * 4;
 
+    // the arguments, read again where a tile begins: they would fill the scalar
+    // registers all the time
+    typedef const __attribute__((address_space(4))) ProductArgs Arguments;
+    const auto args = [] {
+        Arguments *p = (Arguments *)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(p));
+        return p;
+    };
+    uint32_t tiles;
+    if constexpr (GRAD) {
+        tiles = static_cast<uint32_t>(a.tiles_q) * a.tiles_p * a.experts;
+    } else {
+        for (int e = threadIdx.x; e <= a.experts; e += 512) {
+            const int at = a.offsets != nullptr ? a.offsets[e] : e == 0 ? 0 : static_cast<int>(a.rows);
+            const int rows = static_cast<int>(a.rows);
+            *reinterpret_cast<HR_LDS int *>(firsts + e * 4) = at < 0 ? 0 : at > rows ? rows : at;
+        }
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t before = 0;
+            for (int e = lane; e - static_cast<int>(lane) < a.experts; e += kWave) {
+                uint32_t n = 0;
+                if (e < a.experts) {
+                    const int lo = lds_read<int>(firsts + e * 4), hi = lds_read<int>(firsts + e * 4 + 4);
+                    n = hi > lo ? (hi - lo + BQ - 1) / BQ * a.tiles_p : 0;
+                }
+#pragma unroll
+                for (int d = 1; d < kWave; d *= 2) {
+                    const uint32_t v = __shfl_up(n, d);
+                    if (static_cast<int>(lane) >= d) n += v;
+                }
+                if (e < a.experts) *reinterpret_cast<HR_LDS uint32_t *>(counts + e * 4) = before + n;
+                before += __builtin_amdgcn_readlane(n, kWave - 1);
+            }
+        }
+        __syncthreads();
+        tiles = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(counts + (a.experts - 1) * 4));
+    }
+    // this die's run of tiles, and this workgroup's in it
+    const uint32_t each = (tiles + 7) / 8, stride = gridDim.x / 8;
+    uint32_t t = blockIdx.x % 8 * each + blockIdx.x / 8;
+    const uint32_t end = (blockIdx.x % 8 + 1) * each < tiles ? (blockIdx.x % 8 + 1) * each : tiles;
+    if (t >= end) return;
+
+    // the tile's place: its part of the operands, of out, and what is there of it
+    const char *qs, *ps;
+    char *out;
+    const float *xs = nullptr, *ws = nullptr;
+    int nq, np, nc, stages;
+    const size_t q_step = QA ? CK * a.q_stride : 128, p_step = PA ? CK * a.p_stride : 128;
+    uint32_t off_p[4], off_q[4], off_s = kNowhere;
+    int e0 = 0;                         // experts before have no tile left
     // offsets of a wave's loads: P, and the two panels of Q (c values of the stage
     // left; the last stage's are trimmed before its loads go out)
-    uint32_t off_p[4], off_q[4], off_s = kNowhere;
     const auto offsets = [&](int c) {
+        const uint32_t l = here_only(lane);
+        const auto &a = *args();
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             uint32_t row, unit;
-            PanelP::source(wave * 4 + d, lane, row, unit);
+            PanelP::source(wave * 4 + d, l, row, unit);
             off_p[d] = PanelP::there(row, unit, np, c) ? static_cast<uint32_t>(row * a.p_stride) + unit * 16 : kNowhere;
-            PanelQ::source(wave * 2 + (d & 1), lane, row, unit);
+            PanelQ::source(wave * 2 + (d & 1), l, row, unit);
             if constexpr (QA)
                 unit += (d >> 1) * H / PanelQ::kUnit;
             else
@@ -756,11 +823,60 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
             off_q[d] = PanelQ::there(row, unit, nq, c) ? static_cast<uint32_t>(row * a.q_stride) + unit * 16 : kNowhere;
         }
     };
-    offsets(nc < CK ? nc : CK);
-    if constexpr (SCALED) {
-        const int row = wave % 4 * 64 + lane;                   // (either set brings them all)
-        if (row < nq) off_s = static_cast<uint32_t>(row * a.q_scales_stride * 4);
-    }
+    const auto place = [&] {
+        const auto &a = *args();
+        int expert, tq, tp;
+        uint32_t first, last;
+        if constexpr (GRAD) {
+            const uint32_t per = static_cast<uint32_t>(a.tiles_q) * a.tiles_p;
+            expert = static_cast<int>(t / per);
+            in_bands(t % per, a.tiles_q, a.tiles_p, tq, tp);
+            uint32_t lo, hi;
+            segment(a.offsets, a.rows, expert, lo, hi);
+            first = __builtin_amdgcn_readfirstlane(lo);
+            last = __builtin_amdgcn_readfirstlane(hi);
+        } else {
+            uint32_t upto;
+            uint64_t past;
+            for (;; e0 += kWave) {
+                // (the last count is past every tile)
+                const int e = e0 + static_cast<int>(lane) < a.experts ? e0 + static_cast<int>(lane) : a.experts - 1;
+                upto = lds_read<uint32_t>(counts + e * 4);
+                past = __ballot(t < upto);
+                if (past != 0) break;
+            }
+            expert = __builtin_amdgcn_readfirstlane(e0 + __builtin_ctzll(past));
+            const int lo = __builtin_amdgcn_readfirstlane(lds_read<int>(firsts + expert * 4));
+            const int hi = __builtin_amdgcn_readfirstlane(lds_read<int>(firsts + expert * 4 + 4));
+            first = lo, last = hi;
+            const uint32_t high = (last - first + BQ - 1) / BQ;
+            const uint32_t all = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(counts + expert * 4));
+            in_bands(t - (all - high * a.tiles_p), high, a.tiles_p, tq, tp);
+        }
+        const int q0 = tq * BQ, p0 = tp * BP;
+        nq = GRAD ? a.nq - q0 : static_cast<int>(last - first) - q0;
+        np = a.np - p0;
+        nc = GRAD ? static_cast<int>(last - first) : a.nc;
+        stages = (nc + CK - 1) / CK;
+        if constexpr (GRAD) {
+            qs = a.q + first * a.q_stride + static_cast<size_t>(q0) * SIZE;
+            ps = a.p + first * a.p_stride + static_cast<size_t>(p0) * SIZE;
+            out = a.out + expert * a.out_expert_stride + static_cast<size_t>(q0) * a.out_stride;
+        } else {
+            qs = a.q + (static_cast<size_t>(first) + q0) * a.q_stride;
+            ps = a.p + expert * a.p_expert_stride + (PA ? static_cast<size_t>(p0) * SIZE : p0 * a.p_stride);
+            out = a.out + (static_cast<size_t>(first) + q0) * a.out_stride;
+        }
+        out += static_cast<size_t>(p0) * kOut<O>;
+        offsets(nc < CK ? nc : CK);
+        if constexpr (SCALED) {
+            xs = a.q_scales + (static_cast<size_t>(first) + q0) * a.q_scales_stride;
+            const int block = (p0 + wp * 64) / 128, most = (a.np - 1) / 128;
+            ws = a.p_scales + expert * a.scales_expert + (block < most ? block : most) * a.scales_p;
+            const int row = wave % 4 * 64 + lane;               // (either set brings them all)
+            off_s = row < nq ? static_cast<uint32_t>(row * a.q_scales_stride * 4) : kNowhere;
+        }
+    };
     const auto trim = [&](int s) {
         if (s == stages - 1 && s > 0 && nc % CK != 0) offsets(nc % CK);
     };
@@ -813,21 +929,15 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
             }
         }
     };
-    // a turn's instructions for one panel of Q, with the turn's loads between them
+    // a turn's instructions for one panel of Q; e4m3: with the turn's loads between them
     const auto multiply = [&](f32x4 (&sum)[FP][FH], auto loads_, auto load) {
         constexpr int loads = decltype(loads_)::value;
         __builtin_amdgcn_s_setprio(1);
         if constexpr (!SCALED) {
-            constexpr int N = 2 * FP * FH, EACH = N / (loads + 1);
 #pragma unroll
-            for (int t = 0; t < N; ++t) {
+            for (int t = 0; t < 2 * FP * FH; ++t) {
                 const int half = t / (FP * FH), j = t / FP % FH, i = t % FP;
                 sum[i][j] = mfma16<E>(w[half][i], x[half][j], sum[i][j]);
-                if (t % EACH == EACH - 1 && t / EACH < loads) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    load(t / EACH);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
             }
         } else {
             // (a part is scaled two instructions later, when it is there)
@@ -854,95 +964,127 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
             for (int j = 0; j < FH; ++j) asm volatile("" : "+v"(sum[i][j]));
         __builtin_amdgcn_s_setprio(0);
     };
-    char *out = a.out + (GRAD ? tile.expert * a.out_expert_stride + static_cast<size_t>(q0) * a.out_stride
-                              : (static_cast<size_t>(tile.first) + q0) * a.out_stride);
-    out += static_cast<size_t>(p0) * kOut<O>;
     const auto clear = [](f32x4 (&sum)[FP][FH]) {
 #pragma unroll
         for (int i = 0; i < FP; ++i)
 #pragma unroll
             for (int j = 0; j < FH; ++j) sum[i][j] = f32x4{0, 0, 0, 0};
     };
-    const auto store = [&](const f32x4 (&sum)[FP][FH], int turn) {
-        store_sums<O, LACED, FP, FH>(sum, out, a.out_stride, [&](int j) { return turn * H + wq * 64 + 16 * j; }, wp * 64,
-                                     nq, np, lane);
+    // 16 bits: a turn's loads go out after its reads
+    const auto reading = [&](auto loads_, auto load) {
+        if constexpr (!SCALED) {
+#pragma unroll
+            for (int d = 0; d < decltype(loads_)::value; ++d) load(d);
+        }
     };
-
     const std::integral_constant<int, D0> d0;
     const std::integral_constant<int, D1> d1;
-    f32x4 sum0[FP][FH];
-    clear(sum0);
-    if constexpr (SCALED) block_of(0);
-    if (nq <= H) {
-        //     turn          2 s    2 s + 1   2 s + 2   2 s + 3
-        //     first set     read   multiply  read      multiply
-        //     second set           read      multiply  read
+    // the loads before a tile's first turns
+    const auto begin = [&] {
+        if constexpr (SCALED) block_of(0);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            trim(s);
+        for (int d = 0; d < D0; ++d) bring0(0, 0, d);
+        if (nq > H) {
 #pragma unroll
-            for (int d = 0; d < D0; ++d) bring0(s, s, d);
+            for (int d = 0; d < D1; ++d) bring1(0, 0, d);
         }
-        landed<D0>();
-        change();
-        if (second) change();
-        int b = 0;
-        for (int s = 0; s < stages; ++s) {
-            read_p(lds0 + b * PB);
-            read_q(s, 0, lds0 + 3 * PB + b * QB);
-            if (second) landed<0>();                            // stage s + 1
-            read_done();
-            change();
-            trim(s + 2);
-            if constexpr (SCALED) block_of(s + 1);
-            const int to = b == 0 ? 2 : b - 1;
-            multiply(sum0, d0, [&](int d) { bring0(s + 2, to, d); });
-            if (!second) landed<D0>();                          // stage s + 1
-            change();
-            b = b == 2 ? 0 : b + 1;
-        }
-        if (!second) change();
-        landed<0>();            // (nothing may reach this LDS when it is another's)
-        store(sum0, 0);
-        return;
-    }
+        trim(1);
+#pragma unroll
+        for (int d = 0; d < D0; ++d) bring0(1, 1, d);
+    };
 
-#pragma unroll
-    for (int d = 0; d < D0; ++d) bring0(0, 0, d);
-#pragma unroll
-    for (int d = 0; d < D1; ++d) bring1(0, 0, d);
-    trim(1);
-#pragma unroll
-    for (int d = 0; d < D0; ++d) bring0(1, 1, d);
-    landed<D0 + D1>();          // stage 0, for its first turn
-    change();
-    if (second) change();
-    f32x4 sum1[FP][FH];
-    clear(sum1);
-    for (int s = 0; s < stages; ++s) {
-        const int b = s & 1;
-        read_p(lds0 + b * PB);
-        read_q(s, 0, lds0 + 3 * PB + b * QB);
-        if (second) landed<D0>();                               // stage s, second turn
-        read_done();
-        change();
-        multiply(sum0, d1, [&](int d) { bring1(s + 1, b ^ 1, d); });
-        if (!second) landed<D0 + D1>();                         // the same
-        change();
-        read_q(s, 1, lds0 + 2 * PB + b * QB);
-        if (second) landed<D1>();                               // stage s + 1, first turn
-        read_done();
-        change();
-        trim(s + 2);
-        if constexpr (SCALED) block_of(s + 1);
-        multiply(sum1, d0, [&](int d) { bring0(s + 2, b, d); });
-        if (!second) landed<D0 + D1>();                         // the same
-        change();
+    f32x4 sum0[FP][FH], sum1[FP][FH];
+    place();
+    begin();
+    int stored = 0;                     // stores that are behind the first loads
+    for (;;) {
+        // all but the last n loads, and the last tile's stores, which a wave issued
+        // after its first loads
+        const auto wait = [&](auto n_, int s) {
+            constexpr int n = decltype(n_)::value;
+            if (s > 0 || stored == 0)
+                landed<n>();
+            else if (stored == STORES)
+                landed<n + STORES>();
+            else
+                landed<n + 2 * STORES>();
+        };
+        clear(sum0);
+        if (nq > H) {
+            clear(sum1);
+            wait(std::integral_constant<int, D0 + D1>(), 0);    // stage 0, for its first turn
+            change();
+            if (second) change();
+            for (int s = 0; s < stages; ++s) {
+                const int b = s & 1;
+                read_p(lds0 + b * PB);
+                read_q(s, 0, lds0 + 3 * PB + b * QB);
+                const auto last = [&](int d) { bring1(s + 1, b ^ 1, d); };
+                reading(d1, last);
+                if (second) wait(std::integral_constant<int, SCALED ? D0 : D0 + D1>(), s);  // stage s, second turn
+                read_done();
+                change();
+                multiply(sum0, d1, last);
+                if (!second) wait(std::integral_constant<int, D0 + D1>(), s);               // the same
+                change();
+                read_q(s, 1, lds0 + 2 * PB + b * QB);
+                trim(s + 2);
+                const auto first = [&](int d) { bring0(s + 2, b, d); };
+                reading(d0, first);
+                if (second) wait(std::integral_constant<int, SCALED ? D1 : D0 + D1>(), s);  // stage s + 1, first turn
+                read_done();
+                change();
+                if constexpr (SCALED) block_of(s + 1);
+                multiply(sum1, d0, first);
+                if (!second) wait(std::integral_constant<int, D0 + D1>(), s);               // the same
+                change();
+            }
+            if (!second) change();
+        } else {
+            //     turn          2 s    2 s + 1   2 s + 2   2 s + 3
+            //     first set     read   multiply  read      multiply
+            //     second set           read      multiply  read
+            wait(d0, 0);
+            change();
+            if (second) change();
+            int b = 0;
+            for (int s = 0; s < stages; ++s) {
+                read_p(lds0 + b * PB);
+                read_q(s, 0, lds0 + 3 * PB + b * QB);
+                trim(s + 2);
+                const int to = b == 0 ? 2 : b - 1;
+                const auto first = [&](int d) { bring0(s + 2, to, d); };
+                reading(d0, first);
+                if (second) wait(std::integral_constant<int, SCALED ? 0 : D0>(), s);        // stage s + 1
+                read_done();
+                change();
+                if constexpr (SCALED) block_of(s + 1);
+                multiply(sum0, d0, first);
+                if (!second) wait(d0, s);                                                   // stage s + 1
+                change();
+                b = b == 2 ? 0 : b + 1;
+            }
+            if (!second) change();
+        }
+        landed<0>();        // (loads from nowhere; after the last tile this LDS is another's)
+        char *const to = out;
+        const int rows = nq, width = np;
+        t += stride;
+        const bool more = t < end;
+        if (more) {
+            place();
+            begin();
+        }
+        store_sums<O, LACED, FP, FH>(sum0, to, args()->out_stride, [&](int j) { return wq * 64 + 16 * j; }, wp * 64, rows,
+                                     width, lane);
+        if (rows > H)
+            store_sums<O, LACED, FP, FH>(sum1, to, args()->out_stride, [&](int j) { return H + wq * 64 + 16 * j; }, wp * 64,
+                                         rows, width, lane);
+        if (!more) break;
+        // a partial tile's stores are not counted, but waited for
+        stored = width >= BP && (rows == H || rows >= BQ) ? (rows > H ? 2 * STORES : STORES) : 0;
+        if (stored == 0) landed<0>();
     }
-    if (!second) change();
-    landed<0>();
-    store(sum0, 0);
-    store(sum1, 1);
 }
 
 }  // namespace hr

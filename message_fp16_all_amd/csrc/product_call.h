@@ -141,6 +141,16 @@ hr_status launch_tiles(K kernel, size_t tiles, int threads, hr_stream_t stream, 
     return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
+// One workgroup of large tiles per compute unit, as many to each of the eight dies.
+template <class K>
+hr_status launch_large(K kernel, size_t tiles, hr_stream_t stream, const ProductArgs &a) {
+    if (tiles >= size_t(1) << 31) return HR_ERR_TOO_LARGE;
+    int device = 0, units = 0;
+    if (stream_device(stream, &device) != hipSuccess || device_cu_count(device, &units) != hipSuccess) return HR_ERR_HIP;
+    const size_t most = units < 8 ? 8 : static_cast<size_t>(units) / 8 * 8;
+    return launch_tiles(kernel, tiles < most ? tiles : most, 512, stream, a);
+}
+
 // Tiles that segments of so many rows in all take at most.
 inline size_t tiles_of(size_t rows, int experts, size_t high) {
     const size_t used = static_cast<size_t>(experts) < rows ? experts : rows;
@@ -166,8 +176,8 @@ hr_status launch_product(ProductArgs &a, bool across, bool any, hr_stream_t stre
     if (each >= 256) {
         a.tiles_p = (a.np + 255) / 256;
         const size_t tiles = tiles_of(a.rows, a.experts, 256) * a.tiles_p;
-        return across ? launch_tiles(product_large<E, O, false, true, false>, tiles, 512, stream, a)
-                      : launch_tiles(product_large<E, O, false, false, false>, tiles, 512, stream, a);
+        return across ? launch_large(product_large<E, O, false, true, false>, tiles, stream, a)
+                      : launch_large(product_large<E, O, false, false, false>, tiles, stream, a);
     }
     if (each >= 32)
         return across ? run_product<E, O, Middle, true, false>(a, stream)
@@ -191,7 +201,7 @@ hr_status launch_product_grad(ProductArgs &a, bool any, hr_stream_t stream) {
         a.tiles_q = (a.nq + 255) / 256;
         a.tiles_p = (a.np + 255) / 256;
         const size_t each = static_cast<size_t>(a.tiles_q) * a.tiles_p;
-        return launch_tiles(product_large<E, O, true, true, true>, each * a.experts, 512, stream, a);
+        return launch_large(product_large<E, O, true, true, true>, each * a.experts, stream, a);
     }
     return run_product_grad<E, O, Middle, false>(a, stream);
 }
