@@ -72,6 +72,7 @@ struct ProductArgs {
     int experts;
     int nq, np, nc;                     // extents of q (gradient), p and c (product)
     int tiles_q, tiles_p;               // tiles_q: of the gradient
+    int stream;                         // out passes the caches by
 };
 
 // One stage's place in a lane's address: 16 bytes from `offset` past the
@@ -383,9 +384,8 @@ __device__ __forceinline__ void exchange4(uint32_t &a, uint32_t &b, uint32_t &c,
 // q_of(j) + 15, the wave's first value of P is p0; nq rows and np values are there.
 // A lane holds row q_of(j) + lane % 16, and per operand of P four adjacent values:
 // laced, 16 of four operands; in 16 bits made so (stores of 8 bytes to rows 32
-// bytes long each took the gradient of 16384 x 4096 x 4096 from 282 us of
-// storing to ...).
-template <class O, bool LACED, int FP, int FQ, class Q>
+// bytes long each are slower).
+template <class O, bool LACED, bool NT, int FP, int FQ, class Q>
 __device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out, size_t stride, Q q_of, int p0, int nq,
                                            int np, uint32_t lane_) {
     const uint32_t lane = here_only(lane_);
@@ -403,7 +403,11 @@ __device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out
 #pragma unroll
                 for (int r = 0; r < RUN; ++r) {
                     if (p + 4 * r + 4 <= np) {
-                        *reinterpret_cast<f32x4_row *>(row + (p + 4 * r) * 4) = sum[i + r][j];
+                        f32x4_row *to = reinterpret_cast<f32x4_row *>(row + (p + 4 * r) * 4);
+                        if constexpr (NT)
+                            __builtin_nontemporal_store(sum[i + r][j], to);
+                        else
+                            *to = sum[i + r][j];
                     } else {
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
@@ -427,8 +431,9 @@ __device__ __forceinline__ void store_sums(const f32x4 (&sum)[FP][FQ], char *out
                 if (q >= nq) continue;
                 if (p + 4 * RUN <= np) {
                     if constexpr (RUN == 4) {
-                        store_vec<false>(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, row + p * 2);
-                        store_vec<false>(u32x4{v[2].x, v[2].y, v[3].x, v[3].y}, row + p * 2 + 16);
+                        const u32x4 v0 = {v[0].x, v[0].y, v[1].x, v[1].y}, v1 = {v[2].x, v[2].y, v[3].x, v[3].y};
+                        store_vec<NT>(v0, row + p * 2);
+                        store_vec<NT>(v1, row + p * 2 + 16);
                     } else {
                         *reinterpret_cast<u32x2_row *>(row + p * 2) = v[0];
                     }
@@ -704,7 +709,7 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
 
     char *out = a.out + (GRAD ? tile.expert * a.out_expert_stride + static_cast<size_t>(q0) * a.out_stride
                               : (static_cast<size_t>(tile.first) + q0) * a.out_stride);
-    store_sums<O, LACED, FP, FQ>(sum, out + static_cast<size_t>(p0) * kOut<O>, a.out_stride,
+    store_sums<O, LACED, false, FP, FQ>(sum, out + static_cast<size_t>(p0) * kOut<O>, a.out_stride,
                                  [&](int j) { return wq * PQ + 16 * j; }, wp * PP, nq, np, lane);
 }
 
@@ -791,10 +796,13 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         __syncthreads();
         tiles = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(counts + (a.experts - 1) * 4));
     }
-    // this die's run of tiles, and this workgroup's in it
-    const uint32_t each = (tiles + 7) / 8, stride = gridDim.x / 8;
-    uint32_t t = blockIdx.x % 8 * each + blockIdx.x / 8;
-    const uint32_t end = (blockIdx.x % 8 + 1) * each < tiles ? (blockIdx.x % 8 + 1) * each : tiles;
+    // this die's run of tiles, which its workgroups take in rounds; their places in
+    // a round move on by one every second round, so that tiles of half the work
+    // (each second, third or fourth one of an expert) come to all of them (384 rows
+    // for each of 128 experts, 4096 -> 2048: 892 -> 822 us)
+    const uint32_t each = (tiles + 7) / 8, places = gridDim.x / 8, die = blockIdx.x % 8;
+    const uint32_t end = (die + 1) * each < tiles ? (die + 1) * each : tiles;
+    uint32_t round = 0, t = die * each + blockIdx.x / 8;
     if (t >= end) return;
 
     // the tile's place: its part of the operands, of out, and what is there of it
@@ -1069,17 +1077,26 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         landed<0>();        // (loads from nowhere; after the last tile this LDS is another's)
         char *const to = out;
         const int rows = nq, width = np;
-        t += stride;
+        ++round;
+        t = die * each + round * places + (blockIdx.x / 8 + round / 2) % places;
         const bool more = t < end;
         if (more) {
             place();
             begin();
         }
-        store_sums<O, LACED, FP, FH>(sum0, to, args()->out_stride, [&](int j) { return wq * 64 + 16 * j; }, wp * 64, rows,
-                                     width, lane);
-        if (rows > H)
-            store_sums<O, LACED, FP, FH>(sum1, to, args()->out_stride, [&](int j) { return H + wq * 64 + 16 * j; }, wp * 64,
-                                         rows, width, lane);
+        const size_t out_stride = args()->out_stride;
+        const auto store = [&](auto nt) {
+            constexpr bool NT = decltype(nt)::value;
+            store_sums<O, LACED, NT, FP, FH>(sum0, to, out_stride, [&](int j) { return wq * 64 + 16 * j; }, wp * 64, rows,
+                                             width, lane);
+            if (rows > H)
+                store_sums<O, LACED, NT, FP, FH>(sum1, to, out_stride, [&](int j) { return H + wq * 64 + 16 * j; },
+                                                 wp * 64, rows, width, lane);
+        };
+        if (GRAD && args()->stream)
+            store(std::integral_constant<bool, GRAD>());
+        else
+            store(std::false_type());
         if (!more) break;
         // a partial tile's stores are not counted, but waited for
         stored = width >= BP && (rows == H || rows >= BQ) ? (rows > H ? 2 * STORES : STORES) : 0;

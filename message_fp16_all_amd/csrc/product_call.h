@@ -126,6 +126,8 @@ inline hr_status product_grad_check(const hr_experts_product_grad_args *q, Produ
     a.experts = q->experts;
     a.nq = static_cast<int>(q->n);
     a.np = static_cast<int>(q->k);
+    // (as the expert rows': dw of 1.07 GB 816 us, past the caches 742; of 134 MB 35 and 47)
+    a.stream = w.region.rows * w.region.width >= size_t(1) << 28;
     any = !(units16(q->dy) && units16(q->x) && a.q_stride % 16 == 0 && a.p_stride % 16 == 0 && q->n % 8 == 0 &&
             q->k % 8 == 0);
     return HR_OK;
