@@ -147,7 +147,7 @@ struct Panel {
     // across: the move of row c's slots of 32 (16-bit) or 16 (e4m3) bytes
     static constexpr int kSlot = SIZE == 2 ? 32 : 16;
     static __device__ __forceinline__ uint32_t move_across(uint32_t c) {
-        constexpr int shared = kPitch >= 256 ? 0 : kPitch == 128 ? 1 : 2;
+        constexpr int shared = kPitch >= 256 ? 0 : kPitch == 128 ? 1 : kPitch == 64 ? 2 : kPitch == 32 ? 3 : 4;
         return (SIZE == 2 ? (c & 3) | ((c >> 3) & 1) << 2 : (c & 7) | ((c >> 4) & 1) << 3) >> shared;
     }
 
@@ -468,8 +468,8 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
     constexpr int SIZE = kBytes<E>, BQ = SH::BQ, BP = SH::BP, S = SH::S;
     constexpr int PQ = BQ / SH::WQ, PP = BP / SH::WP;           // a wave's part of the tile
     constexpr int FQ = PQ / 16, FP = PP / 16;
-    constexpr bool LACED = !PA;                                 // P's rows interleaved by four operands
-    static_assert(PQ % 16 == 0 && PP % 16 == 0 && (!LACED || PP % 64 == 0), "whole operands");
+    constexpr bool LACED = !PA && PP % 64 == 0;                 // P's rows interleaved by four operands
+    static_assert(PQ % 16 == 0 && PP % 16 == 0, "whole operands");
     using PanelQ = Panel<SIZE, BQ, QA, false>;
     using PanelP = Panel<SIZE, BP, PA, LACED>;
     constexpr int CK = PanelQ::kC;

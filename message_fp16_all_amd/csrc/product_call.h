@@ -160,6 +160,19 @@ inline size_t tiles_of(size_t rows, int experts, size_t high) {
     return most < rows ? most : rows;
 }
 
+// The shapes, from the largest: tile, waves over q, p and the panels of a stage,
+// stages.  Where weights are read for few rows all but the smallest come near to
+// HBM's rate, and what counts is that the GPU is full.
+typedef Shape<128, 256, 2, 4, 1, 3> Half;
+typedef Shape<128, 128, 2, 2, 1, 2, 2> Middle;
+typedef Shape<64, 128, 2, 2, 1, 3, 2> Some;
+typedef Shape<32, 128, 1, 2, 2, 3> Low;
+typedef Shape<16, 32, 1, 1, 4, 3, 2> Few;
+typedef Shape<16, 64, 1, 1, 4, 3> FewAcross;    // (32 values of a strided row are half a line)
+typedef Shape<16, 16, 1, 1, 4, 4> Tiny;
+typedef Shape<64, 64, 1, 1, 4, 2> Deep;         // the gradient of few matrices
+typedef Shape<32, 128, 1, 4, 1, 2, 2> AnyFew;
+
 template <class E, class O, class SH, bool PA, bool ANY>
 hr_status run_product(ProductArgs &a, hr_stream_t stream) {
     a.tiles_p = (a.np + SH::BP - 1) / SH::BP;
@@ -167,24 +180,43 @@ hr_status run_product(ProductArgs &a, hr_stream_t stream) {
                         SH::kThreads, stream, a);
 }
 
-typedef Shape<128, 128, 2, 2, 1, 2> Middle;
-typedef Shape<16, 64, 1, 1, 4, 2> Few;
+// The largest shape whose height fits the segments and whose tiles fill the GPU.
+// 4096 x 4096 matrices, bfloat16, us by shape (the chosen one first), one
+// matrix: 16 rows Tiny 7.2 Few 8.0; 64 Few 12.2 Low 21.4; 256 Low 22.9 Some 32.1
+// Few 39; 512 Some 33.8 Low 43 Middle 43; 1024 Some 42.8 Middle 47 Half 60; 2048
+// Middle 63.9 Half 66.0 large 78; 4096 large 98 Middle 133 Half 138.  64 matrices
+// of 2048 x 4096 and rows spread over them, on average 8: Few 157 Some 162; 16: Some
+// 174 Middle 170 Few 196; 32: Middle 175 Half 181 Some 192 Few 272; 64: Half 224
+// large 210 Middle 236; 128: Half 268 large 293; 256: large 372 Half 391.  e4m3: 8: Few
+// 86 Some 105; 16: Some 114 Middle 125; 32: Middle 125 Some 121; 64: Half 144 Some
+// 136; 128: Half 173 large 206; 256: large 255 Half 266.
+template <class E, class O, bool PA>
+hr_status pick_product(ProductArgs &a, bool any, hr_stream_t stream) {
+    const size_t each = a.rows / a.experts;
+    const auto fits = [&](size_t bq, size_t bp, size_t least_rows, size_t least_tiles) {
+        return each >= least_rows && tiles_of(a.rows, a.experts, bq) * ((a.np + bp - 1) / bp) >= least_tiles;
+    };
+    if (any)
+        return each < 24 ? run_product<E, O, AnyFew, PA, true>(a, stream) : run_product<E, O, Middle, PA, true>(a, stream);
+    if (fits(256, 256, 192, 200)) {
+        a.tiles_p = (a.np + 255) / 256;
+        return launch_large(product_large<E, O, false, PA, false>, tiles_of(a.rows, a.experts, 256) * a.tiles_p, stream, a);
+    }
+    if (fits(128, 256, 64, 320)) return run_product<E, O, Half, PA, false>(a, stream);
+    if (fits(128, 128, 20, 320)) return run_product<E, O, Middle, PA, false>(a, stream);
+    if (fits(64, 128, 12, 200)) return run_product<E, O, Some, PA, false>(a, stream);
+    if (fits(32, 128, 12, 128)) return run_product<E, O, Low, PA, false>(a, stream);
+    if constexpr (PA) {
+        return run_product<E, O, FewAcross, PA, false>(a, stream);
+    } else {
+        if (fits(16, 32, 0, 192)) return run_product<E, O, Few, PA, false>(a, stream);
+        return run_product<E, O, Tiny, PA, false>(a, stream);
+    }
+}
 
 template <class E, class O>
 hr_status launch_product(ProductArgs &a, bool across, bool any, hr_stream_t stream) {
-    if (any)
-        return across ? run_product<E, O, Middle, true, true>(a, stream) : run_product<E, O, Middle, false, true>(a, stream);
-    const size_t each = a.rows / a.experts;
-    if (each >= 256) {
-        a.tiles_p = (a.np + 255) / 256;
-        const size_t tiles = tiles_of(a.rows, a.experts, 256) * a.tiles_p;
-        return across ? launch_large(product_large<E, O, false, true, false>, tiles, stream, a)
-                      : launch_large(product_large<E, O, false, false, false>, tiles, stream, a);
-    }
-    if (each >= 32)
-        return across ? run_product<E, O, Middle, true, false>(a, stream)
-                      : run_product<E, O, Middle, false, false>(a, stream);
-    return across ? run_product<E, O, Few, true, false>(a, stream) : run_product<E, O, Few, false, false>(a, stream);
+    return across ? pick_product<E, O, true>(a, any, stream) : pick_product<E, O, false>(a, any, stream);
 }
 
 template <class E, class O, class SH, bool ANY>
@@ -199,13 +231,15 @@ hr_status run_product_grad(ProductArgs &a, hr_stream_t stream) {
 template <class E, class O>
 hr_status launch_product_grad(ProductArgs &a, bool any, hr_stream_t stream) {
     if (any) return run_product_grad<E, O, Middle, true>(a, stream);
-    if (a.nq >= 256 && a.np >= 256) {
+    const auto tiles = [&](int b) { return static_cast<size_t>((a.nq + b - 1) / b) * ((a.np + b - 1) / b) * a.experts; };
+    if (a.nq >= 192 && a.np >= 192 && tiles(256) >= 200) {
         a.tiles_q = (a.nq + 255) / 256;
         a.tiles_p = (a.np + 255) / 256;
-        const size_t each = static_cast<size_t>(a.tiles_q) * a.tiles_p;
-        return launch_large(product_large<E, O, true, true, true>, each * a.experts, stream, a);
+        if (tiles(256) >= size_t(1) << 31) return HR_ERR_TOO_LARGE;
+        return launch_large(product_large<E, O, true, true, true>, tiles(256), stream, a);
     }
-    return run_product_grad<E, O, Middle, false>(a, stream);
+    if (tiles(128) >= 320) return run_product_grad<E, O, Middle, false>(a, stream);
+    return run_product_grad<E, O, Deep, false>(a, stream);
 }
 
 }  // namespace hr
