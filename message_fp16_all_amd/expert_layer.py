@@ -10,7 +10,7 @@ hidden, 16 bits):
     logits = y @ router; weights, ids = top k           router_topk
     per rank: the picks of its experts, sorted          experts_sort
               rows gathered into that order             experts_gather
-              one product per expert                    (torch.mm)
+              every row times its expert's matrix       experts_product
               rows back, weighted and added per token   experts_combine
     x' = x + sum of the ranks' rows; y' = norm(x')      reduce_rmsnorm
 
@@ -80,12 +80,9 @@ class Layer:
         if self.channel is not None:
             self.channel.destroy()
 
-    def segments(self, rank: int):
-        """(expert, first row, row after the last) of a rank's segments that
-        hold any.  (A product over all segments in one kernel would read the
-        offsets on the GPU; one torch.mm each needs them here.)"""
-        o = self.sorts[rank][0].tolist()
-        return [(rank * self.local + i, a, b) for i, (a, b) in enumerate(zip(o, o[1:])) if b > a]
+    def experts_of(self, rank: int) -> slice:
+        """A rank's experts."""
+        return slice(rank * self.local, (rank + 1) * self.local)
 
     def forward(self, x):
         """(x', y') of the residual stream ``x``; self.codes and self.scales
@@ -99,8 +96,8 @@ class Layer:
         for r, (offsets, order, pos) in enumerate(self.sorts):
             hr.experts_sort(self.ids, offsets, order, pos, first=r * self.local, pad=PAD)
             hr.experts_gather(self.y, pos, self.sorted[r], offsets=offsets, order=order)
-            for e, a, b in self.segments(r):
-                torch.mm(self.sorted[r][a:b], w.expert[e], out=self.z[r][a:b])
+            hr.experts_product(self.sorted[r], w.expert[self.experts_of(r)], self.z[r], offsets=offsets,
+                               transposed=True)
             hr.experts_combine(self.z[r], pos, self.parts[r], weights=self.weights)
         parts = self.parts
         if self.channel is not None:
@@ -116,7 +113,7 @@ class Layer:
         import torch
         w, dt = self.w, self.y.dtype
         g = {"scale_out": torch.empty_like(w.scale_out), "scale_in": torch.empty_like(w.scale_in),
-             "expert": torch.zeros_like(w.expert)}
+             "expert": torch.empty_like(w.expert)}
         dh = torch.empty_like(self.x)
         hr.rmsnorm_grad(dy_out, self.x_out, self.rstd_out, dh, weight=w.scale_out, dresidual=dx_out,
                         dweight=g["scale_out"])
@@ -126,9 +123,9 @@ class Layer:
             dz, ds, mine = torch.empty_like(self.z[r]), torch.empty_like(self.z[r]), torch.empty_like(self.weights)
             hr.experts_combine_grad(dh, self.z[r], pos, self.weights, dz, mine, offsets=offsets, order=order)
             dweights += mine
-            for e, a, b in self.segments(r):
-                torch.mm(dz[a:b], w.expert[e].t(), out=ds[a:b])
-                torch.mm(self.sorted[r][a:b].t(), dz[a:b], out=g["expert"][e])
+            mine_w = self.experts_of(r)
+            hr.experts_product(dz, w.expert[mine_w], ds, offsets=offsets)
+            hr.experts_product_grad(self.sorted[r], dz, g["expert"][mine_w], offsets=offsets)
             dys.append(hr.experts_combine(ds, pos, torch.empty_like(self.y)))
         dlogits = torch.empty_like(self.logits)
         hr.router_topk_grad(dweights, self.weights, self.ids, dlogits, renormalize=True)

@@ -115,3 +115,81 @@ def test_act_grad(name, again, same, rows, width):
         ref = act_ref(x, width)
         within(out, ref, tol_of(dt, ref), "out")
     m.check_frames()
+
+
+@pytest.mark.parametrize("used", [0, 1, 5, 9, 12])
+def test_rows_past_the_last_segment(used):
+    m = Maker(used)
+    dt, rows, width = torch.bfloat16, 9, 264
+    at = torch.tensor([0, used // 2, used], dtype=torch.int32, device=DEV)
+    x, dy = m.normal(rows, 2 * width, dtype=dt), m.normal(rows, width, dtype=dt)
+    out, dx = m.place(rows, width, dt), m.place(rows, 2 * width, dt)
+    scales, codes = m.place(rows, 3, torch.float32), torch.full((rows, width), 7.0).to(F8).to(DEV)
+    hr.experts_act(x.to(DEV), out, offsets=at, out8=codes, scales=scales)
+    hr.experts_act_grad(dy.to(DEV), x.to(DEV), dx, offsets=at)
+    n = min(used, rows)
+    ref = act_ref(x, width)
+    within(out[:n], ref[:n], tol_of(dt, ref)[:n], "out")
+    for t in (out, dx, scales, codes):
+        assert (t[n:].float() == 7).all()
+    if n:
+        check_codes(codes[:n], scales[:n], ref[:n], 128, "act")
+        assert not (dx[:n].float() == 7).all()
+
+
+def test_not_finite():
+    """NaN and infinities stay in their values (and their group's scale)."""
+    x = torch.ones(4, 512, dtype=torch.float16)
+    x[0, 3], x[1, 200], x[2, 256 + 40], x[3, 10] = float("nan"), float("inf"), float("nan"), -float("inf")
+    out = torch.empty(4, 256, dtype=torch.float16, device=DEV)
+    codes, scales = torch.empty(4, 256, dtype=F8, device=DEV), torch.empty(4, 2, device=DEV)
+    hr.experts_act(x.to(DEV), out, out8=codes, scales=scales)
+    bad = torch.zeros(4, 256, dtype=torch.bool)
+    bad[0, 3] = bad[2, 40] = bad[3, 10] = True
+    got, s = out.cpu(), scales.cpu()
+    assert torch.equal(torch.isnan(got), bad) and got[1, 200] == float("inf")
+    assert torch.isfinite(got[~bad]).sum() == (~bad).sum() - 1
+    assert torch.equal(torch.isnan(s), torch.tensor([[True, False], [False, False], [True, False], [True, False]]))
+    assert s[1, 1] == float("inf")
+    dx = torch.empty(4, 512, dtype=torch.float16, device=DEV)
+    hr.experts_act_grad(torch.ones(4, 256, dtype=torch.float16, device=DEV), x.to(DEV), dx)
+    d = dx.cpu()
+    assert torch.isfinite(d).sum() >= d.numel() - 8
+
+
+def test_gradient_against_differences():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(3, 40, generator=g).double()
+    dy = torch.randn(3, 20, generator=g).half()
+    h = x.half()
+    dx = torch.empty(3, 40, dtype=torch.float16, device=DEV)
+    hr.experts_act_grad(dy.to(DEV), h.to(DEV), dx)
+    step = 1e-6
+    for r in range(3):
+        for c in range(40):
+            up, down = h.double().clone(), h.double().clone()
+            up[r, c] += step
+            down[r, c] -= step
+            slope = float(((act_ref(up, 20) - act_ref(down, 20)) * dy.double()).sum()) / (2 * step)
+            # (a difference's own error: 1e-9 of values below 2^5)
+            assert abs(float(dx[r, c]) - slope) <= abs(slope) * 2 ** -11 + 2 ** -24 + 1e-7
+
+
+def test_graph():
+    m, width = Maker(2), 1032
+    x = torch.empty(70, 2 * width, dtype=torch.float16, device=DEV)
+    out, again = torch.empty(70, width, dtype=torch.float16, device=DEV), torch.empty(70, width, dtype=torch.float16, device=DEV)
+    codes, scales = torch.empty(70, width, dtype=F8, device=DEV), torch.empty(70, 9, device=DEV)
+    hr.experts_act(x, out, out8=codes, scales=scales)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hr.experts_act(x, out, out8=codes, scales=scales)
+    for _ in range(3):
+        v = m.normal(70, 2 * width, sigma=2.0, dtype=torch.float16)
+        x.copy_(v)
+        graph.replay()
+        hr.experts_act(x, again)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again)
+        check_codes(codes, scales, act_ref(v, width), 128, "act")
