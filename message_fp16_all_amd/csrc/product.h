@@ -269,6 +269,18 @@ __device__ __forceinline__ u32x4 any_unit(const char *p, int left) {
     return v;
 }
 
+// A unit's bytes moved down by `bytes` (0 .. 16), zeros behind them.
+__device__ __forceinline__ u32x4 moved_down(u32x4 v, int bytes) {
+    uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+    const int n = 8 * (bytes & 7);
+    lo = n == 0 ? lo : lo >> n | hi << (64 - n);
+    hi >>= n;
+    if (bytes >= 8) lo = hi, hi = 0;
+    if (bytes >= 16) lo = 0;
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                 static_cast<uint32_t>(hi >> 32)};
+}
+
 // Expert e's rows, whatever the offsets hold: inside 0 .. rows, first <= last.
 __device__ __forceinline__ void segment(const int32_t *offsets, uint32_t all, int e, uint32_t &first, uint32_t &last) {
     if (offsets == nullptr) {
@@ -636,31 +648,76 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
             b = b == S - 1 ? 0 : b + 1;
         }
     } else {
-        static_assert(S == 2 && SH::WK == 1, "one stage in registers");
+        static_assert(S == 2, "one stage in registers");
         u32x4 in_q[DQ], in_p[DP];
         float in_s = 0.0f;
+        // Whole units wherever a row has one: rows and units that are not there
+        // are read from ones that are.  A unit that the row's end cuts is read so
+        // that it ends there, and moved down when it goes to LDS; what lies past a
+        // panel's c is made zero there, in the last panel alone and in those behind
+        // it (a row or column of out that is not there may hold anything).  The loads are straight code: a
+        // branch for every unit made each wait for the one before.
+        constexpr int UNIT = PanelQ::kUnit;
+        const bool narrow = (QA ? a.nq : nc) < UNIT || (PA ? a.np : nc) < UNIT;
+        // unit d of a panel: its row, the values left of its row's from it on, and how
+        // far before its place it is read
+        const auto unit_of = [&](auto panel, bool across, int d, int b, int left, int &r, uint32_t &unit, int &here,
+                                 int &back) {
+            typedef decltype(panel) Pan;
+            uint32_t row;
+            Pan::source(share * (Pan::kDmas / kWaves) + d, lane, row, unit);
+            const int wide = across ? b : left, u = static_cast<int>(unit) * UNIT;
+            r = static_cast<int>(row);
+            here = wide - u;
+            back = here >= UNIT ? 0 : here > 0 ? UNIT - here : u + UNIT - wide;
+        };
+        const auto fetch_one = [&](auto panel, bool across, int d, const char *from, size_t stride, int b, int left) {
+            int r, here, back;
+            uint32_t unit;
+            unit_of(panel, across, d, b, left, r, unit, here, back);
+            const int rows = across ? left : b;
+            return load_vec<false>(from + static_cast<size_t>(r < rows ? r : rows - 1) * stride +
+                                   (static_cast<int>(unit) * 16 - back * SIZE));
+        };
+        const auto narrow_one = [&](auto panel, bool across, int d, const char *from, size_t stride, int b, int left) {
+            int r, here, back;
+            uint32_t unit;
+            unit_of(panel, across, d, b, left, r, unit, here, back);
+            return any_unit<SIZE>(from + r * stride + unit * 16, r < (across ? left : b) ? here : 0);
+        };
+        const auto trimmed = [&](auto panel, bool across, int d, u32x4 v, int b, int left) {
+            int r, here, back;
+            uint32_t unit;
+            unit_of(panel, across, d, b, left, r, unit, here, back);
+            v = moved_down(v, here >= UNIT ? 0 : here > 0 ? back * SIZE : 16);
+            return across && r >= left ? u32x4{0, 0, 0, 0} : v;
+        };
         const auto fetch = [&](int s) {
-            const int left = nc - s * CK;
-            const char *fq = qs + s * q_step, *fp = ps + s * p_step;
+            const int panel = s * SH::WK + wk, left = nc - panel * CK;
+            const char *fq = qs + panel * q_step, *fp = ps + panel * p_step;
+            if (narrow) {
 #pragma unroll
-            for (int j = 0; j < DQ; ++j) {
-                uint32_t row, unit;
-                PanelQ::source(share * DQ + j, lane, row, unit);
-                const int across = static_cast<int>(row) < (QA ? left : nq) ? (QA ? nq : left) : 0;
-                in_q[j] = any_unit<SIZE>(fq + row * a.q_stride + unit * 16, across - static_cast<int>(unit) * PanelQ::kUnit);
-            }
+                for (int j = 0; j < DQ; ++j) in_q[j] = narrow_one(PanelQ(), QA, j, fq, a.q_stride, nq, left);
 #pragma unroll
-            for (int j = 0; j < DP; ++j) {
-                uint32_t row, unit;
-                PanelP::source(share * DP + j, lane, row, unit);
-                const int across = static_cast<int>(row) < (PA ? left : np) ? (PA ? np : left) : 0;
-                in_p[j] = any_unit<SIZE>(fp + row * a.p_stride + unit * 16, across - static_cast<int>(unit) * PanelP::kUnit);
+                for (int j = 0; j < DP; ++j) in_p[j] = narrow_one(PanelP(), PA, j, fp, a.p_stride, np, left);
+            } else {
+#pragma unroll
+                for (int j = 0; j < DQ; ++j) in_q[j] = fetch_one(PanelQ(), QA, j, fq, a.q_stride, nq, left);
+#pragma unroll
+                for (int j = 0; j < DP; ++j) in_p[j] = fetch_one(PanelP(), PA, j, fp, a.p_stride, np, left);
             }
             if constexpr (SCALED)
-                in_s = off_s != kNowhere ? xs[(share * SROWS + lane) * a.q_scales_stride + s] : 0.0f;
+                in_s = off_s != kNowhere && left > 0 ? xs[(share * SROWS + lane) * a.q_scales_stride + panel] : 0.0f;
         };
-        const auto put = [&](int b) {
-            const uint32_t to = mine + b * kStageBytes;
+        const auto put = [&](int s) {
+            const int left = nc - (s * SH::WK + wk) * CK;
+            const uint32_t to = mine + (s & 1) * kStageBytes;
+            if (!narrow && (left < CK || (QA && nq < BQ) || (PA && np < BP))) {
+#pragma unroll
+                for (int j = 0; j < DQ; ++j) in_q[j] = trimmed(PanelQ(), QA, j, in_q[j], nq, left);
+#pragma unroll
+                for (int j = 0; j < DP; ++j) in_p[j] = trimmed(PanelP(), PA, j, in_p[j], np, left);
+            }
 #pragma unroll
             for (int j = 0; j < DQ; ++j)
                 *reinterpret_cast<HR_LDS u32x4 *>(to + (share * DQ + j) * 1024 + lane * 16) = in_q[j];
@@ -679,7 +736,7 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
             __syncthreads();
             if (s + 1 < stages) fetch(s + 1);
             add(s, mine + (s & 1) * kStageBytes);
-            if (s + 1 < stages) put(~s & 1);
+            if (s + 1 < stages) put(s + 1);
         }
     }
 

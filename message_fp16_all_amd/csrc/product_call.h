@@ -171,7 +171,7 @@ typedef Shape<16, 32, 1, 1, 4, 3, 2> Few;
 typedef Shape<16, 64, 1, 1, 4, 3> FewAcross;    // (32 values of a strided row are half a line)
 typedef Shape<16, 16, 1, 1, 4, 4> Tiny;
 typedef Shape<64, 64, 1, 1, 4, 2> Deep;         // the gradient of few matrices
-typedef Shape<32, 128, 1, 4, 1, 2, 2> AnyFew;
+typedef Shape<16, 32, 1, 1, 4, 2, 3> AnyFew;
 
 template <class E, class O, class SH, bool PA, bool ANY>
 hr_status run_product(ProductArgs &a, hr_stream_t stream) {
@@ -181,15 +181,21 @@ hr_status run_product(ProductArgs &a, hr_stream_t stream) {
 }
 
 // The largest shape whose height fits the segments and whose tiles fill the GPU.
-// 4096 x 4096 matrices, bfloat16, us by shape (the chosen one first), one
-// matrix: 16 rows Tiny 7.2 Few 8.0; 64 Few 12.2 Low 21.4; 256 Low 22.9 Some 32.1
-// Few 39; 512 Some 33.8 Low 43 Middle 43; 1024 Some 42.8 Middle 47 Half 60; 2048
-// Middle 63.9 Half 66.0 large 78; 4096 large 98 Middle 133 Half 138.  64 matrices
-// of 2048 x 4096 and rows spread over them, on average 8: Few 157 Some 162; 16: Some
-// 174 Middle 170 Few 196; 32: Middle 175 Half 181 Some 192 Few 272; 64: Half 224
-// large 210 Middle 236; 128: Half 268 large 293; 256: large 372 Half 391.  e4m3: 8: Few
-// 86 Some 105; 16: Some 114 Middle 125; 32: Middle 125 Some 121; 64: Half 144 Some
-// 136; 128: Half 173 large 206; 256: large 255 Half 266.
+// (The rows are the buffer's: with padded segments more than there are.)  us by
+// shape, the chosen one first.
+// 4096 x 4096, bfloat16, one matrix: 16 rows Tiny 7.2 Few 8.0; 64 Few 12.2 Low
+// 21.4; 256 Low 22.9 Some 32.1 Few 39; 512 Some 33.8 Low 43 Middle 43; 1024 Some
+// 42.8 Middle 47 Half 60; 2048 Middle 63.9 Half 66.0 large 78; 4096 large 98
+// Middle 133 Half 138.
+// 64 matrices of 2048 x 4096, rows per matrix on average 8: Few 157 Some 162; 16: Low
+// 179 Middle 170 Few 196; 32: Some 192 Middle 175 Few 272; 47 with padding: Middle
+// 176 Half 183 Some 192; 64: Half 224 large 210 Middle 236; 128: Half 268 large 293;
+// 256: large 372 Half 391.  e4m3: 8: Few 86 Some 105; 16: Low 115 Some 114 Middle
+// 125; 32: Some 121 Middle 125; 47: Middle 126 Some 119; 64: Half 144 Some 136; 128:
+// Half 173 large 206; 256: large 255 Half 266.
+// 64 matrices of 2560 x 5120 and padding to 16 rows, 512 rows in 1472: Some 264 Low 254
+// Middle 299 Few 279; 1024 in 1984: Some 283 Low 285 Middle 310.
+// Transposed 2 rows: FewAcross 10.3 Low 21; e4m3 512 rows of 64: Low 93 FewAcross 123.
 template <class E, class O, bool PA>
 hr_status pick_product(ProductArgs &a, bool any, hr_stream_t stream) {
     const size_t each = a.rows / a.experts;
@@ -197,16 +203,18 @@ hr_status pick_product(ProductArgs &a, bool any, hr_stream_t stream) {
         return each >= least_rows && tiles_of(a.rows, a.experts, bq) * ((a.np + bp - 1) / bp) >= least_tiles;
     };
     if (any)
-        return each < 24 ? run_product<E, O, AnyFew, PA, true>(a, stream) : run_product<E, O, Middle, PA, true>(a, stream);
+        return fits(128, 128, 24, 128) ? run_product<E, O, Middle, PA, true>(a, stream)
+                                       : run_product<E, O, AnyFew, PA, true>(a, stream);
     if (fits(256, 256, 192, 200)) {
         a.tiles_p = (a.np + 255) / 256;
         return launch_large(product_large<E, O, false, PA, false>, tiles_of(a.rows, a.experts, 256) * a.tiles_p, stream, a);
     }
     if (fits(128, 256, 64, 320)) return run_product<E, O, Half, PA, false>(a, stream);
-    if (fits(128, 128, 20, 320)) return run_product<E, O, Middle, PA, false>(a, stream);
-    if (fits(64, 128, 12, 200)) return run_product<E, O, Some, PA, false>(a, stream);
+    if (fits(128, 128, 40, 320)) return run_product<E, O, Middle, PA, false>(a, stream);
+    if (fits(64, 128, 20, 200)) return run_product<E, O, Some, PA, false>(a, stream);
     if (fits(32, 128, 12, 128)) return run_product<E, O, Low, PA, false>(a, stream);
     if constexpr (PA) {
+        if (fits(32, 128, 0, 256)) return run_product<E, O, Low, PA, false>(a, stream);
         return run_product<E, O, FewAcross, PA, false>(a, stream);
     } else {
         if (fits(16, 32, 0, 192)) return run_product<E, O, Few, PA, false>(a, stream);
