@@ -1005,18 +1005,20 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
                 sum[i][j] = mfma16<E>(w[half][i], x[half][j], sum[i][j]);
             }
         } else {
-            // (a part is scaled two instructions later, when it is there)
-            constexpr int N = FP * FH, EACH = N / (loads + 1);
-            f32x4 part[3];
+            // (a part is scaled four instructions later, when it is there: two later
+            // the compiler put waits of up to 9 slots before every other scaling)
+            constexpr int N = FP * FH, EACH = N / (loads + 1), LATER = 4;
+            f32x4 part[LATER + 1];
 #pragma unroll
-            for (int t = 0; t < N + 2; ++t) {
-                if (t < N) part[t % 3] = mfma8(w8[t % FP], x8[t / FP]);
+            for (int t = 0; t < N + LATER; ++t) {
+                if (t < N) part[t % (LATER + 1)] = mfma8(w8[t % FP], x8[t / FP]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (t >= 2) {
-                    const int u = t - 2;
+                if (t >= LATER) {
+                    const int u = t - LATER;
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        sum[u % FP][u / FP][v] = fmaf(part[u % 3][v], scale[u / FP], sum[u % FP][u / FP][v]);
+                        sum[u % FP][u / FP][v] =
+                            fmaf(part[u % (LATER + 1)][v], scale[u / FP], sum[u % FP][u / FP][v]);
                 }
                 if (t % EACH == EACH - 1 && t / EACH < loads) load(t / EACH);
                 __builtin_amdgcn_sched_barrier(0);
