@@ -7,6 +7,8 @@
 //   dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s
 //
 // Bound by HBM: every value is read once and written once.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace hr {
@@ -25,29 +27,55 @@ struct ActArgs {
     int group_lanes;
 };
 
-// s = 1 / (1 + e^-g) and 1 - s, each to a few units in the last place: from
-// z = e^-|g|, whose exponent is corrected by what rounding it left out.  Where s
-// would leave binary32 (g below -64 ln 2), it is given times 2^64, with
-// `factor` 2^-64 for one of its partners; bfloat16 results there are still normal.
+// s = 1 / (1 + e^-g) and 1 - s, each to a few units in the last place.
+//
+// NEAR (|g| below kNear): from z = e^-g, whose exponent is corrected by what its
+// rounding left out; 1 + z stays in binary32's range.
+//
+// Otherwise: from z = e^-|g|, corrected further.  Where s would leave binary32 (g
+// below -64 ln 2), it is given times 2^64, with `factor` 2^-64 for one of its
+// partners; bfloat16 results there are still normal.
+constexpr float kNear = 87.0f;
+
+template <bool NEAR>
 struct Sigmoid {
     float s, rest, factor;
     __device__ __forceinline__ explicit Sigmoid(float g) {
         constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;      // log2(e) = their sum
-        const float a = fabsf(g);
-        const float t = a * kLog2e;
-        // (an infinite exponent has no remainder)
-        const float lost = t < INFINITY ? fmaf(a, kLog2eRest, fmaf(a, kLog2e, -t)) : 0.0f;
-        const bool low = g < 0.0f && t > 64.0f;
-        float z = __builtin_amdgcn_exp2f(low ? 64.0f - t : -t);
-        z = fmaf(z, -0.693147181f * lost, z);
-        factor = low ? 0x1p-64f : 1.0f;
-        const float inv = __builtin_amdgcn_rcpf(1.0f + (low ? 0.0f : z));
-        const float other = z * inv;
-        s = g < 0.0f ? other : inv;
-        rest = g < 0.0f ? inv : other;
-        if (g != g) s = rest = g;
+        constexpr float kLn2 = 0.693147181f;
+        if constexpr (NEAR) {
+            const float t = g * -kLog2e;
+            float z = __builtin_amdgcn_exp2f(t);
+            z = fmaf(z, kLn2 * fmaf(g, -kLog2e, -t), z);
+            s = __builtin_amdgcn_rcpf(1.0f + z);
+            rest = z * s;
+            factor = 1.0f;
+        } else {
+            const float a = fabsf(g);
+            const float t = a * kLog2e;
+            // (an infinite exponent has no remainder)
+            const float lost = t < INFINITY ? fmaf(a, kLog2eRest, fmaf(a, kLog2e, -t)) : 0.0f;
+            const bool low = g < 0.0f && t > 64.0f;
+            float z = __builtin_amdgcn_exp2f(low ? 64.0f - t : -t);
+            z = fmaf(z, -kLn2 * lost, z);
+            factor = low ? 0x1p-64f : 1.0f;
+            const float inv = __builtin_amdgcn_rcpf(1.0f + (low ? 0.0f : z));
+            const float other = z * inv;
+            s = g < 0.0f ? other : inv;
+            rest = g < 0.0f ? inv : other;
+            if (g != g) s = rest = g;
+        }
     }
 };
+
+// Whether all of the wave's gates are near: which is nearly always so, and makes a
+// value's sigmoid 8 instructions instead of some 20.
+__device__ __forceinline__ bool all_near(const float (&g)[8]) {
+    bool near = true;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) near = near && fabsf(g[e]) < kNear;
+    return __all(near);
+}
 
 __device__ __forceinline__ uint32_t rows_used(const ActArgs &a) {
     if (a.used == nullptr) return a.rows;
@@ -55,87 +83,130 @@ __device__ __forceinline__ uint32_t rows_used(const ActArgs &a) {
     return n < 0 ? 0u : static_cast<uint32_t>(n) < a.rows ? static_cast<uint32_t>(n) : a.rows;
 }
 
-// L lanes per row, one unit of 8 values each at a time.
-template <class E, int L, bool GATED, bool TAIL>
+// L lanes per row, a unit of 8 values of U rows each at a time, so that a lane has
+// 2 U loads on their way before it works on the first.
+template <class E, int L, int U, bool GATED, bool TAIL, bool NT>
 __global__ __launch_bounds__(kActThreads) void act_rows(ActArgs a) {
     constexpr uint32_t R = kActThreads / L;
     const uint32_t used = rows_used(a);
-    const uint32_t r = blockIdx.x * R + threadIdx.x / L;
-    if (blockIdx.x * R >= used) return;
-    const bool here = r < used;
+    const uint32_t r0 = blockIdx.x * (R * U) + threadIdx.x / L;
+    if (blockIdx.x * (R * U) >= used) return;
     const int lane = static_cast<int>(threadIdx.x) % L, units = (a.width + 7) / 8;
-    const uint16_t *x = a.x + r * a.x_stride;
     // (every lane of a group takes part in its maximum)
     for (int i0 = 0; i0 < units; i0 += L) {
         const int i = i0 + lane;
-        const bool there = here && i < units;
-        const Unit<TAIL> at(there ? i : 0, a.width);
-        float y[8] = {};
-        if (there) {
-            Wide<E>::widen(at.load(x), y);
-            if constexpr (GATED) {
-                float up[8];
-                Wide<E>::widen(at.load(x + a.width), up);
+        const Unit<TAIL> at(i < units ? i : 0, a.width);
+        u32x4 in[U], up[U];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const Sigmoid g(y[e]);
-                    y[e] = y[e] * g.s * (up[e] * g.factor);
-                }
+        for (int u = 0; u < U; ++u) {
+            const uint32_t r = r0 + u * R;
+            in[u] = up[u] = u32x4{0, 0, 0, 0};
+            if (r < used && i < units) {
+                const uint16_t *x = a.x + r * a.x_stride;
+                in[u] = at.template load<NT>(x);
+                if constexpr (GATED) up[u] = at.template load<NT>(x + a.width);
             }
-            if (a.out != nullptr) at.store_own(a.out + r * a.out_stride, Wide<E>::narrow(y));
         }
-        if (a.codes == nullptr) continue;
-        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t m = __builtin_bit_cast(uint32_t, y[e]) & 0x7FFFFFFFu;
-            if (there && at.own(e)) top = m > top ? m : top;
-        }
-        top = max_of_group(top, a.group_lanes);
-        if (!there) continue;
-        const float scale = e4m3_scale(__builtin_bit_cast(float, top));
-        if (i % a.group_lanes == 0) a.scales[r * a.scales_stride + i / a.group_lanes] = scale;
-        const E4m3Codes at_scale(scale, y);
-        const u32x2 c = at_scale.codes(y);
-        uint8_t *p = a.codes + r * a.codes_stride + at.start;
-        if (!TAIL || (a.width >= 8 && at.skip == 0)) {
-            *reinterpret_cast<u32x2_row *>(p) = c;
-        } else {
+        for (int u = 0; u < U; ++u) {
+            const uint32_t r = r0 + u * R;
+            const bool there = r < used && i < units;
+            float y[8];
+            Wide<E>::widen(in[u], y);
+            if constexpr (GATED) {
+                float v[8];
+                Wide<E>::widen(up[u], v);
+                const auto gate = [&](auto near) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (at.own(e)) p[e] = static_cast<uint8_t>(c[e / 4] >> (8 * (e & 3)));
+                    for (int e = 0; e < 8; ++e) {
+                        const Sigmoid<decltype(near)::value> g(y[e]);
+                        y[e] = y[e] * g.s * (v[e] * g.factor);
+                    }
+                };
+                if (all_near(y))
+                    gate(std::true_type());
+                else
+                    gate(std::false_type());
+            }
+            if (there && a.out != nullptr) at.template store_own<NT>(a.out + r * a.out_stride, Wide<E>::narrow(y));
+            if (a.codes == nullptr) continue;
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t m = __builtin_bit_cast(uint32_t, y[e]) & 0x7FFFFFFFu;
+                if (there && at.own(e)) top = m > top ? m : top;
+            }
+            top = max_of_group(top, a.group_lanes);
+            if (!there) continue;
+            const float scale = e4m3_scale(__builtin_bit_cast(float, top));
+            if (i % a.group_lanes == 0) a.scales[r * a.scales_stride + i / a.group_lanes] = scale;
+            const E4m3Codes at_scale(scale, y);
+            const u32x2 c = at_scale.codes(y);
+            uint8_t *p = a.codes + r * a.codes_stride + at.start;
+            if (!TAIL || (a.width >= 8 && at.skip == 0)) {
+                if constexpr (NT)
+                    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_row *>(p));
+                else
+                    *reinterpret_cast<u32x2_row *>(p) = c;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at.own(e)) p[e] = static_cast<uint8_t>(c[e / 4] >> (8 * (e & 3)));
+            }
         }
     }
 }
 
-template <class E, int L, bool TAIL>
+template <class E, int L, int U, bool TAIL, bool NT>
 __global__ __launch_bounds__(kActThreads) void act_grad_rows(ActArgs a) {
     constexpr uint32_t R = kActThreads / L;
-    const uint32_t r = blockIdx.x * R + threadIdx.x / L;
-    if (r >= rows_used(a)) return;
+    const uint32_t used = rows_used(a);
+    const uint32_t r0 = blockIdx.x * (R * U) + threadIdx.x / L;
+    if (r0 >= used) return;
     const int lane = static_cast<int>(threadIdx.x) % L, units = (a.width + 7) / 8;
-    const uint16_t *x = a.x + r * a.x_stride, *dy = a.dy + r * a.dy_stride;
-    uint16_t *dx = a.dx + r * a.dx_stride;
     for (int i = lane; i < units; i += L) {
         // (dx may be x: a unit's values that are its neighbour's may have been
         // overwritten, and are not stored)
         const Unit<TAIL> at(i, a.width);
-        float gate[8], up[8], d[8], y[8];
-        Wide<E>::widen(at.load(x), gate);
-        Wide<E>::widen(at.load(x + a.width), up);
-        Wide<E>::widen(at.load(dy), d);
+        u32x4 in[3][U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const Sigmoid g(gate[e]);
-            const float silu = gate[e] * g.s;
-            const float u = up[e] * g.factor;
-            y[e] = silu * u;
-            up[e] = d[e] * u * (g.s * fmaf(gate[e], g.rest, 1.0f));
-            gate[e] = d[e] * g.factor * silu;
+        for (int u = 0; u < U; ++u) {
+            const uint32_t r = r0 + u * R;
+            if (r < used) {
+                const uint16_t *x = a.x + r * a.x_stride;
+                in[0][u] = at.template load<NT>(x);
+                in[1][u] = at.template load<NT>(x + a.width);
+                in[2][u] = at.template load<NT>(a.dy + r * a.dy_stride);
+            }
         }
-        at.store_own(dx, Wide<E>::narrow(up));
-        at.store_own(dx + a.width, Wide<E>::narrow(gate));
-        if (a.out != nullptr) at.store_own(a.out + r * a.out_stride, Wide<E>::narrow(y));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t r = r0 + u * R;
+            if (r >= used) continue;
+            uint16_t *dx = a.dx + r * a.dx_stride;
+            float gate[8], up[8], d[8], y[8];
+            Wide<E>::widen(in[0][u], gate);
+            Wide<E>::widen(in[1][u], up);
+            Wide<E>::widen(in[2][u], d);
+            const auto grad = [&](auto near) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const Sigmoid<decltype(near)::value> g(gate[e]);
+                    const float silu = gate[e] * g.s;
+                    const float v = up[e] * g.factor;
+                    y[e] = silu * v;
+                    up[e] = d[e] * v * (g.s * fmaf(gate[e], g.rest, 1.0f));
+                    gate[e] = d[e] * g.factor * silu;
+                }
+            };
+            if (all_near(gate))
+                grad(std::true_type());
+            else
+                grad(std::false_type());
+            at.template store_own<NT>(dx, Wide<E>::narrow(up));
+            at.template store_own<NT>(dx + a.width, Wide<E>::narrow(gate));
+            if (a.out != nullptr) at.template store_own<NT>(a.out + r * a.out_stride, Wide<E>::narrow(y));
+        }
     }
 }
 
@@ -143,24 +214,54 @@ namespace {
 
 int act_lanes(size_t width) { return width <= 128 ? 16 : width <= 512 ? 64 : kActThreads; }
 
+// Calls that read or write this much go past the caches, two rows to a lane.
+// Measured from three sets of buffers in turn, one row cached and two streamed:
+// activation 65528 x 2048 to bfloat16 135 and 127 us, as rows are to e4m3 77 and 63,
+// gradient 234 and 209; of 16383 x 4096 143 and 135; 8192 x 2048 to e4m3 (101 MB) 19.2
+// and 20.6, its gradient (168 MB) 30.9 and 28.3; four rows 130, 65, 218, 141.
+constexpr size_t kActStreamBytes = size_t(1) << 27;
+constexpr int kActRows = 2;
+
 template <class K>
-hr_status launch_act(K kernel, int lanes, const ActArgs &a, hr_stream_t stream) {
-    const size_t grid = (static_cast<size_t>(a.rows) + kActThreads / lanes - 1) / (kActThreads / lanes);
+hr_status launch_act(K kernel, int lanes, int rows, const ActArgs &a, hr_stream_t stream) {
+    const size_t high = static_cast<size_t>(kActThreads / lanes) * rows;
+    const size_t grid = (a.rows + high - 1) / high;
     if (grid >= (size_t(1) << 32) / kActThreads) return HR_ERR_TOO_LARGE;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(kActThreads), 0,
                        reinterpret_cast<hipStream_t>(stream), a);
     return hipGetLastError() == hipSuccess ? HR_OK : HR_ERR_HIP;
 }
 
+// The variant of a kernel K<E, lanes, rows, .., TAIL, NT> for a call: several rows to
+// a lane, past the caches, where the values are many.
+#define HR_ACT_AT(K, L, U, NT, ...)                                                                       \
+    (a.width % 8 != 0 ? launch_act(K<E, L, U, ##__VA_ARGS__, true, NT>, L, U, a, stream)                    \
+                      : launch_act(K<E, L, U, ##__VA_ARGS__, false, NT>, L, U, a, stream))
+#define HR_ACT(K, ...)                                                                                    \
+    do {                                                                                                  \
+        const int lanes = act_lanes(a.width);                                                             \
+        if (static_cast<size_t>(a.rows) * a.width * (a.dy != nullptr ? 10 : 4) >= kActStreamBytes) {                               \
+            if (lanes == 16) return HR_ACT_AT(K, 16, kActRows, true, ##__VA_ARGS__);                      \
+            if (lanes == 64) return HR_ACT_AT(K, 64, kActRows, true, ##__VA_ARGS__);                      \
+            return HR_ACT_AT(K, kActThreads, kActRows, true, ##__VA_ARGS__);                              \
+        }                                                                                                 \
+        if (lanes == 16) return HR_ACT_AT(K, 16, 1, false, ##__VA_ARGS__);                                \
+        if (lanes == 64) return HR_ACT_AT(K, 64, 1, false, ##__VA_ARGS__);                                \
+        return HR_ACT_AT(K, kActThreads, 1, false, ##__VA_ARGS__);                                        \
+    } while (0)
+
 template <class E, bool GATED>
 hr_status run_act(const ActArgs &a, hr_stream_t stream) {
-    const int lanes = act_lanes(a.width);
-    const bool tail = a.width % 8 != 0;
-    if (lanes == 16) return launch_act(tail ? act_rows<E, 16, GATED, true> : act_rows<E, 16, GATED, false>, 16, a, stream);
-    if (lanes == 64) return launch_act(tail ? act_rows<E, 64, GATED, true> : act_rows<E, 64, GATED, false>, 64, a, stream);
-    return launch_act(tail ? act_rows<E, kActThreads, GATED, true> : act_rows<E, kActThreads, GATED, false>, kActThreads,
-                      a, stream);
+    HR_ACT(act_rows, GATED);
 }
+
+template <class E>
+hr_status run_act_grad(const ActArgs &a, hr_stream_t stream) {
+    HR_ACT(act_grad_rows);
+}
+
+#undef HR_ACT
+#undef HR_ACT_AT
 
 template <class E>
 hr_status act_impl(const hr_experts_act_args *q, hr_stream_t stream) {
@@ -235,12 +336,7 @@ hr_status act_grad_impl(const hr_experts_act_grad_args *q, hr_stream_t stream) {
     a.used = q->offsets != nullptr ? q->offsets + q->experts : nullptr;
     a.rows = static_cast<uint32_t>(q->rows);
     a.width = static_cast<int>(w);
-    const int lanes = act_lanes(w);
-    const bool tail = w % 8 != 0;
-    if (lanes == 16) return launch_act(tail ? act_grad_rows<E, 16, true> : act_grad_rows<E, 16, false>, 16, a, stream);
-    if (lanes == 64) return launch_act(tail ? act_grad_rows<E, 64, true> : act_grad_rows<E, 64, false>, 64, a, stream);
-    return launch_act(tail ? act_grad_rows<E, kActThreads, true> : act_grad_rows<E, kActThreads, false>, kActThreads, a,
-                      stream);
+    return run_act_grad<E>(a, stream);
 }
 
 }  // namespace
