@@ -931,8 +931,8 @@ typedef struct {
  * experts, null pointers, scales missing or not wanted, a stride below the row,
  * overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (n or k above
  * HR_EXPERTS_PRODUCT_MAX, experts above HR_EXPERTS_MAX, 2^31 rows or more, rows
- * more than 4 MiB apart, a launch of 2^32 work-items or more, at the least one
- * per 4 values of out), HR_ERR_HIP.
+ * more than 4 MiB apart, a launch of 2^32 work-items or 2^31 tiles or more),
+ * HR_ERR_HIP.
  */
 HR_API hr_status hr_experts_product_f16(const hr_experts_product_args *args, hr_stream_t stream);
 HR_API hr_status hr_experts_product_bf16(const hr_experts_product_args *args, hr_stream_t stream);
@@ -994,7 +994,8 @@ typedef struct {
  * Errors: HR_ERR_INVALID_ARG (width 0, group, codes without scales or scales
  * without codes, nothing to write, offsets with experts below 1, null pointers, a
  * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (2^31 rows
- * or more, width above HR_EXPERTS_PRODUCT_MAX), HR_ERR_HIP.
+ * or more, width above HR_EXPERTS_PRODUCT_MAX, a launch of 2^32 work-items or
+ * more: 2^24 rows of more than 512 values, 2^28 of up to 128), HR_ERR_HIP.
  */
 HR_API hr_status hr_experts_act_f16(const hr_experts_act_args *args, hr_stream_t stream);
 HR_API hr_status hr_experts_act_bf16(const hr_experts_act_args *args, hr_stream_t stream);

@@ -1096,7 +1096,7 @@ def _call_on(fn, name: str, args, stream, first, *others):
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on several devices")
-    if dev >= 0 and _torch.cuda.current_device() != dev:
+    if dev >= 0 and _torch._C._cuda_getDevice() != dev:
         with _torch.cuda.device(dev):
             st = fn(args, _stream_of(stream, first))
     else:

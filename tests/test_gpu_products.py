@@ -428,10 +428,10 @@ def test_gradients_against_differences():
         assert total(x, v) - base == float(dw[e, r, c])
 
 
-def test_graphs_and_streams():
+@pytest.mark.parametrize("k,n,E,rows", [(136, 264, 4, 700), (72, 1032, 12, 6000)])
+def test_graphs_and_streams(k, n, E, rows):
     """Captured calls replayed with fresh inputs and offsets, beside eager ones on another stream."""
-    m, k, n, E, rows = Maker(8), 136, 264, 4, 700
-    dt = torch.bfloat16
+    m, dt = Maker(8), torch.bfloat16
     x, w, dy = (torch.empty(*s, dtype=dt, device=DEV) for s in ((rows, k), (E, n, k), (rows, n)))
     at = on_device([0] * (E + 1))
     out, dx, dw = torch.zeros(rows, n, dtype=dt, device=DEV), torch.zeros_like(x), torch.empty_like(w)
