@@ -475,6 +475,13 @@ struct Shape {
 // E: operands; O: out (F16, BF16 or float); QA, PA: the operand lies across.
 // GRAD: the weights' gradient.  ANY: rows of any address and length, brought
 // through registers.
+//
+// Waves that share a panel meet once a stage, after their loads of it have landed
+// and before those of S - 1 stages later go out; a wave with a panel of its own
+// (WK > 1) meets nobody until the sums are joined.  For few rows bound by HBM: 512
+// rows of 64 matrices of 2560 x 5120 246 us (6.8 TB/s of weights), padded to 16 rows
+// 254-264; e4m3 384 rows of 64 of 5120 x 5120 237 (7.1 TB/s); two rows of two
+// matrices of 2048 x 4096 6.5 (a graph node alone 1.6).
 template <class E, class O, class SH, bool QA, bool PA, bool GRAD, bool ANY>
 __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(ProductArgs a) {
     constexpr int SIZE = kBytes<E>, BQ = SH::BQ, BP = SH::BP, S = SH::S;
@@ -783,17 +790,26 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
 //     first set     read   multiply  read      multiply  read
 //     second set           read      multiply  read      multiply
 //
-// Loads go out between matrix instructions.  P and the first panel of Q were
-// last read in turn 4 s + 1, and the loads of stage s + 2 into their place go out
-// while a set multiplies for the second time; those of the second panel of
-// stage s + 1 while it does so for the first.  A set waits for its own loads
-// before the barrier after which either set reads them, three to four turns
-// later.  Every turn of a wave issues the same number of loads, the last stages'
-// from nowhere, so that the turns are straight code and the waits' counts fixed.
-// (A tile of at most 128 rows takes one turn per stage, and has three buffers.)
-// (Tiles one after the other: a workgroup has a compute unit to itself.  The next
+// P and the first panel of Q were last read in turn 4 s + 1, the second panel in
+// 4 s + 3.  So the loads of stage s + 2's P and first panel go out with the second
+// reading of stage s, those of stage s + 1's second panel with the first; in 16
+// bits behind the reads, in e4m3, where the reading turns are the longer ones,
+// between the matrix instructions that follow (8192 x 8192 x 8192 520 -> 487 us; in
+// 16 bits 749 behind the reads, 804 between).  A set waits for its own loads before
+// the barrier after which either set reads them, four to six turns later.  Every
+// turn of a wave issues the same number of loads, the last stages' from nowhere,
+// so that the turns are straight code and the waits' counts fixed.
+// A tile of at most 128 rows takes one turn per stage, and has three buffers.
+//
+// Tiles one after the other: a workgroup has a compute unit to itself.  The next
 // tile's first loads go out before this one's sums are stored, and the stores
-// are waited for a stage later.)
+// are waited for a stage later (loads and stores complete in order).
+//
+// 8192 x 8192 x 8192: bfloat16 730-760 us (1.45-1.51 PF), transposed 753, gradient
+// 760-787; e4m3 465-488 (2.3 PF).  Without any loads these are 640 and 411, with
+// zeros for data e4m3 takes 400 with loads: the rest is power.  Segments of 512 rows
+// of 128 matrices (4096 -> 2048) 886: their panels come from HBM, 20 of them for 32
+// tiles on a die where one large matrix needs 12.
 template <class E, class O, bool QA, bool PA, bool GRAD>
 __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     constexpr int SIZE = kBytes<E>, BQ = 256, BP = 256, H = 128, FP = 4, FH = 4;
