@@ -930,9 +930,9 @@ typedef struct {
  * Errors: HR_ERR_INVALID_ARG (n, k or experts 0, offsets NULL with several
  * experts, null pointers, scales missing or not wanted, a stride below the row,
  * overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (n or k above
- * HR_EXPERTS_PRODUCT_MAX, experts above HR_EXPERTS_MAX, 2^31 rows or more, rows
- * more than 4 MiB apart, a launch of 2^32 work-items or 2^31 tiles or more),
- * HR_ERR_HIP.
+ * HR_EXPERTS_PRODUCT_MAX, experts above HR_EXPERTS_MAX, more than 2^31 - 4096
+ * rows, rows more than 4 MiB apart, a launch of 2^32 work-items or 2^31 tiles or
+ * more), HR_ERR_HIP.
  */
 HR_API hr_status hr_experts_product_f16(const hr_experts_product_args *args, hr_stream_t stream);
 HR_API hr_status hr_experts_product_bf16(const hr_experts_product_args *args, hr_stream_t stream);

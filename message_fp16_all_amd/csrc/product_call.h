@@ -8,6 +8,8 @@ namespace hr {
 
 // Rows of at most 4 MiB apart: a tile's 256 stay inside a buffer's 2 GiB.
 constexpr size_t kMaxProductStride = size_t(1) << 22;
+// A row number and some stages' rows behind it stay below 2^31.
+constexpr size_t kMaxProductRows = (size_t(1) << 31) - 4096;
 
 inline bool units16(const void *p) { return aligned(p, 16); }
 
@@ -41,7 +43,7 @@ hr_status product_check(const hr_experts_product_args *q, ProductArgs &a, bool &
     if (q == nullptr || q->n == 0 || q->k == 0 || q->experts < 1 || (q->offsets == nullptr && q->experts != 1))
         return HR_ERR_INVALID_ARG;
     if (q->n > HR_EXPERTS_PRODUCT_MAX || q->k > HR_EXPERTS_PRODUCT_MAX || q->experts > HR_EXPERTS_MAX ||
-        q->rows > 0x7FFFFFFFu)
+        q->rows > kMaxProductRows)
         return HR_ERR_TOO_LARGE;
     const bool across = q->transposed != 0;
     const size_t wr = across ? q->k : q->n, wc = across ? q->n : q->k;
@@ -97,7 +99,7 @@ inline hr_status product_grad_check(const hr_experts_product_grad_args *q, Produ
     if (q == nullptr || q->n == 0 || q->k == 0 || q->experts < 1 || (q->offsets == nullptr && q->experts != 1))
         return HR_ERR_INVALID_ARG;
     if (q->n > HR_EXPERTS_PRODUCT_MAX || q->k > HR_EXPERTS_PRODUCT_MAX || q->experts > HR_EXPERTS_MAX ||
-        q->rows > 0x7FFFFFFFu)
+        q->rows > kMaxProductRows)
         return HR_ERR_TOO_LARGE;
     size_t ys = q->dy_stride, xs = q->x_stride;
     const size_t ob = q->dw_f32 ? 4 : 2;

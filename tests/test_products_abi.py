@@ -70,6 +70,15 @@ def test_product_refusals_8(over, status):
     assert product(True, **over) == status
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_most_rows(eight):
+    """A row number plus a tile's or a stage's rows stays in 31 bits."""
+    assert product(eight, rows=(1 << 31) - 4095) == LARGE
+    assert product(eight, rows=(1 << 31) - 4096, out=at(2) + 1) == ALIGN
+    assert grad(rows=(1 << 31) - 4095) == LARGE
+    assert grad(rows=(1 << 31) - 4096, dw=at(2) + 1) == ALIGN
+
+
 def test_matrices_in_pieces():
     """The bytes between matrices that are apart are not theirs."""
     gap = dict(n=64, k=64, w_expert_stride=1 << 20)
