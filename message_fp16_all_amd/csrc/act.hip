@@ -36,7 +36,9 @@ struct ActArgs {
 //
 // Otherwise: from z = e^-|g|, corrected further.  Where s would leave binary32 (g
 // below -64 ln 2), it is given times 2^64, with `factor` 2^-64 for one of its
-// partners; bfloat16 results there are still normal.
+// partners; bfloat16 results there are still normal.  A near gate that comes this way,
+// because its neighbours are not near, is given as the other way gives it: a value's
+// result does not depend on its neighbours.
 constexpr float kNear = 87.0f;
 
 template <bool NEAR>
@@ -66,6 +68,10 @@ struct Sigmoid {
             s = g < 0.0f ? other : inv;
             rest = g < 0.0f ? inv : other;
             if (g != g) s = rest = g;
+            if (a < kNear) {
+                const Sigmoid<true> near(g);
+                s = near.s, rest = near.rest, factor = 1.0f;
+            }
         }
     }
 };

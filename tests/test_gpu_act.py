@@ -194,3 +194,23 @@ def test_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, again)
         check_codes(codes, scales, act_ref(v, width), 128, "act")
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("rows,width", [(4096, 64), (2048, 504), (512, 2048)])
+def test_a_value_does_not_depend_on_its_neighbours(name, rows, width):
+    """Gates far from zero take another way to the sigmoid; the others' results have the same bits beside them."""
+    dt = TYPES[name]
+    m = Maker(rows + width)
+    x, dy = m.normal(rows, 2 * width, sigma=20.0, dtype=dt).clamp(-80, 80).to(DEV), m.normal(rows, width, dtype=dt).to(DEV)
+    far = x.clone()
+    apart = torch.arange(rows * width, device=DEV).view(rows, width) % 31 == 0
+    for value in (-100.0, 100.0, float("nan")):
+        far[:, :width][apart] = value
+        got = [[torch.zeros(rows, w, dtype=dt, device=DEV) for w in (width, 2 * width)] for _ in range(2)]
+        for (out, dx), v in zip(got, (x, far)):
+            hr.experts_act(v, out)
+            hr.experts_act_grad(dy, v, dx)
+        for a, b in zip(*got):
+            a, b = a.view(rows, -1, width), b.view(rows, -1, width)
+            assert torch.equal(a.movedim(1, 0)[:, ~apart], b.movedim(1, 0)[:, ~apart])
