@@ -462,3 +462,21 @@ def test_graphs_and_streams(k, n, E, rows):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
         ref, mag = product_ref(x.cpu(), w.cpu(), at.tolist(), False)
         within(out.cpu(), ref, sum_tol(dt, ref, mag, k), "out")
+
+
+def test_most_rows():
+    """As many rows as there may be, the last of them in a segment that begins just before."""
+    rows, k, n = (1 << 31) - 4096, 8, 2
+    x = torch.zeros(rows, k, dtype=torch.float16, device=DEV)
+    at = [0, 1, 255, 256, 1 << 30, rows - 300, rows - 299, rows - 257, rows - 256, rows - 1]
+    for i, r in enumerate(at):
+        x[r] = i + 1
+    w = torch.ones(2, n, k, dtype=torch.float16, device=DEV)
+    w[1] = 2
+    out = torch.full((rows, n), 7.0, dtype=torch.float16, device=DEV)
+    hr.experts_product(x, w, out, offsets=on_device([0, rows - 299, rows]))
+    for i, r in enumerate(at):
+        assert (out[r] == (i + 1) * 8 * (2 if r >= rows - 299 else 1)).all()
+        out[r] = 0
+    for a in range(0, rows, 1 << 28):
+        assert not out[a:a + (1 << 28)].any()
