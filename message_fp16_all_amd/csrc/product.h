@@ -822,8 +822,8 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     constexpr uint32_t kScales = 3 * (PB + QB), kTable = kScales + (SCALED ? 4 * BQ * 4 : 0);
     constexpr int D0 = 6 + SCALED, D1 = 2;                                  // a wave's loads for the turns
     constexpr int STORES = kOut<O> == 4 ? FP * FH : FH * 2;                 // of a wave and turn, full tile
-    // (and the segments' first rows, and their tiles counted up)
-    __shared__ __align__(1024) char lds[kTable + (GRAD ? 0 : (2 * HR_EXPERTS_MAX + 1) * 4)];
+    // (and the segments' first rows, and their tiles counted up, or their order)
+    __shared__ __align__(1024) char lds[kTable + (2 * HR_EXPERTS_MAX + 1) * 4];
 
     const uint32_t lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -840,16 +840,31 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         asm volatile("" : "+s"(p));
         return p;
     };
+    for (int e = threadIdx.x; e <= a.experts; e += 512) {
+        const int at = a.offsets != nullptr ? a.offsets[e] : e == 0 ? 0 : static_cast<int>(a.rows);
+        const int rows = static_cast<int>(a.rows);
+        *reinterpret_cast<HR_LDS int *>(firsts + e * 4) = at < 0 ? 0 : at > rows ? rows : at;
+    }
+    __syncthreads();
     uint32_t tiles;
     if constexpr (GRAD) {
-        tiles = static_cast<uint32_t>(a.tiles_q) * a.tiles_p * a.experts;
-    } else {
-        for (int e = threadIdx.x; e <= a.experts; e += 512) {
-            const int at = a.offsets != nullptr ? a.offsets[e] : e == 0 ? 0 : static_cast<int>(a.rows);
-            const int rows = static_cast<int>(a.rows);
-            *reinterpret_cast<HR_LDS int *>(firsts + e * 4) = at < 0 ? 0 : at > rows ? rows : at;
+        // The longest segments first, so that a round's tiles are alike, and every second
+        // round the other way round (32 segments of 32768 rows, 1024 x 2048 199 -> 160
+        // us, 1024 x 1024 112 -> 101).
+        for (int e = threadIdx.x; e < a.experts; e += 512) {
+            const int rows = lds_read<int>(firsts + e * 4 + 4) - lds_read<int>(firsts + e * 4);
+            int longer = 0, lo = lds_read<int>(firsts);
+#pragma unroll 8
+            for (int i = 0; i < a.experts; ++i) {
+                const int hi = lds_read<int>(firsts + i * 4 + 4);
+                longer += hi - lo > rows || (hi - lo == rows && i < e);
+                lo = hi;
+            }
+            *reinterpret_cast<HR_LDS int *>(counts + longer * 4) = e;
         }
         __syncthreads();
+        tiles = static_cast<uint32_t>(a.tiles_q) * a.tiles_p * a.experts;
+    } else {
         if (wave == 0) {
             uint32_t before = 0;
             for (int e = lane; e - static_cast<int>(lane) < a.experts; e += kWave) {
@@ -870,14 +885,23 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         __syncthreads();
         tiles = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(counts + (a.experts - 1) * 4));
     }
-    // this die's run of tiles, which its workgroups take in rounds; their places in
-    // a round move on by one every second round, so that tiles of half the work
-    // (each second, third or fourth one of an expert) come to all of them (384 rows
-    // for each of 128 experts, 4096 -> 2048: 892 -> 822 us)
-    const uint32_t each = (tiles + 7) / 8, places = gridDim.x / 8, die = blockIdx.x % 8;
-    const uint32_t end = (die + 1) * each < tiles ? (die + 1) * each : tiles;
-    uint32_t round = 0, t = die * each + blockIdx.x / 8;
-    if (t >= end) return;
+    // Rounds of a tile for every workgroup, an eighth of it for each die: a run, which
+    // shares panels.  (With one run of all rounds' tiles for each die, one of them had
+    // 1.5 to 1.8 times the work of the gradient of 32 segments: 16384 rows padded to
+    // 128, 4096 x 4096, 772 -> 711 us; 65528 rows of 128 experts, 4096 -> 2048, 1138 ->
+    // 1108.)  The product's places in a round move on by one every second round, so that
+    // tiles of half the work (each second, third or fourth one of an expert) come to
+    // all workgroups (384 rows for each of 128 experts, 4096 -> 2048: 892 -> 822).
+    const uint32_t places = gridDim.x / 8, die = blockIdx.x % 8;
+    uint32_t round = 0, t;
+    const auto there = [&] {
+        const uint32_t left = tiles - round * gridDim.x;
+        const uint32_t run = left < gridDim.x ? (left + 7) / 8 : places;
+        const uint32_t at = (blockIdx.x / 8 + (GRAD ? 0 : round / 2)) % places, deal = die * run + at;
+        t = round * gridDim.x + (GRAD && round % 2 != 0 ? 8 * run - 1 - deal : deal);
+        return round * gridDim.x < tiles && at < run && t < tiles;
+    };
+    if (!there()) return;
 
     // the tile's place: its part of the operands, of out, and what is there of it
     const char *qs, *ps;
@@ -911,12 +935,11 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         uint32_t first, last;
         if constexpr (GRAD) {
             const uint32_t per = static_cast<uint32_t>(a.tiles_q) * a.tiles_p;
-            expert = static_cast<int>(t / per);
+            expert = __builtin_amdgcn_readfirstlane(lds_read<int>(counts + t / per * 4));
             in_bands(t % per, a.tiles_q, a.tiles_p, tq, tp);
-            uint32_t lo, hi;
-            segment(a.offsets, a.rows, expert, lo, hi);
-            first = __builtin_amdgcn_readfirstlane(lo);
-            last = __builtin_amdgcn_readfirstlane(hi);
+            const int lo = __builtin_amdgcn_readfirstlane(lds_read<int>(firsts + expert * 4));
+            const int hi = __builtin_amdgcn_readfirstlane(lds_read<int>(firsts + expert * 4 + 4));
+            first = lo, last = hi < lo ? lo : hi;
         } else {
             uint32_t upto;
             uint64_t past;
@@ -1154,8 +1177,7 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
         char *const to = out;
         const int rows = nq, width = np;
         ++round;
-        t = die * each + round * places + (blockIdx.x / 8 + round / 2) % places;
-        const bool more = t < end;
+        const bool more = there();
         if (more) {
             place();
             begin();

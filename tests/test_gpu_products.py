@@ -480,3 +480,27 @@ def test_most_rows():
         out[r] = 0
     for a in range(0, rows, 1 << 28):
         assert not out[a:a + (1 << 28)].any()
+
+
+@pytest.mark.parametrize("kind", ["equal", "ties", "few", "any"])
+def test_many_tiles_grad_in_any_order(kind):
+    """Segments of equal and of unlike lengths, most of none, and offsets that go down again: five rounds of tiles."""
+    m, dt, E, k, n, rows = Maker(len(kind)), torch.bfloat16, 300, 392, 512, 3000
+    if kind == "any":
+        offsets = torch.randint(-200, rows + 200, (E + 1,), generator=m.g).tolist()
+    else:
+        count = {"equal": torch.full((E,), 10), "ties": torch.arange(E) % 3 * 9, "few": torch.zeros(E, dtype=torch.int64)}[kind]
+        if kind == "few":
+            count[7], count[150], count[299] = 1000, 1500, 300
+        offsets = offsets_of(count.tolist())
+    dy, x = m.normal(rows, n, dtype=dt), m.normal(rows, k, dtype=dt)
+    dw = m.place(E * n, k, dt).view(E, n, k)
+    hr.experts_product_grad(dy.to(DEV), x.to(DEV), dw, offsets=on_device(offsets))
+    dy, x = dy.to(DEV).float(), x.to(DEV).float()
+    for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        a = min(max(a, 0), rows)
+        b = max(min(b, rows), a)
+        d, v = dy[a:b].double(), x[a:b].double()
+        ref, mag = (d.t() @ v).cpu(), (d.abs().t() @ v.abs()).cpu()
+        within(dw[e], ref, sum_tol(dt, ref, mag, b - a), f"dw of expert {e}")
+    m.check_frames()
