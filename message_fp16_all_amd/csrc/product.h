@@ -301,10 +301,24 @@ struct Tile {
 
 // Consecutive workgroups go to the 8 dies in turn; each die takes a run of
 // consecutive tiles, so that what its tiles share stays in its own cache.
+//
+// DEALT: runs of 16, and an eighth each of what is left, where tiles differ in time
+// or take longer than their panels: the gradient of 2151 rows of 8 segments, 1327 x
+// 1001, 39 -> 27 us, of 16384 of 32, 4097 x 4097, 1846 -> 1416, its product 1154 -> 1074;
+// but the product of 64 matrices that are read for 32 rows each 176 -> 228.
+template <bool DEALT>
 __device__ __forceinline__ bool on_die(uint32_t group, uint32_t tiles, uint32_t &tile) {
-    const uint32_t each = (tiles + 7) / 8, i = group / 8;
-    tile = (group % 8) * each + i;
-    return i < each && tile < tiles;
+    const uint32_t i = group / 8;
+    uint32_t before = 0, run = (tiles + 7) / 8, at = i;
+    if constexpr (DEALT) {
+        constexpr uint32_t RUN = 16;
+        before = i / RUN * (8 * RUN);
+        if (before >= tiles) return false;
+        run = tiles - before < 8 * RUN ? (tiles - before + 7) / 8 : RUN;
+        at = i % RUN;
+    }
+    tile = before + group % 8 * run + at;
+    return at < run && tile < tiles;
 }
 
 // Tile number t of nq x np: bands of 4 q, so that 32 running tiles are 4 x 8.
@@ -317,7 +331,7 @@ __device__ __forceinline__ void in_bands(uint32_t t, uint32_t nq, uint32_t np, i
 
 // Which tile of the product this workgroup computes: the segments' tiles one
 // after the other, counted by every wave for itself, 64 experts at a time.
-template <int BQ>
+template <int BQ, bool ANY>
 __device__ __forceinline__ Tile product_tile(const ProductArgs &a, uint32_t group) {
     Tile t{};
     const int lane = threadIdx.x % kWave;
@@ -329,7 +343,7 @@ __device__ __forceinline__ Tile product_tile(const ProductArgs &a, uint32_t grou
     }
     const uint32_t tiles = reduce_lanes<64>(mine, [](uint32_t x, uint32_t y) { return x + y; }) * a.tiles_p;
     uint32_t tile;
-    t.there = on_die(__builtin_amdgcn_readfirstlane(group), __builtin_amdgcn_readfirstlane(tiles), tile);
+    t.there = on_die<ANY>(__builtin_amdgcn_readfirstlane(group), __builtin_amdgcn_readfirstlane(tiles), tile);
     if (!t.there) return t;
     for (int e0 = 0; e0 < a.experts; e0 += kWave) {
         uint32_t lo = 0, hi = 0;
@@ -361,7 +375,7 @@ __device__ __forceinline__ Tile gradient_tile(const ProductArgs &a, uint32_t gro
     Tile t{};
     const uint32_t each = static_cast<uint32_t>(a.tiles_q) * a.tiles_p;
     uint32_t tile;
-    t.there = on_die(group, each * a.experts, tile);
+    t.there = on_die<true>(group, each * a.experts, tile);
     if (!t.there) return t;
     t.expert = static_cast<int>(tile / each);
     in_bands(tile % each, a.tiles_q, a.tiles_p, t.q, t.p);
@@ -503,7 +517,7 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
     constexpr int kJoin = SH::WK > 1 ? (SH::WK - 1) * FQ * FP * 1024 * kWaves : 0;
     __shared__ __align__(1024) char lds[S * kStageBytes > kJoin ? S * kStageBytes : kJoin];
 
-    const Tile tile = GRAD ? gradient_tile(a, blockIdx.x) : product_tile<BQ>(a, blockIdx.x);
+    const Tile tile = GRAD ? gradient_tile(a, blockIdx.x) : product_tile<BQ, ANY>(a, blockIdx.x);
     if (!tile.there) return;
     const uint32_t lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
