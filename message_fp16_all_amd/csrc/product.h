@@ -822,9 +822,10 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
 // 8192 x 8192 x 8192: bfloat16 730-760 us (1.45-1.51 PF), transposed 753, gradient
 // 760-787; e4m3 465-488 (2.3 PF).  Without any loads these are 640 and 411, with
 // zeros for data e4m3 takes 400 with loads: the rest is power.  Instructions of 32 x 32
-// x 16 instead of 16 x 16 x 32: 812 against 760.  Segments of 512 rows
-// of 128 matrices (4096 -> 2048) 886: their panels come from HBM, 20 of them for 32
-// tiles on a die where one large matrix needs 12.
+// x 16 instead of 16 x 16 x 32: 812 against 760.  The next tile's loads and the sets'
+// turns without a break between tiles: 787 against 762.  Segments of 512 rows of 128
+// matrices (4096 -> 2048) 886: their panels come from HBM, 20 of them for 32 tiles
+// on a die where one large matrix needs 12.
 template <class E, class O, bool QA, bool PA, bool GRAD>
 __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     constexpr int SIZE = kBytes<E>, BQ = 256, BP = 256, H = 128, FP = 4, FH = 4;
