@@ -6,7 +6,8 @@ which shows y to 24 bits.
 Bound, in units of 2^-23 of the value.  z = e^-gate: the exponential's 1, what
 correcting its exponent rounds off 1/2 (the correction's own error is below
 2^-30); 1 + z 1/2; the reciprocal 1; two products 1/2 each; the scale's quotient
-1/2: 4.5 in all.
+1/2: 4.5 in all.  (Of a gate of 87 or more in magnitude: no sum and a reciprocal
+of 1; one product more: 4.)
 """
 import pytest
 import torch
@@ -54,6 +55,13 @@ def test_every_near_gate_of_float16(low, high, sign):
 def test_near_gates_of_bfloat16(sign):
     bits = torch.arange(0x3800, 0x42AE, dtype=torch.int16)
     check(bits.view(torch.bfloat16) * sign, 2.0 ** 40)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_far_gates_of_bfloat16(sign):
+    """From 87 up to 128."""
+    bits = torch.arange(0x42AE, 0x4301, dtype=torch.int16)
+    check(bits.view(torch.bfloat16) * sign, 2.0 ** 100)
 
 
 def test_near_gates_beside_far_ones():
