@@ -234,7 +234,6 @@ hr_status run_product_grad(ProductArgs &a, hr_stream_t stream) {
     a.tiles_q = (a.nq + SH::BQ - 1) / SH::BQ;
     a.tiles_p = (a.np + SH::BP - 1) / SH::BP;
     const size_t each = static_cast<size_t>(a.tiles_q) * a.tiles_p;
-    if (each >= (size_t(1) << 32) / HR_EXPERTS_MAX) return HR_ERR_TOO_LARGE;
     return launch_tiles(product_tiles<E, O, SH, true, true, true, ANY>, each * a.experts, SH::kThreads, stream, a);
 }
 

@@ -504,3 +504,19 @@ def test_many_tiles_grad_in_any_order(kind):
         ref, mag = (d.t() @ v).cpu(), (d.abs().t() @ v.abs()).cpu()
         within(dw[e], ref, sum_tol(dt, ref, mag, b - a), f"dw of expert {e}")
     m.check_frames()
+
+
+def test_gradient_of_a_very_large_matrix():
+    """One row's outer product with more than 2^22 tiles and 2^36 values (137 GB)."""
+    n = k = (1 << 18) + 1
+    m = Maker(4)
+    dy, x = m.normal(1, n, dtype=torch.bfloat16).to(DEV), m.normal(1, k, dtype=torch.bfloat16).to(DEV)
+    torch.cuda.empty_cache()
+    dw = torch.full((n, k), 7.0, dtype=torch.bfloat16, device=DEV)
+    hr.experts_product_grad(dy, x, dw)
+    for a in range(0, n, 1 << 13):
+        d = dy[0, a:a + (1 << 13), None].float()
+        # (one product, exact in binary32, rounded once)
+        assert torch.equal(dw[a:a + (1 << 13)], (d * x.float()).to(torch.bfloat16)), f"rows {a} .."
+    del dw
+    torch.cuda.empty_cache()

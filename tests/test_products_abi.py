@@ -109,6 +109,18 @@ def test_grad_refusals(over, status):
     assert grad(**over) == status
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where no kernel can start")
+def test_largest_gradient():
+    """Up to 2^32 work-items: of 128 x 128 values 2^24 tiles for all matrices together."""
+    one = dict(rows=1, experts=1, offsets=None)
+    odd = dict(k=(1 << 18) + 1)
+    assert grad(**one, n=(1 << 17) + 1, **odd) == hr.HR_ERR_HIP
+    assert grad(**one, n=(1 << 18) + 1, **odd) == hr.HR_ERR_HIP          # 2^22 tiles and more
+    assert grad(**one, n=8187 * 128, **odd) == hr.HR_ERR_HIP
+    assert grad(**one, n=8187 * 128 + 1, **odd) == LARGE
+    assert grad(rows=1, offsets=BASE - STEP, n=(1 << 18) + 1, **odd) == LARGE      # eight of them
+
+
 def act(**over):
     a = hr.hr_experts_act_args()
     a.x, a.out, a.codes, a.scales, a.offsets = (at(i) for i in range(5))
