@@ -88,18 +88,21 @@ __device__ __forceinline__ i32x4 buffer_of(const char *base, bool here = true) {
 // 16 (or 4) bytes a lane from HBM to LDS at `to` + 16 (4) * lane.  Written out
 // because the compiler, seeing the builtin, waits for every load in flight
 // before any LDS read; nothing here lands in registers.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"     // (m0 is reserved: the compiler writes it again before its own uses)
 __device__ __forceinline__ void dma16(i32x4 from, uint32_t offset, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(to), "v"(offset), "s"(from)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(i32x4 from, uint32_t offset, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(to), "v"(offset), "s"(from)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // All but the last N loads have landed, and this wave's LDS reads are done.
 template <int N>
