@@ -925,8 +925,13 @@ typedef struct {
  * one's leading bit; everything beyond that in binary32.  Without offsets it is
  * a dense layer's product.
  *
- * The order of every sum depends on the sizes alone: equal inputs give equal
- * outputs.  A row's NaN and infinities stay in its row.
+ * The order of a sum depends on the call's sizes and layout, and on whether x and
+ * w, their strides and rows are whole units of 16 bytes (then one kernel reads
+ * them, else another); not on offsets, other addresses or what else runs.  Equal
+ * calls of equal inputs give equal bits; calls that differ in such a unit alone
+ * may differ by the roundings of another order.  The scales of a group are
+ * multiplied with each other first, in binary32.  A row's NaN and infinities stay
+ * in its row.
  * Errors: HR_ERR_INVALID_ARG (n, k or experts 0, offsets NULL with several
  * experts, null pointers, scales missing or not wanted, a stride below the row,
  * overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (n or k above
@@ -956,9 +961,10 @@ typedef struct {
  *
  *     dw[e][j][i] = sum over e's rows r of dy[r][j] * x[r][i]
  *
- * summed in binary32 in the rows' order, rounded once; zeros for an expert
- * without rows.  Rows of no segment are not used.  (Matrices kept transposed:
- * dy and x exchanged, and n and k.)
+ * summed in binary32 and rounded once; zeros for an expert without rows.  The
+ * order of the rows in a sum (not always one after the other) is fixed as the
+ * product's is, by dy and x.  Rows of no segment are not used.  (Matrices kept
+ * transposed: dy and x exchanged, and n and k.)
  * Errors: as hr_experts_product.
  */
 HR_API hr_status hr_experts_product_grad_f16(const hr_experts_product_grad_args *args, hr_stream_t stream);
