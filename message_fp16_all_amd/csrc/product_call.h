@@ -6,8 +6,10 @@
 
 namespace hr {
 
-// Rows of at most 4 MiB apart: a tile's 256 stay inside a buffer's 2 GiB.
+// Rows of at most 4 MiB apart: a tile's 256 stay inside a buffer's 2 GiB.  (One
+// row has no other to be apart from.)
 constexpr size_t kMaxProductStride = size_t(1) << 22;
+inline bool too_far_apart(size_t rows, size_t bytes) { return rows > 1 && bytes > kMaxProductStride; }
 // A row number and some stages' rows behind it stay below 2^31.
 constexpr size_t kMaxProductRows = (size_t(1) << 31) - 4096;
 
@@ -56,8 +58,8 @@ hr_status product_check(const hr_experts_product_args *q, ProductArgs &a, bool &
     if (SIZE == 1 && (!row_stride(q->rows, kb, &ss, 4) ||
                       !matrices(q->w_scales, q->experts, rb, cb, q->w_scales_stride, q->w_scales_expert_stride, 4, &ws)))
         return HR_ERR_INVALID_ARG;
-    if (xs * SIZE > kMaxProductStride || w.stride * SIZE > kMaxProductStride || os * 2 > kMaxProductStride ||
-        ss * 4 > kMaxProductStride)
+    if (too_far_apart(q->rows, xs * SIZE) || too_far_apart(wr, w.stride * SIZE) || too_far_apart(q->rows, os * 2) ||
+        (SIZE == 1 && too_far_apart(q->rows, ss * 4)))
         return HR_ERR_TOO_LARGE;
     if (q->rows == 0) return HR_OK;
     if (q->x == nullptr || q->w == nullptr || q->out == nullptr) return HR_ERR_INVALID_ARG;
@@ -107,7 +109,7 @@ inline hr_status product_grad_check(const hr_experts_product_grad_args *q, Produ
     if (!row_stride(q->rows, q->n, &ys, 2) || !row_stride(q->rows, q->k, &xs, 2) ||
         !matrices(q->dw, q->experts, q->n, q->k, q->dw_stride, q->dw_expert_stride, ob, &w))
         return HR_ERR_INVALID_ARG;
-    if (ys * 2 > kMaxProductStride || xs * 2 > kMaxProductStride || w.stride * ob > kMaxProductStride)
+    if (too_far_apart(q->rows, ys * 2) || too_far_apart(q->rows, xs * 2) || too_far_apart(q->n, w.stride * ob))
         return HR_ERR_TOO_LARGE;
     if (q->dw == nullptr || (q->rows > 0 && (q->dy == nullptr || q->x == nullptr))) return HR_ERR_INVALID_ARG;
     if (!aligned(q->dy, 2) || !aligned(q->x, 2) || !aligned(q->dw, ob) || !aligned(q->offsets, 4))

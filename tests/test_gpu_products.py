@@ -520,3 +520,28 @@ def test_gradient_of_a_very_large_matrix():
         assert torch.equal(dw[a:a + (1 << 13)], (d * x.float()).to(torch.bfloat16)), f"rows {a} .."
     del dw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("k,n", [(136, 272), (135, 271), (1, 272), (136, 1), (1, 1)])
+def test_one_row_with_a_large_distance(k, n, transposed):
+    """Through the C entry: the distance of rows that are one row is not used."""
+    m, dt, far = Maker(k + n), torch.float16, (1 << 32) + 8
+    wr, wc = (k, n) if transposed else (n, k)
+    x, w, dy = m.normal(1, k, dtype=dt), m.normal(1, wr, wc, dtype=dt), m.normal(1, n, dtype=dt)
+    xd, wd, yd, out = x.to(DEV), w.to(DEV), dy.to(DEV), m.place(1, n, dt)
+    a = hr.hr_experts_product_args()
+    a.x, a.w, a.out, a.rows, a.n, a.k, a.experts = xd.data_ptr(), wd.data_ptr(), out.data_ptr(), 1, n, k, 1
+    a.x_stride, a.out_stride, a.w_stride, a.transposed = far, far, far if wr == 1 else 0, int(transposed)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert hr.hr_experts_product_f16(a, stream) == hr.HR_OK
+    ref, mag = product_ref(x, w, [0, 1], transposed)
+    within(out, ref, sum_tol(dt, ref, mag, k), "out")
+    dw = m.place(n, k, dt)
+    g = hr.hr_experts_product_grad_args()
+    g.dy, g.x, g.dw, g.rows, g.n, g.k, g.experts = yd.data_ptr(), xd.data_ptr(), dw.data_ptr(), 1, n, k, 1
+    g.dy_stride, g.x_stride, g.dw_stride = far, far, far if n == 1 else 0
+    assert hr.hr_experts_product_grad_f16(g, stream) == hr.HR_OK
+    ref, mag = grad_ref(dy, x, [0, 1])
+    within(dw, ref[0], sum_tol(dt, ref, mag, 1)[0], "dw")
+    m.check_frames()

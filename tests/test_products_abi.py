@@ -79,6 +79,23 @@ def test_most_rows(eight):
     assert grad(rows=(1 << 31) - 4096, dw=at(2) + 1) == ALIGN
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_one_row_is_not_apart_from_another(eight):
+    """The distance of a row that no second one follows is not limited."""
+    far, late = 1 << 30, dict(out=at(2) + 1)                     # (refused by what is looked at next)
+    one = dict(rows=1, x_stride=far, out_stride=far, **(dict(x_scales_stride=far) if eight else {}))
+    assert product(eight, **one, **late) == ALIGN
+    assert product(eight, n=1, w_stride=far, **late) == ALIGN
+    assert product(eight, k=1, transposed=1, w_stride=far, n=384, **late) == ALIGN
+    assert product(eight, **{**one, "rows": 2}, **late) == LARGE
+    assert product(eight, n=2, w_stride=far, **late) == LARGE
+    assert product(eight, x_stride=far, rows=0) == hr.HR_OK
+    late = dict(dw=at(2) + 1)
+    assert grad(rows=1, dy_stride=far, x_stride=far, **late) == ALIGN
+    assert grad(n=1, dw_stride=far, **late) == ALIGN
+    assert grad(n=2, dw_stride=far, **late) == LARGE
+
+
 def test_matrices_in_pieces():
     """The bytes between matrices that are apart are not theirs."""
     gap = dict(n=64, k=64, w_expert_stride=1 << 20)
