@@ -999,9 +999,10 @@ typedef struct {
  * gives NaN, as the formula does.
  * Errors: HR_ERR_INVALID_ARG (width 0, group, codes without scales or scales
  * without codes, nothing to write, offsets with experts below 1, null pointers, a
- * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (2^31 rows
- * or more, width above HR_EXPERTS_PRODUCT_MAX, a launch of 2^32 work-items or
- * more: 2^24 rows of more than 512 values, 2^28 of up to 128), HR_ERR_HIP.
+ * stride below the row, overlap), HR_ERR_ALIGNMENT, HR_ERR_TOO_LARGE (width above
+ * HR_EXPERTS_PRODUCT_MAX; 2^31 rows or more; a launch of 2^32 work-items or more:
+ * above 2^25 - 2 rows of more than 512 values, 2^27 - 8 of more than 128, 2^29 - 32
+ * of fewer), HR_ERR_HIP.
  */
 HR_API hr_status hr_experts_act_f16(const hr_experts_act_args *args, hr_stream_t stream);
 HR_API hr_status hr_experts_act_bf16(const hr_experts_act_args *args, hr_stream_t stream);

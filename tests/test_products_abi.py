@@ -181,6 +181,20 @@ def test_act_grad_refusals(over, status):
     assert act_grad(**over) == status
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where no kernel can start")
+@pytest.mark.parametrize("width,most", [(513, (1 << 25) - 2), (1 << 20, (1 << 25) - 2), (512, (1 << 27) - 8),
+                                        (129, (1 << 27) - 8), (128, (1 << 29) - 32), (1, (1 << 29) - 32)])
+def test_most_rows_of_the_activation(width, most):
+    """A launch has fewer than 2^32 work-items: the rows that the header names."""
+    far = [(i + 1) << 56 for i in range(4)]                      # (the buffers take up to 2^47 bytes)
+    forward = dict(width=width, x=far[0], out=far[1], codes=None, scales=None, offsets=None, experts=0)
+    back = dict(width=width, dy=far[0], x=far[1], dx=far[2], out=far[3], offsets=None, experts=0)
+    for rows, status in ((most, hr.HR_ERR_HIP), (most + 1, LARGE), ((1 << 31) - 1, LARGE)):
+        assert act(rows=rows, **forward) == status
+        assert act(rows=rows, gated=0, **forward) == status
+        assert act_grad(rows=rows, **back) == status
+
+
 # ---------------------------------------------------------------- the binding
 
 @pytest.mark.parametrize("dt,end", [(torch.float16, "f16"), (torch.bfloat16, "bf16")])
