@@ -3,6 +3,7 @@
 #pragma once
 
 #include "product.h"
+#include "product_shape.h"
 
 namespace hr {
 
@@ -157,13 +158,6 @@ hr_status launch_large(K kernel, size_t tiles, hr_stream_t stream, const Product
     return launch_tiles(kernel, tiles < most ? tiles : most, 512, stream, a);
 }
 
-// Tiles that segments of so many rows in all take at most.
-inline size_t tiles_of(size_t rows, int experts, size_t high) {
-    const size_t used = static_cast<size_t>(experts) < rows ? experts : rows;
-    const size_t most = rows / high + used;
-    return most < rows ? most : rows;
-}
-
 // The shapes, from the largest: tile, waves over q, p and the panels of a stage,
 // stages.  Where weights are read for few rows all but the smallest come near to
 // HBM's rate, and what counts is that the GPU is full.
@@ -184,46 +178,27 @@ hr_status run_product(ProductArgs &a, hr_stream_t stream) {
                         SH::kThreads, stream, a);
 }
 
-// The largest shape whose height fits the segments and whose tiles fill the GPU.
-// (The rows are the buffer's: with padded segments more than there are.)  us by
-// shape, the chosen one first.
-// 4096 x 4096, bfloat16, one matrix: 16 rows Tiny 7.2 Few 8.0; 64 Few 12.2 Low
-// 21.4; 256 Low 22.9 Some 32.1 Few 39; 512 Some 33.8 Low 43 Middle 43; 1024 Some
-// 42.8 Middle 47 Half 60; 2048 Middle 63.9 Half 66.0 large 78; 4096 large 98
-// Middle 133 Half 138.
-// 64 matrices of 2048 x 4096, rows per matrix on average 8: Few 157 Some 162; 16: Low
-// 179 Middle 170 Few 196; 32: Some 192 Middle 175 Few 272; 47 with padding: Middle
-// 176 Half 183 Some 192; 64: Half 224 large 210 Middle 236; 128: Half 268 large 293;
-// 256: large 372 Half 391.  e4m3: 8: Few 86 Some 105; 16: Low 115 Some 114 Middle
-// 125; 32: Some 121 Middle 125; 47: Middle 126 Some 119; 64: Half 144 Some 136; 128:
-// Half 173 large 206; 256: large 255 Half 266.
-// 64 matrices of 2560 x 5120 and padding to 16 rows, 512 rows in 1472: Some 264 Low 254
-// Middle 299 Few 279; 1024 in 1984: Some 283 Low 285 Middle 310.
-// Transposed 2 rows: FewAcross 10.3 Low 21; e4m3 512 rows of 64: Low 93 FewAcross 123.
 template <class E, class O, bool PA>
 hr_status pick_product(ProductArgs &a, bool any, hr_stream_t stream) {
-    const size_t each = a.rows / a.experts;
-    const auto fits = [&](size_t bq, size_t bp, size_t least_rows, size_t least_tiles) {
-        return each >= least_rows && tiles_of(a.rows, a.experts, bq) * ((a.np + bp - 1) / bp) >= least_tiles;
-    };
-    if (any)
-        return fits(128, 128, 24, 128) ? run_product<E, O, Middle, PA, true>(a, stream)
-                                       : run_product<E, O, AnyFew, PA, true>(a, stream);
-    if (fits(256, 256, 192, 200)) {
-        a.tiles_p = (a.np + 255) / 256;
-        return launch_large(product_large<E, O, false, PA, false>, tiles_of(a.rows, a.experts, 256) * a.tiles_p, stream, a);
+    const ProductShape shape = product_shape(a.rows, a.experts, a.np, PA, any);
+    switch (shape) {
+        case ProductShape::Large:
+            a.tiles_p = (a.np + 255) / 256;
+            return launch_large(product_large<E, O, false, PA, false>, tiles_of(a.rows, a.experts, 256) * a.tiles_p, stream, a);
+        case ProductShape::Half: return run_product<E, O, Half, PA, false>(a, stream);
+        case ProductShape::Middle: return run_product<E, O, Middle, PA, false>(a, stream);
+        case ProductShape::Some: return run_product<E, O, Some, PA, false>(a, stream);
+        case ProductShape::Low: return run_product<E, O, Low, PA, false>(a, stream);
+        case ProductShape::AnyMiddle: return run_product<E, O, Middle, PA, true>(a, stream);
+        case ProductShape::AnyFew: return run_product<E, O, AnyFew, PA, true>(a, stream);
+        default: break;                 // the lowest: of one layout each
     }
-    if (fits(128, 256, 64, 320)) return run_product<E, O, Half, PA, false>(a, stream);
-    if (fits(128, 128, 40, 320)) return run_product<E, O, Middle, PA, false>(a, stream);
-    if (fits(64, 128, 20, 200)) return run_product<E, O, Some, PA, false>(a, stream);
-    if (fits(32, 128, 12, 128)) return run_product<E, O, Low, PA, false>(a, stream);
-    if constexpr (PA) {
-        if (fits(32, 128, 0, 256)) return run_product<E, O, Low, PA, false>(a, stream);
+    if constexpr (PA)
         return run_product<E, O, FewAcross, PA, false>(a, stream);
-    } else {
-        if (fits(16, 32, 0, 192)) return run_product<E, O, Few, PA, false>(a, stream);
+    else if (shape == ProductShape::Few)
+        return run_product<E, O, Few, PA, false>(a, stream);
+    else
         return run_product<E, O, Tiny, PA, false>(a, stream);
-    }
 }
 
 template <class E, class O>
@@ -241,19 +216,18 @@ hr_status run_product_grad(ProductArgs &a, hr_stream_t stream) {
 
 template <class E, class O>
 hr_status launch_product_grad(ProductArgs &a, bool any, hr_stream_t stream) {
-    if (any) return run_product_grad<E, O, Middle, true>(a, stream);
-    const auto tiles = [&](int b) { return static_cast<size_t>((a.nq + b - 1) / b) * ((a.np + b - 1) / b) * a.experts; };
-    // (segments differ in length: one round of large tiles is as long as the longest.  32
-    // matrices of 1024 x 512 over 32768 rows, 256 large tiles 77 us, 1024 of Middle 56;
-    // 1024 x 1024 93 and 101; one matrix has no such difference)
-    if (a.nq >= 192 && a.np >= 192 && tiles(256) >= (a.experts > 1 ? 400u : 200u)) {
-        a.tiles_q = (a.nq + 255) / 256;
-        a.tiles_p = (a.np + 255) / 256;
-        if (tiles(256) >= size_t(1) << 31) return HR_ERR_TOO_LARGE;
-        return launch_large(product_large<E, O, true, true, true>, tiles(256), stream, a);
+    switch (gradient_shape(a.experts, a.nq, a.np, any)) {
+        case GradientShape::Large: {
+            a.tiles_q = (a.nq + 255) / 256;
+            a.tiles_p = (a.np + 255) / 256;
+            const size_t tiles = static_cast<size_t>(a.tiles_q) * a.tiles_p * a.experts;
+            if (tiles >= size_t(1) << 31) return HR_ERR_TOO_LARGE;
+            return launch_large(product_large<E, O, true, true, true>, tiles, stream, a);
+        }
+        case GradientShape::Middle: return run_product_grad<E, O, Middle, false>(a, stream);
+        case GradientShape::AnyMiddle: return run_product_grad<E, O, Middle, true>(a, stream);
+        default: return run_product_grad<E, O, Deep, false>(a, stream);
     }
-    if (tiles(128) >= 320) return run_product_grad<E, O, Middle, false>(a, stream);
-    return run_product_grad<E, O, Deep, false>(a, stream);
 }
 
 }  // namespace hr
