@@ -7,7 +7,7 @@
 //   dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s
 //
 // Bound by HBM: every value is read once and written once.  65528 x 2048 to bfloat16 125
-// us (6.4 TB/s), its gradient 209 (6.4); to e4m3 126 (5.3), where the instructions of
+// us (6.4 TB/s), its gradient 209 (6.4); to e4m3 113-118 (5.7-6.0), where the instructions of
 // the sigmoid, the maximum and the exact quotient take most of the time.
 #include <type_traits>
 

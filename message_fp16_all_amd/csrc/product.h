@@ -307,7 +307,7 @@ struct Tile {
 //
 // DEALT: runs of 16, and an eighth each of what is left, where tiles differ in time
 // or take longer than their panels: the gradient of 2151 rows of 8 segments, 1327 x
-// 1001, 39 -> 27 us, of 16384 of 32, 4097 x 4097, 1846 -> 1416, its product 1154 -> 1074;
+// 1001, 39 -> 27 us, of 16384 of 32, 4097 x 4097, 1846 -> 1416, its product 1154 -> 1073;
 // but the product of 64 matrices that are read for 32 rows each 176 -> 228.
 template <bool DEALT>
 __device__ __forceinline__ bool on_die(uint32_t group, uint32_t tiles, uint32_t &tile) {
@@ -822,13 +822,14 @@ __global__ __launch_bounds__(SH::kThreads, SH::kMinWaves) void product_tiles(Pro
 // tile's first loads go out before this one's sums are stored, and the stores
 // are waited for a stage later (loads and stores complete in order).
 //
-// 8192 x 8192 x 8192: bfloat16 730-760 us (1.45-1.51 PF), transposed 753, gradient
-// 760-787; e4m3 465-488 (2.3 PF).  Without any loads these are 640 and 411, with
-// zeros for data e4m3 takes 400 with loads: the rest is power.  Instructions of 32 x 32
-// x 16 instead of 16 x 16 x 32: 812 against 760.  The next tile's loads and the sets'
-// turns without a break between tiles: 787 against 762.  Segments of 512 rows of 128
-// matrices (4096 -> 2048) 886: their panels come from HBM, 20 of them for 32 tiles
-// on a die where one large matrix needs 12.
+// 8192 x 8192 x 8192, normally distributed values: bfloat16 730-760 us (1.45-1.51 PF),
+// transposed 753, gradient 760-787; e4m3 465-488 (2.3 PF; 500-540 where every 97th
+// value is 8 times as large).  Without any loads bfloat16 and e4m3 take 640 and 411,
+// with zeros for data e4m3 takes 400 with loads: the rest is power.  Instructions of 32
+// x 32 x 16 instead of 16 x 16 x 32: 812 against 760.  The next tile's loads and the
+// sets' turns without a break between tiles: 787 against 762.  Segments of 512 rows of
+// 128 matrices (4096 -> 2048) 895: a die's 32 tiles have 20 panels there, of one large
+// matrix 12.
 template <class E, class O, bool QA, bool PA, bool GRAD>
 __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     constexpr int SIZE = kBytes<E>, BQ = 256, BP = 256, H = 128, FP = 4, FH = 4;
@@ -906,10 +907,10 @@ __global__ __launch_bounds__(512, 2) void product_large(ProductArgs a) {
     // Rounds of a tile for every workgroup, an eighth of it for each die: a run, which
     // shares panels.  (With one run of all rounds' tiles for each die, one of them had
     // 1.5 to 1.8 times the work of the gradient of 32 segments: 16384 rows padded to
-    // 128, 4096 x 4096, 772 -> 711 us; 65528 rows of 128 experts, 4096 -> 2048, 1138 ->
-    // 1108.)  The product's places in a round move on by one every second round, so that
+    // 128, 4096 x 4096, 772 -> 711 us, 696 with the longest first; 65528 rows of 128
+    // experts, 4096 -> 2048, 1138 -> 1108.)  The product's places in a round move on by one every second round, so that
     // tiles of half the work (each second, third or fourth one of an expert) come to
-    // all workgroups (384 rows for each of 128 experts, 4096 -> 2048: 892 -> 822).
+    // all workgroups (384 rows for each of 128 experts, 4096 -> 2048: 892 -> 822, now 791).
     const uint32_t places = gridDim.x / 8, die = blockIdx.x % 8;
     uint32_t round = 0, t;
     const auto there = [&] {
